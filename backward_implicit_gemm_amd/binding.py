@@ -23,7 +23,13 @@ EXPORTED = (
     "gc_conv_bwd_weight", "gc_status_string", "gc_fastdiv_selfcheck", "gc_version",
     "gc_set_kernel_policy", "gc_conv_fwd_bias", "gc_conv_bwd_bias", "gc_conv_bwd",
     "gc_conv_plan_name", "gc_conv_fwd_noalloc", "gc_conv_bwd_weight_bias",
+    "gc_embed_fwd", "gc_embed_bwd", "gc_embed_workspace_bytes", "gc_group_norm_fwd",
+    "gc_group_norm_bwd", "gc_group_norm_workspace_bytes", "gc_grad_norm", "gc_grad_clip",
+    "gc_grad_clip_workspace_bytes",
 )
+GC_I32, GC_I64, GC_U8 = 0, 1, 2
+GC_NCHW, GC_NHWC = 0, 1
+GC_ACT_NONE, GC_ACT_RELU, GC_ACT_SILU, GC_ACT_GELU = range(4)
 GC_POLICY_AUTO, GC_POLICY_GENERIC = 0, 1
 
 
@@ -35,6 +41,22 @@ class GcError(RuntimeError):
 
 class gc_conv_desc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("B", "IC", "H", "W", "OC", "KH", "KW", "stride")]
+
+
+class gc_embed_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("tokens", ctypes.c_int), ("V", ctypes.c_int),
+                ("D", ctypes.c_int), ("itype", ctypes.c_int), ("ld", ctypes.c_int64),
+                ("ld_tok", ctypes.c_int64)]
+
+
+class gc_norm_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "C", "H", "W", "groups", "layout", "act")] + \
+               [("eps", ctypes.c_float)]
+
+
+class gc_tensor(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int)]
 
 
 _lib = None
@@ -80,6 +102,26 @@ def lib():
     L.gc_version.restype = i
     L.gc_set_kernel_policy.argtypes = [i]
     L.gc_set_kernel_policy.restype = i
+    f, ep, np_ = ctypes.c_float, ctypes.POINTER(gc_embed_desc), ctypes.POINTER(gc_norm_desc)
+    L.gc_embed_fwd.argtypes = [vp, vp, vp, ep, f, i, vp]
+    L.gc_embed_fwd.restype = i
+    L.gc_embed_workspace_bytes.argtypes = [ep, i]
+    L.gc_embed_workspace_bytes.restype = sz
+    L.gc_embed_bwd.argtypes = [vp, vp, vp, vp, sz, ep, f, i, vp]
+    L.gc_embed_bwd.restype = i
+    L.gc_group_norm_workspace_bytes.argtypes = [i, np_, i]
+    L.gc_group_norm_workspace_bytes.restype = sz
+    L.gc_group_norm_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, np_, i, i, vp]
+    L.gc_group_norm_fwd.restype = i
+    L.gc_group_norm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, np_, i, i, vp]
+    L.gc_group_norm_bwd.restype = i
+    L.gc_grad_clip_workspace_bytes.argtypes = [i]
+    L.gc_grad_clip_workspace_bytes.restype = sz
+    tp = ctypes.POINTER(gc_tensor)
+    L.gc_grad_norm.argtypes = [tp, i, f, vp, vp, sz, vp]
+    L.gc_grad_norm.restype = i
+    L.gc_grad_clip.argtypes = [tp, i, f, f, f, vp, vp, sz, vp]
+    L.gc_grad_clip.restype = i
     _lib = L
     return L
 
@@ -349,3 +391,246 @@ class Conv:
     def bwd_bias(self, dy, y, db, stream=None):
         return gc_conv_bwd_bias(dy, y if self.relu else None, db, self.relu, self.x_shape,
                                 self.w_shape, self.stride, self.ws[GC_OP_BWD_BIAS], stream)
+
+
+# ---------------------------------------------------------------------------
+# The operators around the convolutions
+# ---------------------------------------------------------------------------
+_ACTS = {"none": GC_ACT_NONE, "relu": GC_ACT_RELU, "silu": GC_ACT_SILU, "gelu": GC_ACT_GELU}
+_LAYOUTS = {"nchw": (GC_NCHW, torch.contiguous_format), "nhwc": (GC_NHWC, torch.channels_last)}
+_DTYPES = {torch.float32: GC_F32, torch.bfloat16: GC_BF16}
+_INDEX_TYPES = {torch.int32: GC_I32, torch.int64: GC_I64, torch.uint8: GC_U8}
+
+
+def _code(dtype):
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}; expected float32 or bfloat16")
+    return _DTYPES[dtype]
+
+
+def _named(table, value, what):
+    if value not in table:
+        raise ValueError(f"unknown {what} {value!r}; expected one of {', '.join(table)}")
+    return table[value]
+
+
+def _arg(t, name, dtype, shape, device, fmt=torch.contiguous_format):
+    """Address of tensor t after checking its shape, dtype, layout and device,
+    in this order."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if not t.is_contiguous(memory_format=fmt):
+        raise ValueError(f"{name} must be dense in {fmt}")
+    return _on(t, name, device)
+
+
+def _on(t, name, device):
+    """Address of tensor t, which has to be on this device."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's workspace is on {device}")
+    return t.data_ptr()
+
+
+def _device(device):
+    """The device with its index, where there is one (a helper may be made
+    without a GPU; its calls then refuse their tensors)."""
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None and torch.cuda.is_available():
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
+def _raw_stream(stream, device):
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _scratch(n, device):
+    """(address, bytes, tensor) of a workspace of n bytes."""
+    t = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+    return (t.data_ptr() if n else None), n, t
+
+
+class Embedding:
+    """Embedding lookup with scaling and its gradient (gc_embed_fwd and
+    gc_embed_bwd) for tokens of shape (rows, tokens) and a table of shape
+    (vocab, dim).
+
+    Tokens are int32, int64 or uint8; a token outside [0, vocab) is empty: zeros
+    out, no gradient.  ``out`` and ``dout`` have shape (rows, tokens, dim); the
+    rows, and those of the tokens, may lie further apart than they are long
+    (a part of a wider feature row).  Calls of one helper share its workspace
+    and must not overlap in time."""
+
+    def __init__(self, rows, tokens, vocab, dim, dtype, scale=1.0, device="cuda"):
+        self.dtype, self.dt, self.scale = dtype, _code(dtype), float(scale)
+        self.device = _device(device)
+        self.tok_shape = torch.Size((int(rows), int(tokens)))
+        self.out_shape = torch.Size((int(rows), int(tokens), int(dim)))
+        self.table_shape = torch.Size((int(vocab), int(dim)))
+        self.desc = gc_embed_desc(int(rows), int(tokens), int(vocab), int(dim), GC_I32,
+                                  int(tokens) * int(dim), int(tokens))
+        self._ref = ctypes.byref(self.desc)
+        if int(vocab) < 1 or int(dim) < 1 or int(rows) < 0 or int(tokens) < 0:
+            raise ValueError(f"invalid embedding: rows {rows}, tokens {tokens}, vocab {vocab}, dim {dim}")
+        self._ws = _scratch(int(lib().gc_embed_workspace_bytes(self._ref, self.dt)), self.device)
+
+    def _describe(self, tok, rows_like, name):
+        """Fills the descriptor from the tokens' type and both row distances."""
+        rows, tokens, dim = self.out_shape
+        if tok.shape != self.tok_shape:
+            raise ValueError(f"tokens has shape {tuple(tok.shape)}, expected {tuple(self.tok_shape)}")
+        if tok.dtype not in _INDEX_TYPES:
+            raise TypeError(f"tokens has dtype {tok.dtype}; expected int32, int64 or uint8")
+        if rows_like.shape != self.out_shape:
+            raise ValueError(f"{name} has shape {tuple(rows_like.shape)}, expected {tuple(self.out_shape)}")
+        if rows_like.dtype != self.dtype:
+            raise TypeError(f"{name} has dtype {rows_like.dtype}, expected {self.dtype}")
+        self.desc.itype = _INDEX_TYPES[tok.dtype]
+        self.desc.ld_tok = self._distance(tok, "tokens", tokens, (1,))
+        self.desc.ld = self._distance(rows_like, name, tokens * dim, (dim, 1))
+
+    @staticmethod
+    def _distance(t, name, length, inner):
+        """Elements between rows; a row itself has to be dense."""
+        if t.is_contiguous():
+            return length
+        if any(s != want for s, want, n in zip(t.stride()[1:], inner, t.shape[1:]) if n > 1):
+            raise ValueError(f"{name} must be dense within a row")
+        ld = t.stride(0) if t.shape[0] > 1 else length
+        if ld < length:
+            raise ValueError(f"the rows of {name} must not overlap")
+        return ld
+
+    def fwd(self, tok, table, out, stream=None):
+        self._describe(tok, out, "out")
+        tp = _arg(table, "table", self.dtype, self.table_shape, self.device)
+        st = lib().gc_embed_fwd(_on(tok, "tokens", self.device), tp, _on(out, "out", self.device), self._ref,
+                                self.scale, self.dt, _raw_stream(stream, self.device))
+        _check("gc_embed_fwd", st)
+        return out
+
+    def bwd(self, tok, dout, dtable, stream=None):
+        self._describe(tok, dout, "dout")
+        dp = _arg(dtable, "dtable", self.dtype, self.table_shape, self.device)
+        tp, op = _on(tok, "tokens", self.device), _on(dout, "dout", self.device)
+        st = lib().gc_embed_bwd(tp, op, dp, *self._ws[:2], self._ref, self.scale, self.dt,
+                                _raw_stream(stream, self.device))
+        _check("gc_embed_bwd", st)
+        return dtable
+
+
+class GroupNorm:
+    """Group norm with an activation (gc_group_norm_fwd and gc_group_norm_bwd)
+    over tensors of shape (B, C, H, W), in memory NCHW (layout "nchw", as the
+    convolutions have it) or channels last ("nhwc": torch's channels_last
+    format).
+
+    act is "none", "relu", "silu" or "gelu"; gamma and beta (C) have
+    param_dtype, float32 or the storage type, or are None; mean and rstd are
+    float32 (B, groups), in the forward None where they are not wanted.  Calls
+    of one helper share its workspace and must not overlap in time."""
+
+    def __init__(self, shape, groups, act, dtype, layout="nchw", eps=1e-5, param_dtype=torch.float32,
+                 device="cuda"):
+        self.dtype, self.dt = dtype, _code(dtype)
+        self.param_dtype, self.pt = param_dtype, _code(param_dtype)
+        if self.pt not in (GC_F32, self.dt):
+            raise TypeError(f"param_dtype {param_dtype} is neither float32 nor the storage type {dtype}")
+        code, self.format = _named(_LAYOUTS, layout, "layout")
+        self.device = _device(device)
+        B, C, H, W = (int(v) for v in shape)
+        self.shape, self.param_shape = torch.Size((B, C, H, W)), torch.Size((C,))
+        self.stat_shape = torch.Size((B, int(groups)))
+        if min(B, C, H, W, int(groups)) < 1 or C % int(groups):
+            raise ValueError(f"invalid group norm: shape {tuple(self.shape)}, {groups} groups")
+        self.desc = gc_norm_desc(B, C, H, W, int(groups), code, _named(_ACTS, act, "act"), float(eps))
+        self._ref = ctypes.byref(self.desc)
+        need = lib().gc_group_norm_workspace_bytes
+        self._ws = _scratch(max(int(need(op, self._ref, self.dt)) for op in (GC_OP_FWD, GC_OP_BWD)),
+                            self.device)
+
+    def _image(self, t, name):
+        return _arg(t, name, self.dtype, self.shape, self.device, self.format)
+
+    def _param(self, t, name):
+        return None if t is None else _arg(t, name, self.param_dtype, self.param_shape, self.device)
+
+    def _stat(self, t, name):
+        return None if t is None else _arg(t, name, torch.float32, self.stat_shape, self.device)
+
+    def fwd(self, x, gamma, beta, y, mean=None, rstd=None, stream=None):
+        args = (self._image(x, "x"), self._param(gamma, "gamma"), self._param(beta, "beta"),
+                self._image(y, "y"), self._stat(mean, "mean"), self._stat(rstd, "rstd"))
+        st = lib().gc_group_norm_fwd(*args, *self._ws[:2], self._ref, self.dt, self.pt,
+                                     _raw_stream(stream, self.device))
+        _check("gc_group_norm_fwd", st)
+        return y, mean, rstd
+
+    def bwd(self, x, gamma, beta, dy, mean, rstd, dx, dgamma=None, dbeta=None, stream=None):
+        args = (self._image(x, "x"), self._param(gamma, "gamma"), self._param(beta, "beta"),
+                self._image(dy, "dy"), self._stat(mean, "mean"), self._stat(rstd, "rstd"),
+                self._image(dx, "dx"), self._param(dgamma, "dgamma"), self._param(dbeta, "dbeta"))
+        st = lib().gc_group_norm_bwd(*args, *self._ws[:2], self._ref, self.dt, self.pt,
+                                     _raw_stream(stream, self.device))
+        _check("gc_group_norm_bwd", st)
+        return dx, dgamma, dbeta
+
+
+class GradClip:
+    """The global norm of a list of gradients and their clipping (gc_grad_norm
+    and gc_grad_clip), in place or into `out`.
+
+    Made once for a program's gradient tensors, like an optimizer; each call
+    reads the tensors' present addresses.  The norm comes back as a float32 device
+    tensor with one value; nothing is copied to the host.  prescale multiplies the
+    gradients first (the mean over accumulated steps, or an undone loss scale)."""
+
+    def __init__(self, grads, out=None, prescale=1.0, eps=1e-6, device="cuda"):
+        self.grads, self.out = list(grads), list(grads if out is None else out)
+        self.prescale, self.eps = float(prescale), float(eps)
+        if len(self.grads) != len(self.out):
+            raise ValueError(f"{len(self.grads)} gradients but {len(self.out)} outputs")
+        self.device = self.grads[0].device if self.grads else _device(device)
+        self._list = (gc_tensor * len(self.grads))()
+        for i, (g, o) in enumerate(zip(self.grads, self.out)):
+            for t, name in ((g, f"gradient {i}"), (o, f"output {i}")):
+                if t.numel() != g.numel() or t.dtype != g.dtype:
+                    raise ValueError(f"{name} has {t.numel()} elements of {t.dtype}, the gradient "
+                                     f"{g.numel()} of {g.dtype}")
+                if not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
+                if t.device != self.device:
+                    raise ValueError(f"{name} is on {t.device}, gradient 0 is on {self.device}")
+            self._list[i] = gc_tensor(g.data_ptr(), o.data_ptr(), g.numel(), _code(g.dtype))
+        if self.device.type != "cuda":
+            raise ValueError("the gradients must be device tensors")
+        self._ws = torch.empty(int(lib().gc_grad_clip_workspace_bytes(len(self.grads))),
+                               dtype=torch.uint8, device=self.device)
+
+    def _tensors(self):
+        for item, g, o in zip(self._list, self.grads, self.out):
+            if g.numel() != item.n or o.numel() != item.n:
+                raise ValueError("a gradient has changed its size")
+            item.src, item.dst = g.data_ptr(), o.data_ptr()
+        return self._list
+
+    def norm(self, stream=None):
+        norm = torch.empty((), dtype=torch.float32, device=self.device)
+        st = lib().gc_grad_norm(self._tensors(), len(self.grads), self.prescale, norm.data_ptr(),
+                                self._ws.data_ptr(), self._ws.numel(), _raw_stream(stream, self.device))
+        _check("gc_grad_norm", st)
+        return norm
+
+    def clip(self, max_norm, stream=None):
+        norm = torch.empty((), dtype=torch.float32, device=self.device)
+        st = lib().gc_grad_clip(self._tensors(), len(self.grads), float(max_norm), self.prescale, self.eps,
+                                norm.data_ptr(), self._ws.data_ptr(), self._ws.numel(),
+                                _raw_stream(stream, self.device))
+        _check("gc_grad_clip", st)
+        return norm

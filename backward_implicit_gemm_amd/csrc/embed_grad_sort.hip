@@ -1,0 +1,437 @@
+// embed_grad_sort.hip -- the embedding's gradient by sorted tokens:
+//     dtable[v][:] = scale * sum over the tokens k with tok[k] == v of dout[k][:]
+// in fp32, every sum in an order that the sorted positions alone fix, so the
+// result is bit-reproducible; no atomics on values.
+//
+//   1. A stable radix sort of (token, position), 8 bits a pass: digit counts
+//      per tile, (for many tiles a scan of the counts over the tiles,) then
+//      each tile ranks its keys and scatters them.  Tokens outside [0, V)
+//      carry the key V and end up behind all rows.
+//   2. Long runs of one token: every 64 sorted positions that hold one token
+//      are summed into a partial row, and every 64 partials of one token into a
+//      second-level partial, all tiles in parallel.  Other tiles cost nothing.
+//   3. Each row of the table bisects the sorted keys for its run and adds up:
+//      positions to the first tile boundary, partials, second-level partials,
+//      partials, positions.  Rows without a token are written as zeros.
+// Bound by memory: dout is gathered once by rows, dtable written once; at few
+// tokens by the chain of launches.
+#include <algorithm>
+
+#include "gc_embed.h"
+#include "gc_kernels.h"
+#include "gc_vec.h"
+
+namespace gc {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRun = 64;             // sorted positions of a partial, and partials of a second-level one
+constexpr int kScanTiles = 16;       // more tiles than this are scanned by a launch of their own
+constexpr uint32_t kTwoLevels = 4 * kRun * kRun;   // tokens from which second-level partials are made
+
+// ---------------------------------------------------------------- sorting --
+// Key of position i: pass 0 reads the caller's tokens, later passes the
+// previous pass's output.
+struct SortIn {
+    const void *tok;
+    const uint32_t *key, *idx;
+};
+__device__ __forceinline__ uint32_t sort_key(const EmbedGeom &g, const SortIn &in, uint32_t i)
+{
+    if (in.key) return in.key[i];
+    const int64_t t = g.token(in.tok, i);
+    return t >= 0 && t < g.V ? uint32_t(t) : uint32_t(g.V);
+}
+
+// counts[tile][digit]
+template <int ROUNDS>
+__global__ void __launch_bounds__(kThreads) sort_count(EmbedGeom g, SortIn in, int shift,
+                                                       uint32_t *__restrict__ counts)
+{
+    __shared__ uint32_t hist[256];
+    hist[threadIdx.x] = 0;
+    __syncthreads();
+    const uint32_t base = blockIdx.x * (kThreads * ROUNDS);
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const uint32_t i = base + r * kThreads + threadIdx.x;
+        if (i < g.n) atomicAdd(&hist[sort_key(g, in, i) >> shift & 255], 1u);
+    }
+    __syncthreads();
+    counts[size_t(blockIdx.x) * 256 + threadIdx.x] = hist[threadIdx.x];
+}
+
+// One workgroup a digit: counts become their exclusive prefix over the tiles,
+// totals[digit] the sum.
+__global__ void __launch_bounds__(kThreads) sort_scan(uint32_t *__restrict__ counts, int tiles,
+                                                      uint32_t *__restrict__ totals)
+{
+    __shared__ uint32_t part[kThreads];
+    const int d = blockIdx.x, t = threadIdx.x;
+    uint32_t run = 0;
+    for (int t0 = 0; t0 < tiles; t0 += kThreads) {
+        const int tile = t0 + t;
+        const uint32_t c = tile < tiles ? counts[size_t(tile) * 256 + d] : 0;
+        part[t] = c;
+        __syncthreads();
+        for (int w = 1; w < kThreads; w <<= 1) {
+            const uint32_t v = t >= w ? part[t - w] : 0;
+            __syncthreads();
+            part[t] += v;
+            __syncthreads();
+        }
+        if (tile < tiles) counts[size_t(tile) * 256 + d] = run + part[t] - c;
+        run += part[kThreads - 1];
+        __syncthreads();
+    }
+    if (t == 0) totals[d] = run;
+}
+
+// Ranks a tile's keys by their digit (stable) and scatters them.  A wave takes
+// 64 consecutive keys a round; the lanes of one digit find each other by
+// ballots over the digit's bits, and the wave's own counters give the rank
+// among its earlier rounds.
+template <int ROUNDS>
+__global__ void __launch_bounds__(kThreads) sort_scatter(EmbedGeom g, SortIn in, int shift,
+                                                         const uint32_t *__restrict__ counts,
+                                                         const uint32_t *__restrict__ totals, int tiles,
+                                                         uint32_t *__restrict__ key_out,
+                                                         uint32_t *__restrict__ idx_out)
+{
+    constexpr int WAVES = kThreads / 64;
+    __shared__ uint32_t hist[WAVES][256];
+    __shared__ uint32_t scan[256];
+    const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
+    for (int w = 0; w < WAVES; ++w) hist[w][t] = 0;
+    __syncthreads();
+
+    const uint32_t base = blockIdx.x * (kThreads * ROUNDS) + wave * (64 * ROUNDS);
+    uint32_t key[ROUNDS], idx[ROUNDS], rank[ROUNDS];
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const uint32_t i = base + r * 64 + lane;
+        key[r] = i < g.n ? sort_key(g, in, i) : 0;
+        idx[r] = i < g.n ? (in.key ? in.idx[i] : i) : 0;
+    }
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const bool valid = base + r * 64 + lane < g.n;
+        const uint32_t d = key[r] >> shift & 255;
+        uint64_t peers = __ballot(valid);
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+            const uint64_t set = __ballot(d >> b & 1);
+            peers &= (d >> b & 1) ? set : ~set;
+        }
+        const uint64_t below = (uint64_t(1) << lane) - 1;
+        const uint32_t before = __popcll(peers & below);
+        uint32_t seen = 0;
+        if (valid) seen = hist[wave][d];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (valid && before == 0) hist[wave][d] = seen + __popcll(peers);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        rank[r] = seen + before;
+    }
+
+    // thread d: where digit d of this tile starts in the output
+    uint32_t total = 0, prefix = 0;
+    if (totals) {
+        total = totals[t];
+        prefix = counts[size_t(blockIdx.x) * 256 + t];
+    } else {
+        for (int i = 0; i < tiles; ++i) {
+            const uint32_t c = counts[size_t(i) * 256 + t];
+            total += c;
+            if (i < int(blockIdx.x)) prefix += c;
+        }
+    }
+    scan[t] = total;
+    __syncthreads();
+    for (int w = 1; w < 256; w <<= 1) {
+        const uint32_t v = t >= w ? scan[t - w] : 0;
+        __syncthreads();
+        scan[t] += v;
+        __syncthreads();
+    }
+    uint32_t at = scan[t] - total + prefix;
+    for (int w = 0; w < WAVES; ++w) {
+        const uint32_t c = hist[w][t];
+        hist[w][t] = at;
+        at += c;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        if (base + r * 64 + lane >= g.n) continue;
+        const uint32_t dst = hist[wave][key[r] >> shift & 255] + rank[r];
+        key_out[dst] = key[r];
+        idx_out[dst] = idx[r];
+    }
+}
+
+// ------------------------------------------------------------------- sums --
+// Lanes of a row: `team` (a power of two, at most 256) threads, each owning
+// vectors lane, lane + team, ... of the row's D elements.
+template <typename T, int N>
+__device__ __forceinline__ void add_vec(float (&s)[N], const Vec<T, N> &v)
+{
+#pragma unroll
+    for (int j = 0; j < N; ++j) s[j] += v.get(j);
+}
+
+// s += rows idx[a .. b) of dout at column c, in order, four rows in flight
+template <typename T, int N>
+__device__ __forceinline__ void add_positions(const EmbedGeom &g, const T *__restrict__ dout,
+                                              const uint32_t *__restrict__ idx, uint32_t a, uint32_t b, int c,
+                                              float (&s)[N])
+{
+    for (; a + 4 <= b; a += 4) {
+        Vec<T, N> v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = load_vec<T, N>(dout + g.row(idx[a + u]) + c);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) add_vec(s, v[u]);
+    }
+    for (; a < b; ++a) add_vec(s, load_vec<T, N>(dout + g.row(idx[a]) + c));
+}
+
+// s += rows a .. b of a partial table at column c
+template <int N>
+__device__ __forceinline__ void add_partials(const float *__restrict__ part, int D, uint32_t a, uint32_t b, int c,
+                                             float (&s)[N])
+{
+    for (; a + 4 <= b; a += 4) {
+        Vec<float, N> v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = load_vec<float, N>(part + size_t(a + u) * D + c);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) add_vec(s, v[u]);
+    }
+    for (; a < b; ++a) add_vec(s, load_vec<float, N>(part + size_t(a) * D + c));
+}
+
+// Partial p: the sum over sorted positions [p*kRun, (p+1)*kRun) if they all hold
+// one token; else nothing is written (and nothing reads it).
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads) run_partials(EmbedGeom g, const T *__restrict__ dout,
+                                                         const uint32_t *__restrict__ key,
+                                                         const uint32_t *__restrict__ idx,
+                                                         float *__restrict__ part, uint32_t parts, int team)
+{
+    const uint32_t p = blockIdx.x * (kThreads / team) + threadIdx.x / team;
+    if (p >= parts) return;
+    const uint32_t a = p * kRun;
+    const uint32_t k = key[a];
+    if (k != key[a + kRun - 1] || k >= uint32_t(g.V)) return;
+    const int nvec = (g.D + N - 1) / N;
+    for (int i = threadIdx.x % team; i < nvec; i += team) {
+        const int c = min(i * N, g.D - N);
+        float s[N] = {};
+        add_positions<T, N>(g, dout, idx, a, a + kRun, c, s);
+        Vec<float, N> o;
+        o.put(s);
+        store_vec<float, N>(part + size_t(p) * g.D + c, o);
+    }
+}
+
+// Second-level partial q: partials [q*kRun, (q+1)*kRun) where they are all of one token.
+template <int N>
+__global__ void __launch_bounds__(kThreads) run_partials2(int V, int D, const uint32_t *__restrict__ key,
+                                                          const float *__restrict__ part,
+                                                          float *__restrict__ part2, uint32_t parts2, int team)
+{
+    const uint32_t q = blockIdx.x * (kThreads / team) + threadIdx.x / team;
+    if (q >= parts2) return;
+    const uint32_t a = q * (kRun * kRun);
+    const uint32_t k = key[a];
+    if (k != key[a + kRun * kRun - 1] || k >= uint32_t(V)) return;
+    const int nvec = (D + N - 1) / N;
+    for (int i = threadIdx.x % team; i < nvec; i += team) {
+        const int c = min(i * N, D - N);
+        float s[N] = {};
+        add_partials<N>(part, D, q * kRun, (q + 1) * kRun, c, s);
+        Vec<float, N> o;
+        o.put(s);
+        store_vec<float, N>(part2 + size_t(q) * D + c, o);
+    }
+}
+
+// first sorted position whose key is at least v
+__device__ __forceinline__ uint32_t lower_bound(const uint32_t *__restrict__ key, uint32_t n, uint32_t v)
+{
+    uint32_t lo = 0, hi = n;
+    while (lo < hi) {
+        const uint32_t mid = lo + ((hi - lo) >> 1);
+        if (key[mid] < v) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo;
+}
+
+constexpr int kRowsMax = 256;   // table rows of a workgroup, at most
+
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads) table_rows(EmbedGeom g, const T *__restrict__ dout,
+                                                       const uint32_t *__restrict__ key,
+                                                       const uint32_t *__restrict__ idx,
+                                                       const float *__restrict__ part,
+                                                       const float *__restrict__ part2,
+                                                       T *__restrict__ dtable, float scale, int team, int rows_wg)
+{
+    __shared__ uint32_t start[kRowsMax + 1];
+    const int v0 = blockIdx.x * rows_wg;
+    const int rows = min(rows_wg, g.V - v0);
+    for (int i = threadIdx.x; i <= rows; i += kThreads) start[i] = lower_bound(key, g.n, uint32_t(v0 + i));
+    __syncthreads();
+    const int nvec = (g.D + N - 1) / N;
+    const int lane = threadIdx.x % team, teams = kThreads / team;
+    for (int r = threadIdx.x / team; r < rows; r += teams) {
+        const uint32_t a = start[r], b = start[r + 1];
+        // whole tiles [ta, tb) and whole second-level tiles [qa, qb) of the run
+        const uint32_t ta = (a + kRun - 1) / kRun, tb = b / kRun;
+        const uint32_t qa = (ta + kRun - 1) / kRun, qb = tb / kRun;
+        for (int i = lane; i < nvec; i += team) {
+            const int c = min(i * N, g.D - N);
+            float s[N] = {};
+            if (ta < tb) {
+                add_positions<T, N>(g, dout, idx, a, ta * kRun, c, s);
+                if (part2 && qa < qb) {
+                    add_partials<N>(part, g.D, ta, qa * kRun, c, s);
+                    add_partials<N>(part2, g.D, qa, qb, c, s);
+                    add_partials<N>(part, g.D, qb * kRun, tb, c, s);
+                } else {
+                    add_partials<N>(part, g.D, ta, tb, c, s);
+                }
+                add_positions<T, N>(g, dout, idx, tb * kRun, b, c, s);
+            } else {
+                add_positions<T, N>(g, dout, idx, a, b, c, s);
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) s[j] = a < b ? scale * s[j] : 0.f;
+            Vec<T, N> o;
+            o.put(s);
+            store_vec<T, N>(dtable + size_t(v0 + r) * g.D + c, o);
+        }
+    }
+}
+
+// --------------------------------------------------------------- the plan --
+struct SortPlan {
+    int rounds;          // 64-key rounds of a wave: the tile is 256 * rounds keys
+    int tiles, passes;
+    uint32_t parts, parts2;
+    size_t key[2], idx[2], counts, totals, part, part2, bytes;   // byte offsets
+};
+
+size_t take(size_t &at, size_t bytes)
+{
+    const size_t o = at;
+    at += (bytes + 255) & ~size_t(255);
+    return o;
+}
+
+SortPlan plan(const EmbedGeom &g)
+{
+    SortPlan p{};
+    p.rounds = g.n > 131072 ? 16 : 4;
+    const uint32_t tile = kThreads * p.rounds;
+    p.tiles = int((g.n + tile - 1) / tile);
+    int bits = 1;
+    while ((uint64_t(1) << bits) <= uint64_t(g.V)) ++bits;   // keys 0 .. V
+    p.passes = (bits + 7) / 8;
+    p.parts = g.n / kRun;
+    p.parts2 = g.n >= kTwoLevels ? g.n / (kRun * kRun) : 0;
+    size_t at = 0;
+    for (int i = 0; i < 2; ++i) {
+        p.key[i] = take(at, size_t(g.n) * 4);
+        p.idx[i] = take(at, size_t(g.n) * 4);
+    }
+    p.counts = take(at, size_t(p.tiles) * 256 * 4);
+    p.totals = take(at, 256 * 4);
+    p.part = take(at, size_t(p.parts) * g.D * 4);
+    p.part2 = take(at, size_t(p.parts2) * g.D * 4);
+    p.bytes = at;
+    return p;
+}
+
+template <int ROUNDS>
+hipError_t sort_pass(const EmbedGeom &g, const SortPlan &p, const SortIn &in, int shift, uint32_t *counts,
+                     uint32_t *totals, uint32_t *key_out, uint32_t *idx_out, hipStream_t s)
+{
+    hipLaunchKernelGGL(sort_count<ROUNDS>, dim3(p.tiles), dim3(kThreads), 0, s, g, in, shift, counts);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    const bool scan = p.tiles > kScanTiles;
+    if (scan) {
+        hipLaunchKernelGGL(sort_scan, dim3(256), dim3(kThreads), 0, s, counts, p.tiles, totals);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(sort_scatter<ROUNDS>, dim3(p.tiles), dim3(kThreads), 0, s, g, in, shift, counts,
+                       scan ? totals : nullptr, p.tiles, key_out, idx_out);
+    return hipGetLastError();
+}
+
+template <typename T, int N>
+hipError_t sums(const EmbedGeom &g, const SortPlan &p, const void *dout, const uint32_t *key, const uint32_t *idx,
+                float *part, float *part2, void *dtable, float scale, hipStream_t s)
+{
+    const int nvec = (g.D + N - 1) / N;
+    int team = 1;
+    while (team < nvec && team < kThreads) team <<= 1;
+    const int teams = kThreads / team;
+    if (p.parts) {
+        hipLaunchKernelGGL((run_partials<T, N>), dim3((p.parts + teams - 1) / teams), dim3(kThreads), 0, s, g,
+                           (const T *)dout, key, idx, part, p.parts, team);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    if (p.parts2) {
+        hipLaunchKernelGGL(run_partials2<N>, dim3((p.parts2 + teams - 1) / teams), dim3(kThreads), 0, s, g.V, g.D,
+                           key, part, part2, p.parts2, team);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    const int rows_wg = std::min(kRowsMax, teams * 8);
+    hipLaunchKernelGGL((table_rows<T, N>), dim3((g.V + rows_wg - 1) / rows_wg), dim3(kThreads), 0, s, g,
+                       (const T *)dout, key, idx, part, p.parts2 ? part2 : nullptr, (T *)dtable, scale, team, rows_wg);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t embed_grad_sort_ws_bytes(const EmbedGeom &g) { return plan(g).bytes; }
+
+template <typename T>
+hipError_t launch_embed_grad_sort(const EmbedGeom &g, const void *tok, const void *dout, void *dtable, float scale,
+                                  void *ws, hipStream_t s)
+{
+    const SortPlan p = plan(g);
+    char *base = static_cast<char *>(ws);
+    uint32_t *key[2], *idx[2];
+    for (int i = 0; i < 2; ++i) {
+        key[i] = reinterpret_cast<uint32_t *>(base + p.key[i]);
+        idx[i] = reinterpret_cast<uint32_t *>(base + p.idx[i]);
+    }
+    uint32_t *counts = reinterpret_cast<uint32_t *>(base + p.counts);
+    uint32_t *totals = reinterpret_cast<uint32_t *>(base + p.totals);
+    SortIn in{tok, nullptr, nullptr};
+    int out = 0;
+    for (int pass = 0; pass < p.passes && g.n; ++pass) {
+        const hipError_t e = p.rounds == 16
+            ? sort_pass<16>(g, p, in, 8 * pass, counts, totals, key[out], idx[out], s)
+            : sort_pass<4>(g, p, in, 8 * pass, counts, totals, key[out], idx[out], s);
+        if (e != hipSuccess) return e;
+        in = SortIn{tok, key[out], idx[out]};
+        out ^= 1;
+    }
+    float *part = reinterpret_cast<float *>(base + p.part), *part2 = reinterpret_cast<float *>(base + p.part2);
+    if (g.D >= kVec<T>)
+        return sums<T, kVec<T>>(g, p, dout, in.key, in.idx, part, part2, dtable, scale, s);
+    return sums<T, 1>(g, p, dout, in.key, in.idx, part, part2, dtable, scale, s);
+}
+
+template hipError_t launch_embed_grad_sort<float>(const EmbedGeom &, const void *, const void *, void *, float,
+                                                  void *, hipStream_t);
+template hipError_t launch_embed_grad_sort<bf16_t>(const EmbedGeom &, const void *, const void *, void *, float,
+                                                   void *, hipStream_t);
+
+}  // namespace gc

@@ -1,6 +1,7 @@
 // gc_kernels.h -- launchers of the gfx950 kernels, called by the C ABI layer.
 #pragma once
 
+#include "../../include/gc.h"
 #include "gc_common.h"
 
 namespace gc {
@@ -115,5 +116,46 @@ hipError_t launch_wgrad_reduce(const float *part, void *dw, int splits, int n, h
 template <typename T>
 hipError_t launch_wgrad_reduce_bias(const float *part, void *dw, void *db, int splits, int OC, int N,
                                     int NP, hipStream_t s);
+
+// The global gradient norm and clipping (grad_clip.hip).  A launch takes
+// kClipTensors tensors in its arguments.
+constexpr int kClipTensors = 96;
+size_t grad_clip_ws_bytes(int count);
+hipError_t launch_grad_clip(const gc_tensor *list, int count, float max_norm, float prescale, float eps,
+                            bool scale, float *norm, void *ws, hipStream_t s);
+
+// Embedding lookup (embed_fwd.hip) and its gradient by sorted tokens
+// (embed_grad_sort.hip).
+struct EmbedGeom;
+template <typename T>
+hipError_t launch_embed_fwd(const EmbedGeom &g, const void *tok, const void *table, void *out, float scale,
+                            hipStream_t s);
+size_t embed_grad_sort_ws_bytes(const EmbedGeom &g);
+template <typename T>
+hipError_t launch_embed_grad_sort(const EmbedGeom &g, const void *tok, const void *dout, void *dtable, float scale,
+                                  void *ws, hipStream_t s);
+
+// Group norm with an activation.  The split kernels (norm_split.hip) take every
+// shape; plan_norm_split returns false past the largest grid.
+struct NormGeom;
+struct NormSplitPlan {
+    int N;                     // elements of a thread's vector
+    int cols, blocks, slots;   // channels last: vectors of a workgroup's row, column blocks, rows at a time
+    int chunks, len;           // pieces an image's positions are cut into, and their length
+    int64_t grid;
+    size_t part_bytes_fwd, part_bytes_bwd, ws_fwd, ws_bwd;
+};
+bool plan_norm_split(const NormGeom &g, int dtype, NormSplitPlan &q);
+template <typename T>
+hipError_t launch_norm_split_fwd(const NormGeom &g, const NormSplitPlan &q, const void *x, const void *gamma,
+                                 const void *beta, void *y, float *mean, float *rstd, void *ws, hipStream_t s);
+template <typename T>
+hipError_t launch_norm_split_bwd(const NormGeom &g, const NormSplitPlan &q, const void *x, const void *gamma,
+                                 const void *beta, const void *dy, const float *mean, const float *rstd, void *dx,
+                                 void *dgamma, void *dbeta, void *ws, hipStream_t s);
+// dgamma and dbeta from `rows` rows of per-channel pairs (dbeta's, dgamma's)
+template <typename T>
+hipError_t launch_norm_params(const NormGeom &g, int64_t rows, const float *part, void *dgamma, void *dbeta,
+                              hipStream_t s);
 
 }  // namespace gc

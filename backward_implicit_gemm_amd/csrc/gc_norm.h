@@ -1,0 +1,127 @@
+// gc_norm.h -- geometry and arithmetic shared by the group-norm kernels.
+//
+//   hat = (x - mean) * rstd,  z = gamma * hat + beta,  y = act(z)
+//   g = dy * act'(z),  dbeta = sum g,  dgamma = sum g * hat
+//   dx = rstd * (gamma*g - c1 - hat*c2),   c1 = mean over the group of gamma*g,
+//                                          c2 = mean over the group of gamma*g*hat
+#pragma once
+
+#include "../../include/gc.h"
+#include "gc_vec.h"
+
+namespace gc {
+
+struct NormGeom {
+    int B, C, HW, G, Cg;   // Cg = C / G channels of a group
+    int nhwc;              // 0: [B][C][HW], 1: [B][HW][C]
+    int act;               // gc_act
+    int pf32;              // gamma, beta and their gradients in fp32 (else the storage type)
+    float eps;
+    int64_t img;           // C*HW, elements of an image (below 2^31)
+    FastDiv fd_HW, fd_Cg;
+};
+
+template <typename T>
+__device__ __forceinline__ float param(const NormGeom &g, const void *p, int c, float none)
+{
+    if (!p) return none;
+    return g.pf32 ? static_cast<const float *>(p)[c] : to_f32(static_cast<const T *>(p)[c]);
+}
+
+template <typename T>
+__device__ __forceinline__ void set_param(const NormGeom &g, void *p, int c, float v)
+{
+    if (!p) return;
+    if (g.pf32) static_cast<float *>(p)[c] = v;
+    else static_cast<T *>(p)[c] = from_f32<T>(v);
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
+
+// Phi(z), the normal distribution function, and e = exp(-z^2/2): Abramowitz and
+// Stegun 7.1.26 for erf(|z|/sqrt 2), absolute error at most 1.5e-7 (half of that
+// in Phi), whose exponential is the density's.
+__device__ __forceinline__ float phi(float z, float &e)
+{
+    const float u = fabsf(z) * 0.70710678f;
+    e = __expf(-u * u);
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, u, 1.f));
+    float p = fmaf(1.061405429f, t, -1.453152027f);
+    p = fmaf(p, t, 1.421413741f);
+    p = fmaf(p, t, -0.284496736f);
+    p = fmaf(p, t, 0.254829592f);
+    const float tail = 0.5f * p * t * e;   // Phi(-|z|)
+    return z < 0.f ? tail : 1.f - tail;
+}
+
+__device__ __forceinline__ float norm_z(float x, float mean, float rstd, float gamma, float beta)
+{
+    return fmaf((x - mean) * rstd, gamma, beta);
+}
+
+// act(z); a NaN stays one
+template <int N>
+__device__ __forceinline__ void activate(int act, float (&z)[N])
+{
+    if (act == GC_ACT_RELU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) z[j] = z[j] <= 0.f ? 0.f : z[j];
+    } else if (act == GC_ACT_SILU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) z[j] *= sigmoid(z[j]);
+    } else if (act == GC_ACT_GELU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            float e;
+            z[j] *= phi(z[j], e);
+        }
+    }
+}
+
+// Whether z <= 0 for relu's derivative (0 there and at 0).  z in fp32 is off
+// by less than 2^-21 of its product term; nearer to the kink than that (a few
+// elements in a million) the sign is taken in fp64.
+__device__ __forceinline__ bool relu_off(float x, float mean, float rstd, float gamma, float beta, float z)
+{
+    if (fabsf(z) > 4.8e-7f * fabsf(z - beta) || z != z) return z <= 0.f;
+    return (double(x) - mean) * rstd * gamma + beta <= 0.0;
+}
+
+// dy[j] becomes g = dy * act'(z); x[j] becomes hat
+template <int N, int NC>
+__device__ __forceinline__ void act_grad(int act, float (&x)[N], float (&dy)[N], const float (&mean)[NC],
+                                         const float (&rstd)[NC], const float (&gamma)[NC],
+                                         const float (&beta)[NC])
+{
+    static_assert(NC == 1 || NC == N, "constants of one channel or of each element");
+    if (act == GC_ACT_RELU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int k = NC == 1 ? 0 : j;
+            const float hat = (x[j] - mean[k]) * rstd[k];
+            if (relu_off(x[j], mean[k], rstd[k], gamma[k], beta[k], fmaf(hat, gamma[k], beta[k]))) dy[j] = 0.f;
+            x[j] = hat;
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = (x[j] - mean[NC == 1 ? 0 : j]) * rstd[NC == 1 ? 0 : j];
+    if (act == GC_ACT_SILU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float z = fmaf(x[j], gamma[NC == 1 ? 0 : j], beta[NC == 1 ? 0 : j]);
+            const float s = sigmoid(z);
+            dy[j] *= s * fmaf(z, 1.f - s, 1.f);
+        }
+    } else if (act == GC_ACT_GELU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float z = fmaf(x[j], gamma[NC == 1 ? 0 : j], beta[NC == 1 ? 0 : j]);
+            float e;
+            const float p = phi(z, e);
+            dy[j] *= fmaf(z * 0.39894228f, e, p);
+        }
+    }
+}
+
+}  // namespace gc

@@ -1,0 +1,231 @@
+// gc_train_api.hip -- the C ABI of the operators around the convolutions
+// (embedding, group norm, gradient clipping), declared in include/gc.h:
+// argument checks, workspace sizes and the choice of kernels.  All checks
+// come before the first HIP call.
+#include <limits.h>
+#include <math.h>
+
+#include "gc_embed.h"
+#include "gc_kernels.h"
+#include "gc_norm.h"
+
+using namespace gc;
+
+namespace {
+
+bool valid_dtype(int dtype) { return dtype == GC_F32 || dtype == GC_BF16; }
+
+bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+bool aligned_to(const void *p, int dtype) { return aligned(p, dtype == GC_F32 ? 4 : 2); }
+
+int hip_status(hipError_t e) { return e == hipSuccess ? GC_OK : GC_ERR_HIP; }
+
+int check_workspace(const void *ws, size_t have, size_t need)
+{
+    if (!need) return GC_OK;
+    if (!ws || have < need || !aligned(ws, 256)) return GC_ERR_WORKSPACE;
+    return GC_OK;
+}
+
+// ---------------------------------------------------------------- embedding --
+int check_embed(const gc_embed_desc *d, EmbedGeom *g)
+{
+    if (!d || d->rows < 0 || d->tokens < 0 || d->V < 1 || d->D < 1) return GC_ERR_INVALID_ARG;
+    if (d->itype != GC_I32 && d->itype != GC_I64 && d->itype != GC_U8) return GC_ERR_INVALID_ARG;
+    const __int128 n = (__int128)d->rows * d->tokens;
+    if (n > INT_MAX || (__int128)d->tokens * d->D > INT_MAX) return GC_ERR_INVALID_ARG;
+    if (d->ld < (int64_t)d->tokens * d->D || d->ld_tok < d->tokens) return GC_ERR_INVALID_ARG;
+    const __int128 most = (__int128)1 << 60;   // byte offsets stay within 64 bits
+    if ((__int128)d->rows * d->ld > most || (__int128)d->rows * d->ld_tok > most) return GC_ERR_INVALID_ARG;
+    if (g) {
+        g->n = uint32_t(n);
+        g->V = d->V;
+        g->D = d->D;
+        g->itype = d->itype;
+        g->ld = d->ld;
+        g->ld_tok = d->ld_tok;
+        g->fd_T = make_fastdiv(d->tokens > 0 ? uint32_t(d->tokens) : 1u);
+    }
+    return GC_OK;
+}
+
+uintptr_t token_size(int itype) { return itype == GC_I32 ? 4 : itype == GC_I64 ? 8 : 1; }
+
+// ---------------------------------------------------------------- group norm --
+int check_norm(const gc_norm_desc *d, NormGeom *g)
+{
+    if (!d || d->B < 1 || d->C < 1 || d->H < 1 || d->W < 1 || d->groups < 1) return GC_ERR_INVALID_ARG;
+    if (d->C % d->groups) return GC_ERR_INVALID_ARG;
+    if (d->layout != GC_NCHW && d->layout != GC_NHWC) return GC_ERR_INVALID_ARG;
+    if (d->act < GC_ACT_NONE || d->act > GC_ACT_GELU) return GC_ERR_INVALID_ARG;
+    if (!(d->eps >= 0.f) || isinf(d->eps)) return GC_ERR_INVALID_ARG;
+    const int64_t hw = (int64_t)d->H * d->W;
+    if (hw > INT_MAX || (__int128)hw * d->C > INT_MAX) return GC_ERR_INVALID_ARG;
+    if (g) {
+        g->B = d->B;
+        g->C = d->C;
+        g->HW = int(hw);
+        g->G = d->groups;
+        g->Cg = d->C / d->groups;
+        // one position or one channel: both layouts are the same memory
+        g->nhwc = d->layout == GC_NHWC && hw > 1 && d->C > 1;
+        g->act = d->act;
+        g->eps = d->eps;
+        g->img = hw * d->C;
+        g->fd_HW = make_fastdiv(uint32_t(hw));
+        g->fd_Cg = make_fastdiv(uint32_t(g->Cg));
+    }
+    return GC_OK;
+}
+
+int check_norm_types(int dtype, int param_dtype, NormGeom &g)
+{
+    if (!valid_dtype(dtype) || !valid_dtype(param_dtype)) return GC_ERR_INVALID_ARG;
+    if (param_dtype != GC_F32 && param_dtype != dtype) return GC_ERR_INVALID_ARG;
+    g.pf32 = param_dtype == GC_F32;
+    return GC_OK;
+}
+
+int check_list(const gc_tensor *list, int count, bool dst)
+{
+    if (count < 0 || (count > 0 && !list)) return GC_ERR_INVALID_ARG;
+    __int128 total = 0;
+    for (int i = 0; i < count; ++i) {
+        const gc_tensor &t = list[i];
+        if (t.n < 0 || !valid_dtype(t.dtype)) return GC_ERR_INVALID_ARG;
+        if (t.n && (!t.src || !aligned_to(t.src, t.dtype))) return GC_ERR_INVALID_ARG;
+        if (dst && t.n && (!t.dst || !aligned_to(t.dst, t.dtype))) return GC_ERR_INVALID_ARG;
+        total += t.n;
+    }
+    // the chunk numbers of a launch stay within 31 bits
+    return total <= ((__int128)1 << 42) ? GC_OK : GC_ERR_INVALID_ARG;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gc_embed_fwd(const void *tokens, const void *table, void *out, const gc_embed_desc *d, float scale, int dtype,
+                 void *stream)
+{
+    EmbedGeom g;
+    const int st = check_embed(d, &g);
+    if (st != GC_OK) return st;
+    if (!valid_dtype(dtype) || !table || !aligned_to(table, dtype)) return GC_ERR_INVALID_ARG;
+    if (g.n == 0) return GC_OK;
+    if (!tokens || !out || !aligned(tokens, token_size(d->itype)) || !aligned_to(out, dtype))
+        return GC_ERR_INVALID_ARG;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return hip_status(dtype == GC_F32 ? launch_embed_fwd<float>(g, tokens, table, out, scale, s)
+                                      : launch_embed_fwd<bf16_t>(g, tokens, table, out, scale, s));
+}
+
+size_t gc_embed_workspace_bytes(const gc_embed_desc *d, int dtype)
+{
+    EmbedGeom g;
+    if (check_embed(d, &g) != GC_OK || !valid_dtype(dtype)) return 0;
+    return embed_grad_sort_ws_bytes(g);
+}
+
+int gc_embed_bwd(const void *tokens, const void *dout, void *dtable, void *workspace, size_t ws_bytes,
+                 const gc_embed_desc *d, float scale, int dtype, void *stream)
+{
+    EmbedGeom g;
+    int st = check_embed(d, &g);
+    if (st != GC_OK) return st;
+    if (!valid_dtype(dtype) || !dtable || !aligned_to(dtable, dtype)) return GC_ERR_INVALID_ARG;
+    if (g.n && (!tokens || !dout || !aligned(tokens, token_size(d->itype)) || !aligned_to(dout, dtype)))
+        return GC_ERR_INVALID_ARG;
+    st = check_workspace(workspace, ws_bytes, embed_grad_sort_ws_bytes(g));
+    if (st != GC_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return hip_status(dtype == GC_F32
+                          ? launch_embed_grad_sort<float>(g, tokens, dout, dtable, scale, workspace, s)
+                          : launch_embed_grad_sort<bf16_t>(g, tokens, dout, dtable, scale, workspace, s));
+}
+
+size_t gc_group_norm_workspace_bytes(int op, const gc_norm_desc *d, int dtype)
+{
+    NormGeom g;
+    NormSplitPlan q;
+    if (check_norm(d, &g) != GC_OK || !valid_dtype(dtype)) return 0;
+    if ((op != GC_OP_FWD && op != GC_OP_BWD) || !plan_norm_split(g, dtype, q)) return 0;
+    return op == GC_OP_FWD ? q.ws_fwd : q.ws_bwd;
+}
+
+int gc_group_norm_fwd(const void *x, const void *gamma, const void *beta, void *y, float *mean, float *rstd,
+                      void *workspace, size_t ws_bytes, const gc_norm_desc *d, int dtype, int param_dtype,
+                      void *stream)
+{
+    NormGeom g;
+    int st = check_norm(d, &g);
+    if (st == GC_OK) st = check_norm_types(dtype, param_dtype, g);
+    if (st != GC_OK) return st;
+    if (!x || !y || !aligned_to(x, dtype) || !aligned_to(y, dtype)) return GC_ERR_INVALID_ARG;
+    if ((gamma && !aligned_to(gamma, param_dtype)) || (beta && !aligned_to(beta, param_dtype)))
+        return GC_ERR_INVALID_ARG;
+    if (!aligned(mean, 4) || !aligned(rstd, 4)) return GC_ERR_INVALID_ARG;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    NormSplitPlan q;
+    if (!plan_norm_split(g, dtype, q)) return GC_ERR_UNSUPPORTED;
+    st = check_workspace(workspace, ws_bytes, q.ws_fwd);
+    if (st != GC_OK) return st;
+    return hip_status(dtype == GC_F32
+                          ? launch_norm_split_fwd<float>(g, q, x, gamma, beta, y, mean, rstd, workspace, s)
+                          : launch_norm_split_fwd<bf16_t>(g, q, x, gamma, beta, y, mean, rstd, workspace, s));
+}
+
+int gc_group_norm_bwd(const void *x, const void *gamma, const void *beta, const void *dy, const float *mean,
+                      const float *rstd, void *dx, void *dgamma, void *dbeta, void *workspace, size_t ws_bytes,
+                      const gc_norm_desc *d, int dtype, int param_dtype, void *stream)
+{
+    NormGeom g;
+    int st = check_norm(d, &g);
+    if (st == GC_OK) st = check_norm_types(dtype, param_dtype, g);
+    if (st != GC_OK) return st;
+    if (!x || !dy || !mean || !rstd || !dx) return GC_ERR_INVALID_ARG;
+    if (!aligned_to(x, dtype) || !aligned_to(dy, dtype) || !aligned_to(dx, dtype) || !aligned(mean, 4) ||
+        !aligned(rstd, 4))
+        return GC_ERR_INVALID_ARG;
+    const void *params[] = {gamma, beta, dgamma, dbeta};
+    for (const void *p : params)
+        if (p && !aligned_to(p, param_dtype)) return GC_ERR_INVALID_ARG;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    NormSplitPlan q;
+    if (!plan_norm_split(g, dtype, q)) return GC_ERR_UNSUPPORTED;
+    st = check_workspace(workspace, ws_bytes, q.ws_bwd);
+    if (st != GC_OK) return st;
+    return hip_status(dtype == GC_F32 ? launch_norm_split_bwd<float>(g, q, x, gamma, beta, dy, mean, rstd, dx,
+                                                                     dgamma, dbeta, workspace, s)
+                                      : launch_norm_split_bwd<bf16_t>(g, q, x, gamma, beta, dy, mean, rstd, dx,
+                                                                      dgamma, dbeta, workspace, s));
+}
+
+size_t gc_grad_clip_workspace_bytes(int count) { return count < 0 ? 0 : grad_clip_ws_bytes(count); }
+
+int gc_grad_norm(const gc_tensor *list, int count, float prescale, float *norm, void *workspace, size_t ws_bytes,
+                 void *stream)
+{
+    int st = check_list(list, count, false);
+    if (st != GC_OK) return st;
+    if (!norm || !aligned(norm, 4) || !isfinite(prescale)) return GC_ERR_INVALID_ARG;
+    st = check_workspace(workspace, ws_bytes, grad_clip_ws_bytes(count));
+    if (st != GC_OK) return st;
+    return hip_status(launch_grad_clip(list, count, 0.f, prescale, 0.f, false, norm, workspace,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+int gc_grad_clip(const gc_tensor *list, int count, float max_norm, float prescale, float eps, float *norm,
+                 void *workspace, size_t ws_bytes, void *stream)
+{
+    int st = check_list(list, count, true);
+    if (st != GC_OK) return st;
+    if (!norm || !aligned(norm, 4) || !isfinite(prescale) || !isfinite(eps)) return GC_ERR_INVALID_ARG;
+    if (!(max_norm >= 0.f) || eps < 0.f) return GC_ERR_INVALID_ARG;
+    st = check_workspace(workspace, ws_bytes, grad_clip_ws_bytes(count));
+    if (st != GC_OK) return st;
+    return hip_status(launch_grad_clip(list, count, max_norm, prescale, eps, true, norm, workspace,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

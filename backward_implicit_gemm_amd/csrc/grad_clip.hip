@@ -1,0 +1,232 @@
+// grad_clip.hip -- the global norm of a list of tensors, and their clipping:
+//     norm = |prescale| * sqrt(sum of g^2 over every element of every tensor)
+//     c    = prescale * min(1, max_norm / (norm + eps)),   dst = c * g
+//
+// The list travels in the kernel arguments (kClipTensors tensors a launch), so
+// nothing is kept between calls and a captured graph holds its own copy.  Every
+// tensor is cut into chunks of one size; workgroup w of a launch takes chunks
+// w, w + grid, ... and finds a chunk's tensor by bisecting the chunk counts
+// (wave-uniform scalar loads).
+//
+// Pass 1 adds up squares in fp64 (the product of two fp32 values is exact there
+// and cannot overflow or vanish; fp64 adds at the vector unit's full rate hide
+// behind the loads) and writes one partial per workgroup.  Pass 2 sums the
+// partials in the same fixed order in every workgroup, so the norm and the result
+// are bit-reproducible, and scales.  Both passes are bound by memory: the
+// gradients are read twice and written once.
+#include "gc_kernels.h"
+#include "gc_vec.h"
+
+namespace gc {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxGrid = 1024;     // workgroups of a launch: 4 per CU
+constexpr int kFold = 2048;        // more partials than this are folded by a launch of their own
+
+struct ClipArgs {
+    const void *src[kClipTensors];
+    void *dst[kClipTensors];
+    int64_t n[kClipTensors];
+    int first[kClipTensors + 1];          // first chunk of each tensor
+    uint32_t bf16[kClipTensors / 32];     // bit t: tensor t holds bf16
+    int count;
+    int chunk;                            // elements of a chunk
+};
+
+// The tensor chunk c lies in: the last t with first[t] <= c (empty tensors
+// before it share its first chunk).
+__device__ __forceinline__ int tensor_of(const ClipArgs &a, int c)
+{
+    int lo = 0, hi = a.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.first[mid] <= c) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+template <typename T>
+__device__ __forceinline__ double chunk_squares(const T *p, int len)
+{
+    constexpr int V = kVec<T>;
+    double s = 0;
+    const int whole = len / V;
+    for (int i = threadIdx.x; i < whole; i += kThreads) {
+        const Vec<T, V> v = load_vec<T, V>(p + size_t(i) * V);
+#pragma unroll
+        for (int j = 0; j < V; ++j) s = fma(double(v.get(j)), double(v.get(j)), s);
+    }
+    const int e = whole * V + threadIdx.x;
+    if (e < len) s = fma(double(to_f32(p[e])), double(to_f32(p[e])), s);
+    return s;
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_scale(const T *p, T *q, int len, float c)
+{
+    constexpr int V = kVec<T>;
+    const int whole = len / V;
+    for (int i = threadIdx.x; i < whole; i += kThreads) {
+        const Vec<T, V> v = load_vec<T, V>(p + size_t(i) * V);
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = c * v.get(j);
+        Vec<T, V> o;
+        o.put(f);
+        store_vec<T, V>(q + size_t(i) * V, o);
+    }
+    const int e = whole * V + threadIdx.x;
+    if (e < len) q[e] = from_f32<T>(c * to_f32(p[e]));
+}
+
+__global__ void __launch_bounds__(kThreads) clip_squares(const ClipArgs a, double *__restrict__ part)
+{
+    __shared__ double red[16];
+    const int chunks = a.first[a.count];
+    double s = 0;
+    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int t = tensor_of(a, c);
+        const int64_t at = int64_t(c - a.first[t]) * a.chunk;
+        const int len = int(min(int64_t(a.chunk), a.n[t] - at));
+        if (a.bf16[t >> 5] >> (t & 31) & 1)
+            s += chunk_squares(static_cast<const bf16_t *>(a.src[t]) + at, len);
+        else
+            s += chunk_squares(static_cast<const float *>(a.src[t]) + at, len);
+    }
+    s = block_sum(s, red);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+__device__ __forceinline__ double sum_partials(const double *part, int np, double *red)
+{
+    double s = 0;
+    for (int i = threadIdx.x; i < np; i += kThreads) s += part[i];
+    return block_sum(s, red);
+}
+
+__global__ void __launch_bounds__(kThreads) clip_fold(const double *__restrict__ part, int np,
+                                                      double *__restrict__ out)
+{
+    __shared__ double red[16];
+    const double s = sum_partials(part, np, red);
+    if (threadIdx.x == 0) *out = s;
+}
+
+// norm only
+__global__ void __launch_bounds__(kThreads) clip_norm(const double *__restrict__ part, int np,
+                                                      float prescale, float *__restrict__ norm)
+{
+    __shared__ double red[16];
+    const double s = sum_partials(part, np, red);
+    if (threadIdx.x == 0) *norm = float(fabs(double(prescale)) * sqrt(s));
+}
+
+__global__ void __launch_bounds__(kThreads) clip_scale(const ClipArgs a, const double *__restrict__ part,
+                                                       int np, float max_norm, float prescale, float eps,
+                                                       float *__restrict__ norm)
+{
+    __shared__ double red[16];
+    const double total = fabs(double(prescale)) * sqrt(sum_partials(part, np, red));
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = float(total);
+    // a NaN norm (or an infinite one against an infinite max_norm) stays NaN
+    const double r = double(max_norm) / (total + double(eps));
+    const float c = float(double(prescale) * (r >= 1.0 ? 1.0 : r));
+    const int chunks = a.first[a.count];
+    for (int k = blockIdx.x; k < chunks; k += gridDim.x) {
+        const int t = tensor_of(a, k);
+        if (c == 1.f && a.src[t] == a.dst[t]) continue;   // in place, and nothing changes
+        const int64_t at = int64_t(k - a.first[t]) * a.chunk;
+        const int len = int(min(int64_t(a.chunk), a.n[t] - at));
+        if (a.bf16[t >> 5] >> (t & 31) & 1)
+            chunk_scale(static_cast<const bf16_t *>(a.src[t]) + at, static_cast<bf16_t *>(a.dst[t]) + at,
+                        len, c);
+        else
+            chunk_scale(static_cast<const float *>(a.src[t]) + at, static_cast<float *>(a.dst[t]) + at,
+                        len, c);
+    }
+}
+
+int launches(int count) { return (count + kClipTensors - 1) / kClipTensors; }
+
+// Chunk size of a list of `total` elements: about four chunks for each of
+// kMaxGrid workgroups, within 4096 .. 65536 elements.
+int chunk_of(int64_t total)
+{
+    const int64_t c = (total / (4 * kMaxGrid) + 4095) / 4096 * 4096;
+    return int(c < 4096 ? 4096 : c > 65536 ? 65536 : c);
+}
+
+// Arguments of launch l (tensors l*kClipTensors ...); returns its grid, or 0
+// for tensors without elements, or -1 if the chunks pass 2^31.
+int fill_args(const gc_tensor *list, int count, int l, int chunk, ClipArgs &a)
+{
+    const int t0 = l * kClipTensors;
+    a.count = count - t0 < kClipTensors ? count - t0 : kClipTensors;
+    a.chunk = chunk;
+    for (uint32_t &b : a.bf16) b = 0;
+    int64_t chunks = 0;
+    for (int t = 0; t < a.count; ++t) {
+        const gc_tensor &x = list[t0 + t];
+        a.src[t] = x.src;
+        a.dst[t] = x.dst;
+        a.n[t] = x.n;
+        a.first[t] = int(chunks);
+        if (x.dtype == GC_BF16) a.bf16[t >> 5] |= 1u << (t & 31);
+        chunks += (x.n + chunk - 1) / chunk;
+        if (chunks > 0x7FFFFFFF) return -1;
+    }
+    a.first[a.count] = int(chunks);
+    return int(chunks < kMaxGrid ? chunks : kMaxGrid);
+}
+
+}  // namespace
+
+size_t grad_clip_ws_bytes(int count)
+{
+    // one partial a workgroup, and the folded sum
+    return (size_t(launches(count)) * kMaxGrid + 1) * sizeof(double);
+}
+
+hipError_t launch_grad_clip(const gc_tensor *list, int count, float max_norm, float prescale, float eps,
+                            bool scale, float *norm, void *ws, hipStream_t s)
+{
+    double *part = static_cast<double *>(ws);
+    int64_t total = 0;
+    for (int t = 0; t < count; ++t) total += list[t].n;
+    const int chunk = chunk_of(total);
+    const int nl = launches(count);
+    ClipArgs a;
+    for (int l = 0; l < nl; ++l)           // before anything is enqueued
+        if (fill_args(list, count, l, chunk, a) < 0) return hipErrorInvalidValue;
+    int np = 0;
+    for (int l = 0; l < nl; ++l) {
+        const int grid = fill_args(list, count, l, chunk, a);
+        if (!grid) continue;
+        hipLaunchKernelGGL(clip_squares, dim3(grid), dim3(kThreads), 0, s, a, part + np);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+        np += grid;
+    }
+    if (np > kFold) {
+        double *folded = part + np;
+        hipLaunchKernelGGL(clip_fold, dim3(1), dim3(kThreads), 0, s, part, np, folded);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+        part = folded;
+        np = 1;
+    }
+    if (!scale || np == 0) {
+        hipLaunchKernelGGL(clip_norm, dim3(1), dim3(kThreads), 0, s, part, np, prescale, norm);
+        return hipGetLastError();
+    }
+    for (int l = 0; l < nl; ++l) {
+        const int grid = fill_args(list, count, l, chunk, a);
+        if (!grid) continue;
+        hipLaunchKernelGGL(clip_scale, dim3(grid), dim3(kThreads), 0, s, a, part, np, max_norm, prescale,
+                           eps, norm);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace gc

@@ -182,6 +182,110 @@ int gc_conv_bwd(const void *x, const void *w, const void *dy, const void *y_mask
  * buf_bytes == 0.  Enqueues nothing. */
 int gc_conv_plan_name(int op, const gc_conv_desc *d, int dtype, char *buf, size_t buf_bytes);
 
+/* ------------------------------------------------------------------------
+ * The operators a policy network's training step has around its
+ * convolutions.  The conventions above hold, except that element counts may
+ * pass 2^31 where a limit below says so, and the workspace, where one is
+ * needed, is 256-byte aligned.  Inputs and outputs of a call must not
+ * overlap unless a call says that they may.
+ * ------------------------------------------------------------------------ */
+
+/* Embedding: the discrete features of an observation (the encoder the PR
+ * page times embeds 47 of them into rows of 32 values) or any other tokens.
+ *
+ *   out[r,t,:]    = scale * table[tok[r,t],:]     (zeros for an empty token)
+ *   dtable[v,:]   = scale * sum over (r,t) with tok[r,t] == v of dout[r,t,:]
+ *
+ * A token outside [0, V) is empty: its output row is zeros and its gradient
+ * goes nowhere.  tok has `rows` rows of `tokens` values, ld_tok >= tokens
+ * elements apart; out and dout rows of tokens*D elements, ld >= tokens*D
+ * elements apart (so the embedding can be part of a wider feature row; the
+ * elements between are not touched).  table and dtable are dense [V][D].
+ * rows and tokens may be 0; rows*tokens and tokens*D are below 2^31. */
+typedef enum { GC_I32 = 0, GC_I64 = 1, GC_U8 = 2 } gc_index_type;
+typedef struct {
+    int64_t rows;
+    int tokens, V, D;
+    int itype;             /* gc_index_type of tok */
+    int64_t ld, ld_tok;
+} gc_embed_desc;
+
+int gc_embed_fwd(const void *tokens, const void *table, void *out, const gc_embed_desc *d, float scale, int dtype,
+                 void *stream);
+
+/* Every row of dtable is written, rows without a token as zeros.  Sums run in
+ * fp32 over the tokens sorted by value, in an order the tokens alone fix, and
+ * are rounded once: the result is bit-identical from run to run. */
+size_t gc_embed_workspace_bytes(const gc_embed_desc *d, int dtype);
+int gc_embed_bwd(const void *tokens, const void *dout, void *dtable, void *workspace, size_t ws_bytes,
+                 const gc_embed_desc *d, float scale, int dtype, void *stream);
+
+/* Group norm with an activation, per image over groups of C/groups channels:
+ *
+ *   hat = (x - mean) * rstd,  rstd = 1 / sqrt(var + eps)   (var biased)
+ *   y   = act(gamma[c] * hat + beta[c])
+ *
+ * layout GC_NCHW ([B][C][H][W], what the convolutions read and write) or
+ * GC_NHWC ([B][H][W][C]).  x, y, dy, dx have the storage type dtype; gamma,
+ * beta, dgamma and dbeta [C] have param_dtype, GC_F32 or dtype; gamma == NULL
+ * stands for ones, beta == NULL for zeros.  mean and rstd are fp32
+ * [B][groups]; the forward writes them where they are not NULL, the backward
+ * reads them.  C*H*W is below 2^31; B*C*H*W may be larger. */
+typedef enum { GC_NCHW = 0, GC_NHWC = 1 } gc_layout;
+typedef enum {
+    GC_ACT_NONE = 0,
+    GC_ACT_RELU = 1,
+    GC_ACT_SILU = 2,       /* z / (1 + exp(-z)) */
+    GC_ACT_GELU = 3        /* z * Phi(z), Phi the normal distribution function */
+} gc_act;
+typedef struct {
+    int B, C, H, W;
+    int groups;            /* divides C */
+    int layout;            /* gc_layout */
+    int act;               /* gc_act */
+    float eps;             /* >= 0 */
+} gc_norm_desc;
+
+/* op GC_OP_FWD or GC_OP_BWD; 0 if none is needed, or for an invalid descriptor. */
+size_t gc_group_norm_workspace_bytes(int op, const gc_norm_desc *d, int dtype);
+int gc_group_norm_fwd(const void *x, const void *gamma, const void *beta, void *y, float *mean, float *rstd,
+                      void *workspace, size_t ws_bytes, const gc_norm_desc *d, int dtype, int param_dtype,
+                      void *stream);
+
+/* With g = dy * act'(gamma*hat + beta) (relu's derivative is 0 at 0):
+ *   dbeta = sum g,  dgamma = sum g*hat  (over images and positions)
+ *   dx = rstd * (gamma*g - mean(gamma*g) - hat * mean(gamma*g*hat))  (means over the group)
+ * The activation's argument is recomputed from x, mean and rstd.  dgamma and
+ * dbeta may be NULL.  Sums have a fixed order: bit-identical from run to run. */
+int gc_group_norm_bwd(const void *x, const void *gamma, const void *beta, const void *dy, const float *mean,
+                      const float *rstd, void *dx, void *dgamma, void *dbeta, void *workspace, size_t ws_bytes,
+                      const gc_norm_desc *d, int dtype, int param_dtype, void *stream);
+
+/* The global norm of a list of gradients, and their clipping by it:
+ *
+ *   norm = |prescale| * sqrt(sum over all elements of src^2)
+ *   dst  = prescale * min(1, max_norm / (norm + eps)) * src
+ *
+ * The list is host memory, read during the call; a captured graph keeps its
+ * own copy.  Tensors may differ in type and size (n may be 0, the list
+ * empty), and together hold up to 2^42 elements; dst may be src.  Squares are
+ * added in fp64 in a fixed order.  norm (fp32, one value) is written in any
+ * case.  A norm that is NaN makes every dst NaN, an infinite one makes finite
+ * elements 0 and the others NaN, as the formula says; gc_grad_norm writes the
+ * norm alone and leaves dst unread. */
+typedef struct {
+    const void *src;
+    void *dst;
+    int64_t n;
+    int dtype;
+} gc_tensor;
+
+size_t gc_grad_clip_workspace_bytes(int count);
+int gc_grad_norm(const gc_tensor *list, int count, float prescale, float *norm, void *workspace, size_t ws_bytes,
+                 void *stream);
+int gc_grad_clip(const gc_tensor *list, int count, float max_norm, float prescale, float eps, float *norm,
+                 void *workspace, size_t ws_bytes, void *stream);
+
 /* Human-readable name of a status code. */
 const char *gc_status_string(int status);
 

@@ -1,0 +1,177 @@
+"""GPU: embedding lookup with scaling and its gradient against their
+definitions in 64 bits.
+
+Tokens are uniform, skewed (long runs of one value after sorting), all equal
+or all empty; row lengths are odd, shorter than a vector and longer than a
+workgroup; rows of out and dout lie apart.  The forward rounds a product
+(2^-24) and the result; a gradient is a sum of m terms, off by at most
+m * 2^-24 of its absolute terms, and rounded.
+"""
+import pytest
+import torch
+
+import train_ref as ref
+from backward_implicit_gemm_amd import binding as gb
+from parity import Guarded
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def setup_module():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    gb.lib()
+
+
+def tokens(rows, T, V, kind, index, seed, extra=0):
+    gen = torch.Generator("cuda").manual_seed(seed)
+    u = torch.rand((rows, T + extra), generator=gen, device="cuda", dtype=torch.float64)
+    power, empty = {"uniform": (1, 0.0), "skewed": (6, 0.1), "equal": (0, 0.0), "empty": (1, 1.0)}[kind]
+    t = (u ** power * V).long().clamp(max=V - 1)
+    if empty:
+        out = torch.rand(t.shape, generator=gen, device="cuda") < empty
+        t[out] = V + 5 if index == torch.uint8 else -1
+        t[out & (u < 0.5)] = min(V, 255)
+    return t.to(index)[:, :T]
+
+
+def apart(rows, T, D, dtype, extra, offset=0, fill=None):
+    """A (rows, T, D) view whose rows lie `extra` elements further apart, the guard of its buffer and the gaps."""
+    g = Guarded((rows, T * D + extra), dtype, offset=offset)
+    if fill is not None:
+        g.t.copy_(fill)
+    return g, g.t[:, :T * D].unflatten(1, (T, D)), g.t[:, T * D:]
+
+
+CASES = [
+    # rows, T, V, D, kind, index, extra
+    (1, 1, 1, 1, "uniform", torch.int32, 0),
+    (1, 47, 128, 32, "uniform", torch.int32, 0),
+    (1024, 47, 128, 32, "uniform", torch.uint8, 256),
+    (300, 47, 128, 32, "skewed", torch.int64, 3),
+    (513, 7, 61, 33, "skewed", torch.uint8, 1),
+    (65, 129, 300, 3, "uniform", torch.int32, 0),
+    (400, 33, 5000, 129, "skewed", torch.int64, 1),
+    (8, 512, 40000, 1031, "uniform", torch.int32, 0),
+    (16, 1024, 70001, 40, "skewed", torch.int32, 8),
+    (20, 1000, 3, 17, "equal", torch.int32, 0),
+    (31, 1000, 900, 9, "equal", torch.int64, 0),
+    (50, 10, 40, 64, "empty", torch.int32, 2),
+    (3, 5, 200, 2500, "uniform", torch.int32, 0),
+    (200, 1024, 1500, 8, "skewed", torch.int32, 0),     # over 131,072 tokens: the larger sorting tile
+    (2, 3, 255, 5, "uniform", torch.int32, 0),
+    (2, 300, 256, 16, "skewed", torch.int32, 0),        # keys 0 .. 256 need a second sorting pass
+    (1200, 64, 257, 48, "skewed", torch.int32, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("rows,T,V,D,kind,index,extra", CASES)
+def test_matches_the_definition(rows, T, V, D, kind, index, extra, dtype):
+    t = TYPES[dtype]
+    tok = tokens(rows, T, V, kind, index, 3, extra=extra % 5)
+    gen = torch.Generator("cuda").manual_seed(4)
+    scale = 1.7
+    e = gb.Embedding(rows, T, V, D, t, scale)
+    table = torch.randn((V, D), generator=gen, device="cuda").to(t)
+    g, out, gap = apart(rows, T, D, t, extra)
+    before = gap.clone().view(torch.int16 if t == torch.bfloat16 else torch.int32)
+    e.fwd(tok, table, out)
+    torch.cuda.synchronize()
+    g.check("out")
+    assert torch.equal(gap.contiguous().view(before.dtype), before), "elements between rows were written"
+    want = ref.embed_fwd(tok.long(), table, scale)
+    f = ref.over(out, want, (ref.half(t) + 2 * ref.U) * want.abs())
+
+    _, dout, _ = apart(rows, T, D, t, extra, offset=extra % 3,
+                       fill=torch.randn((rows, T * D + extra), generator=gen, device="cuda").to(t))
+    runs = []
+    for _ in range(2):
+        gd = Guarded((V, D), t)
+        e.bwd(tok, dout, gd.t)
+        torch.cuda.synchronize()
+        gd.check("dtable")
+        runs.append(gd.t)
+    assert torch.equal(*runs), "the gradient differs from run to run"
+    want, size, m = ref.embed_bwd(tok.long(), dout, V, scale)
+    bound = (m[:, None] + 2) * ref.U * size
+    b = ref.over(runs[0], want, bound + ref.half(t) * (want.abs() + bound))
+    print(f"rows={rows} T={T} V={V} D={D} {kind} {dtype}: out={f:.2f} dtable={b:.2f}", flush=True)
+    assert f <= 1 and b <= 1
+    assert bool((runs[0][m == 0] == 0).all())
+
+
+def test_no_tokens():
+    for rows, T in ((0, 5), (5, 0)):
+        e = gb.Embedding(rows, T, 9, 4, torch.float32)
+        tok = torch.empty((rows, T), dtype=torch.int32, device="cuda")
+        out = torch.empty((rows, T, 4), device="cuda")
+        table = torch.full((9, 4), 3.0, device="cuda")
+        e.fwd(tok, table, out)
+        e.bwd(tok, out, table)
+        assert bool((table == 0).all())
+
+
+def test_adjoint():
+    """<embed(table), dout> = <table, gradient(dout)>, in integers, exactly."""
+    gen = torch.Generator("cuda").manual_seed(9)
+    for V, D in ((128, 32), (3000, 20)):
+        tok = torch.randint(-3, V + 3, (90, 11), generator=gen, device="cuda", dtype=torch.int32)
+        table, dout = (torch.randint(-8, 9, s, generator=gen, device="cuda").float() for s in ((V, D), (90, 11, D)))
+        e = gb.Embedding(90, 11, V, D, torch.float32, 2.0)
+        out, dtable = torch.empty_like(dout), torch.empty_like(table)
+        e.fwd(tok, table, out)
+        e.bwd(tok, dout, dtable)
+        assert int((out.double() * dout).sum()) == int((table.double() * dtable).sum())
+
+
+@pytest.mark.parametrize("V,D", [(128, 32), (5000, 96)])
+def test_graph_replays_and_other_streams(V, D):
+    gen = torch.Generator("cuda").manual_seed(6)
+    rows, T = 200, 47
+    tok = torch.randint(-1, V, (rows, T), generator=gen, device="cuda", dtype=torch.int32)
+    table, dout = (torch.randn(s, generator=gen, device="cuda").bfloat16() for s in ((V, D), (rows, T, D)))
+    e = gb.Embedding(rows, T, V, D, torch.bfloat16)
+    out, dtable = torch.empty_like(dout), torch.empty_like(table)
+
+    def step():
+        e.fwd(tok, table, out)
+        e.bwd(tok, dout, dtable)
+
+    step()
+    torch.cuda.synchronize()
+    want = [out.clone(), dtable.clone()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    side = torch.cuda.Stream()
+    for rep in range(4):
+        out.fill_(float("nan"))
+        dtable.fill_(float("nan"))
+        torch.cuda.synchronize()
+        if rep % 2:
+            with torch.cuda.stream(side):
+                step()
+        else:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(dtable, want[1]), rep
+
+
+def test_offsets_past_32_bits():
+    """dout of more than 2^31 elements, rows far apart: the last rows count."""
+    rows, T, D, V = 2100, 2, 8, 16
+    ld = 2 ** 20 + 1
+    wide = torch.zeros((rows, ld), dtype=torch.bfloat16, device="cuda")
+    out = wide[:, :T * D].unflatten(1, (T, D))
+    tok = torch.arange(rows * T, device="cuda", dtype=torch.int32).reshape(rows, T) % V
+    table = torch.arange(V * D, device="cuda").reshape(V, D).bfloat16()
+    e = gb.Embedding(rows, T, V, D, torch.bfloat16)
+    e.fwd(tok, table, out)
+    assert torch.equal(out, table[tok.long()])
+    dtable = torch.empty_like(table)
+    out.fill_(1.0)
+    e.bwd(tok, out, dtable)
+    want = torch.bincount(tok.reshape(-1), minlength=V).bfloat16()[:, None].expand(V, D)
+    assert torch.equal(dtable, want)
