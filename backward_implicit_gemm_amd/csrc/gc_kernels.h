@@ -153,6 +153,37 @@ template <typename T>
 hipError_t launch_norm_split_bwd(const NormGeom &g, const NormSplitPlan &q, const void *x, const void *gamma,
                                  const void *beta, const void *dy, const float *mean, const float *rstd, void *dx,
                                  void *dgamma, void *dbeta, void *ws, hipStream_t s);
+// Groups that stay in registers (norm_res_nchw.hip, norm_res_nhwc.hip; planned in
+// norm_plan.hip): plan_norm_res returns false where a group is too large.
+struct NormResPlan {
+    int N, NV;             // elements of a vector, vectors a thread holds
+    int L, teams, threads; // threads of a team, teams of a workgroup, threads of a workgroup
+    int two;               // NCHW: vectors may straddle two channels
+    int wave;              // channels last: a team is one wave
+    int P;                 // lanes that add up one group (channels last) or channel (NCHW)
+    int slots, CW, slabs, Gs;   // channels last: rows at a time; channels, number and groups of a slab
+    int width, team_lds;   // channels last: LDS entries of a row, LDS words of a team
+    int images;            // backward: image slots walking the batch
+    int rows;              // backward: rows of per-channel partials
+    FastDiv fd_cols, fd_Eg;
+    int64_t grid;
+    size_t lds_bytes, ws_bytes;
+};
+bool plan_norm_res(const NormGeom &g, int dtype, bool bwd, NormResPlan &q);
+template <typename T>
+hipError_t launch_norm_res_nchw_fwd(const NormGeom &g, const NormResPlan &q, const void *x, const void *gamma,
+                                    const void *beta, void *y, float *mean, float *rstd, hipStream_t s);
+template <typename T>
+hipError_t launch_norm_res_nchw_bwd(const NormGeom &g, const NormResPlan &q, const void *x, const void *gamma,
+                                    const void *beta, const void *dy, const float *mean, const float *rstd, void *dx,
+                                    float *part, hipStream_t s);
+template <typename T>
+hipError_t launch_norm_res_nhwc_fwd(const NormGeom &g, const NormResPlan &q, const void *x, const void *gamma,
+                                    const void *beta, void *y, float *mean, float *rstd, hipStream_t s);
+template <typename T>
+hipError_t launch_norm_res_nhwc_bwd(const NormGeom &g, const NormResPlan &q, const void *x, const void *gamma,
+                                    const void *beta, const void *dy, const float *mean, const float *rstd, void *dx,
+                                    float *part, hipStream_t s);
 // dgamma and dbeta from `rows` rows of per-channel pairs (dbeta's, dgamma's)
 template <typename T>
 hipError_t launch_norm_params(const NormGeom &g, int64_t rows, const float *part, void *dgamma, void *dbeta,

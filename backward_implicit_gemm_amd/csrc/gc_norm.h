@@ -78,15 +78,6 @@ __device__ __forceinline__ void activate(int act, float (&z)[N])
     }
 }
 
-// Whether z <= 0 for relu's derivative (0 there and at 0).  z in fp32 is off
-// by less than 2^-21 of its product term; nearer to the kink than that (a few
-// elements in a million) the sign is taken in fp64.
-__device__ __forceinline__ bool relu_off(float x, float mean, float rstd, float gamma, float beta, float z)
-{
-    if (fabsf(z) > 4.8e-7f * fabsf(z - beta) || z != z) return z <= 0.f;
-    return (double(x) - mean) * rstd * gamma + beta <= 0.0;
-}
-
 // dy[j] becomes g = dy * act'(z); x[j] becomes hat
 template <int N, int NC>
 __device__ __forceinline__ void act_grad(int act, float (&x)[N], float (&dy)[N], const float (&mean)[NC],
@@ -95,12 +86,30 @@ __device__ __forceinline__ void act_grad(int act, float (&x)[N], float (&dy)[N],
 {
     static_assert(NC == 1 || NC == N, "constants of one channel or of each element");
     if (act == GC_ACT_RELU) {
+        // 0 where z <= 0.  z in fp32 is off by less than 2^-21 of its product term;
+        // nearer to the kink than that (an element in a million) its sign is taken in fp64.
+        uint32_t off = 0, near = 0;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int k = NC == 1 ? 0 : j;
-            const float hat = (x[j] - mean[k]) * rstd[k];
-            if (relu_off(x[j], mean[k], rstd[k], gamma[k], beta[k], fmaf(hat, gamma[k], beta[k]))) dy[j] = 0.f;
-            x[j] = hat;
+            const float z = norm_z(x[j], mean[k], rstd[k], gamma[k], beta[k]);
+            off |= z <= 0.f ? 1u << j : 0u;
+            near |= fabsf(z) <= 4.8e-7f * fabsf(z - beta[k]) ? 1u << j : 0u;
+        }
+        if (near) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int k = NC == 1 ? 0 : j;
+                if (!(near >> j & 1)) continue;
+                const double z = (double(x[j]) - mean[k]) * rstd[k] * gamma[k] + beta[k];
+                off = (off & ~(1u << j)) | (z <= 0.0 ? 1u << j : 0u);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int k = NC == 1 ? 0 : j;
+            if (off >> j & 1) dy[j] = 0.f;
+            x[j] = (x[j] - mean[k]) * rstd[k];
         }
         return;
     }

@@ -67,8 +67,9 @@ int check_norm(const gc_norm_desc *d, NormGeom *g)
         g->HW = int(hw);
         g->G = d->groups;
         g->Cg = d->C / d->groups;
-        // one position or one channel: both layouts are the same memory
-        g->nhwc = d->layout == GC_NHWC && hw > 1 && d->C > 1;
+        // with one position or one channel both layouts are the same memory: taken as
+        // the one whose rows are long
+        g->nhwc = hw == 1 || (d->layout == GC_NHWC && d->C > 1);
         g->act = d->act;
         g->eps = d->eps;
         g->img = hw * d->C;
@@ -84,6 +85,51 @@ int check_norm_types(int dtype, int param_dtype, NormGeom &g)
     if (param_dtype != GC_F32 && param_dtype != dtype) return GC_ERR_INVALID_ARG;
     g.pf32 = param_dtype == GC_F32;
     return GC_OK;
+}
+
+// The kernels of a group norm: resident where a group fits, else split.
+enum class NormKind { Resident, Split, None };
+struct NormSel {
+    NormKind k;
+    NormResPlan r;
+    NormSplitPlan q;
+    size_t ws_bytes;
+};
+NormSel select_norm(const NormGeom &g, int dtype, bool bwd)
+{
+    NormSel s{};
+    if (plan_norm_res(g, dtype, bwd, s.r)) {
+        s.k = NormKind::Resident;
+        s.ws_bytes = s.r.ws_bytes;
+    } else if (plan_norm_split(g, dtype, s.q)) {
+        s.k = NormKind::Split;
+        s.ws_bytes = bwd ? s.q.ws_bwd : s.q.ws_fwd;
+    } else {
+        s.k = NormKind::None;
+    }
+    return s;
+}
+
+template <typename T>
+hipError_t norm_fwd(const NormGeom &g, const NormSel &s, const void *x, const void *gamma, const void *beta, void *y,
+                    float *mean, float *rstd, void *ws, hipStream_t st)
+{
+    if (s.k == NormKind::Split) return launch_norm_split_fwd<T>(g, s.q, x, gamma, beta, y, mean, rstd, ws, st);
+    return g.nhwc ? launch_norm_res_nhwc_fwd<T>(g, s.r, x, gamma, beta, y, mean, rstd, st)
+                  : launch_norm_res_nchw_fwd<T>(g, s.r, x, gamma, beta, y, mean, rstd, st);
+}
+
+template <typename T>
+hipError_t norm_bwd(const NormGeom &g, const NormSel &s, const void *x, const void *gamma, const void *beta,
+                    const void *dy, const float *mean, const float *rstd, void *dx, void *dgamma, void *dbeta,
+                    void *ws, hipStream_t st)
+{
+    if (s.k == NormKind::Split)
+        return launch_norm_split_bwd<T>(g, s.q, x, gamma, beta, dy, mean, rstd, dx, dgamma, dbeta, ws, st);
+    float *part = dgamma || dbeta ? static_cast<float *>(ws) : nullptr;
+    const hipError_t e = g.nhwc ? launch_norm_res_nhwc_bwd<T>(g, s.r, x, gamma, beta, dy, mean, rstd, dx, part, st)
+                                : launch_norm_res_nchw_bwd<T>(g, s.r, x, gamma, beta, dy, mean, rstd, dx, part, st);
+    return e == hipSuccess && part ? launch_norm_params<T>(g, s.r.rows, part, dgamma, dbeta, st) : e;
 }
 
 int check_list(const gc_tensor *list, int count, bool dst)
@@ -147,10 +193,8 @@ int gc_embed_bwd(const void *tokens, const void *dout, void *dtable, void *works
 size_t gc_group_norm_workspace_bytes(int op, const gc_norm_desc *d, int dtype)
 {
     NormGeom g;
-    NormSplitPlan q;
-    if (check_norm(d, &g) != GC_OK || !valid_dtype(dtype)) return 0;
-    if ((op != GC_OP_FWD && op != GC_OP_BWD) || !plan_norm_split(g, dtype, q)) return 0;
-    return op == GC_OP_FWD ? q.ws_fwd : q.ws_bwd;
+    if (check_norm(d, &g) != GC_OK || !valid_dtype(dtype) || (op != GC_OP_FWD && op != GC_OP_BWD)) return 0;
+    return select_norm(g, dtype, op == GC_OP_BWD).ws_bytes;
 }
 
 int gc_group_norm_fwd(const void *x, const void *gamma, const void *beta, void *y, float *mean, float *rstd,
@@ -166,13 +210,12 @@ int gc_group_norm_fwd(const void *x, const void *gamma, const void *beta, void *
         return GC_ERR_INVALID_ARG;
     if (!aligned(mean, 4) || !aligned(rstd, 4)) return GC_ERR_INVALID_ARG;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    NormSplitPlan q;
-    if (!plan_norm_split(g, dtype, q)) return GC_ERR_UNSUPPORTED;
-    st = check_workspace(workspace, ws_bytes, q.ws_fwd);
+    const NormSel sel = select_norm(g, dtype, false);
+    if (sel.k == NormKind::None) return GC_ERR_UNSUPPORTED;
+    st = check_workspace(workspace, ws_bytes, sel.ws_bytes);
     if (st != GC_OK) return st;
-    return hip_status(dtype == GC_F32
-                          ? launch_norm_split_fwd<float>(g, q, x, gamma, beta, y, mean, rstd, workspace, s)
-                          : launch_norm_split_fwd<bf16_t>(g, q, x, gamma, beta, y, mean, rstd, workspace, s));
+    return hip_status(dtype == GC_F32 ? norm_fwd<float>(g, sel, x, gamma, beta, y, mean, rstd, workspace, s)
+                                      : norm_fwd<bf16_t>(g, sel, x, gamma, beta, y, mean, rstd, workspace, s));
 }
 
 int gc_group_norm_bwd(const void *x, const void *gamma, const void *beta, const void *dy, const float *mean,
@@ -191,14 +234,14 @@ int gc_group_norm_bwd(const void *x, const void *gamma, const void *beta, const 
     for (const void *p : params)
         if (p && !aligned_to(p, param_dtype)) return GC_ERR_INVALID_ARG;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    NormSplitPlan q;
-    if (!plan_norm_split(g, dtype, q)) return GC_ERR_UNSUPPORTED;
-    st = check_workspace(workspace, ws_bytes, q.ws_bwd);
+    const NormSel sel = select_norm(g, dtype, true);
+    if (sel.k == NormKind::None) return GC_ERR_UNSUPPORTED;
+    st = check_workspace(workspace, ws_bytes, sel.ws_bytes);
     if (st != GC_OK) return st;
-    return hip_status(dtype == GC_F32 ? launch_norm_split_bwd<float>(g, q, x, gamma, beta, dy, mean, rstd, dx,
-                                                                     dgamma, dbeta, workspace, s)
-                                      : launch_norm_split_bwd<bf16_t>(g, q, x, gamma, beta, dy, mean, rstd, dx,
-                                                                      dgamma, dbeta, workspace, s));
+    return hip_status(dtype == GC_F32 ? norm_bwd<float>(g, sel, x, gamma, beta, dy, mean, rstd, dx, dgamma, dbeta,
+                                                        workspace, s)
+                                      : norm_bwd<bf16_t>(g, sel, x, gamma, beta, dy, mean, rstd, dx, dgamma, dbeta,
+                                                         workspace, s));
 }
 
 size_t gc_grad_clip_workspace_bytes(int count) { return count < 0 ? 0 : grad_clip_ws_bytes(count); }

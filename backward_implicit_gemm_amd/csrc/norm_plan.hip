@@ -1,0 +1,168 @@
+// norm_plan.hip -- the shapes the resident group-norm kernels take, on the host.
+//
+// A plan is a vector length N, the vectors a thread holds (NV) and the threads of
+// a team (L).  Of the plans that fit, the one of least estimated time is taken:
+// a thread's time grows as NV plus a constant for its reductions, and teams past
+// what the chip holds at once (4096 waves at these register counts) wait for
+// their turn.
+#include <algorithm>
+
+#include "gc_kernels.h"
+#include "gc_norm_res.h"
+#include "ig_common.h"
+
+namespace gc {
+namespace {
+
+constexpr double kWavesAtOnce = 4096;
+constexpr int kVectors[] = {1, 2, 3, 4, 8};
+constexpr size_t kLdsMost = 64 * 1024;
+
+double cost(double units, int L, int NV, double waste)
+{
+    return std::max(1.0, units * L / (64 * kWavesAtOnce)) * (2 + NV) * waste;
+}
+
+// whether a kernel of L threads that hold `held` elements each is built
+bool holds(bool bwd, int L, int held)
+{
+    return bwd ? held <= kHeldMost && L <= res_threads_bwd(held) : L <= res_threads_fwd(held);
+}
+
+int pow2_at_most(int64_t v)
+{
+    int p = 1;
+    while (int64_t(p) * 2 <= v) p *= 2;
+    return p;
+}
+
+bool plan_nchw(const NormGeom &g, int widest, bool bwd, NormResPlan &best)
+{
+    // the longest vector that lies in one channel, if it has 8 bytes at least; else a
+    // full one that straddles
+    int N = widest;
+    while (N > 1 && g.HW % N) N >>= 1;
+    const bool two = N * 2 < widest && g.HW >= widest;
+    if (two) N = widest;
+    const int64_t M = int64_t(g.Cg) * g.HW, nvec = (M + N - 1) / N;
+    double least = 1e300;
+    for (int NV : kVectors)
+        for (int L = 1; L <= 1024; L *= 2) {
+            if (int64_t(L) * NV < nvec || (L > 1 && int64_t(L) * NV >= 4 * nvec)) continue;
+            if (!holds(bwd, L, N * NV)) continue;
+            const double c = cost(double(g.B) * g.G, L, NV, 1.0);
+            if (c >= least) continue;
+            NormResPlan q{};
+            q.N = N;
+            q.NV = NV;
+            q.two = two;
+            q.L = L;
+            q.threads = L > 64 ? L : kResThreads;   // past a wave the workgroup is the team
+            q.teams = q.threads / L;
+            q.P = pow2_at_most(std::max(1, std::min(64, L / std::max(1, std::min(g.Cg, L)))));
+            if (bwd) {
+                q.lds_bytes = std::max<size_t>(256, size_t(q.teams) * nvec * 2 * (two ? 2 : 1) * sizeof(float));
+                if (q.lds_bytes > kLdsMost) continue;
+                q.images = int(std::min<double>(g.B, std::max(1.0, kWavesAtOnce * 64 / (double(g.G) * L))));
+                q.rows = q.images;
+                q.grid = (int64_t(q.images) * g.G + q.teams - 1) / q.teams;
+            } else {
+                q.grid = (int64_t(g.B) * g.G + q.teams - 1) / q.teams;
+            }
+            if (q.grid > 0x7FFFFFFF) continue;
+            least = c;
+            best = q;
+        }
+    return least < 1e300;
+}
+
+bool plan_nhwc(const NormGeom &g, int widest, int size, bool bwd, NormResPlan &best)
+{
+    double least = 1e300;
+    for (int N = widest; N >= 1; N >>= 1) {
+        if (g.C % N) continue;
+        // slabs of k whole groups, as wide as fits and no narrower than 64 bytes
+        for (int k = g.G; k >= 1; --k) {
+            if (g.G % k) continue;
+            const int CW = k * g.Cg;
+            if (CW % N || (k < g.G && CW * size < 64)) continue;
+            const int CV = CW / N, slabs = g.G / k;
+            for (int NV : kVectors)
+                for (int L = 64; L <= 1024; L *= 2) {
+                    if (!holds(bwd, L, N * NV) || CV > L) continue;
+                    const int slots = L / CV;
+                    if (int64_t(slots) * NV < g.HW) continue;
+                    const double c = cost(double(g.B) * slabs, L, NV, CW * size < 128 && k < g.G ? 1.5 : 1.0);
+                    if (c >= least) continue;
+                    NormResPlan q{};
+                    q.N = N;
+                    q.NV = NV;
+                    q.L = L;
+                    q.wave = L == 64;
+                    q.threads = q.wave ? kResThreads : L;
+                    q.teams = q.threads / L;
+                    q.slots = std::min(slots, g.HW);
+                    q.CW = CW;
+                    q.slabs = slabs;
+                    q.Gs = k;
+                    const bool one = g.Cg % N == 0;
+                    q.width = one ? CV : CW;
+                    q.fd_cols = make_fastdiv(CV);
+                    q.fd_Eg = make_fastdiv(one ? g.Cg / N : g.Cg);
+                    q.P = pow2_at_most(std::max(1, std::min(64, L / k)));
+                    q.team_lds = 2 * q.slots * q.width + 2 * k;
+                    size_t lds = size_t(q.teams) * q.team_lds * sizeof(float);
+                    if (bwd) lds = std::max(lds, size_t(q.teams) * q.slots * CW * 2 * sizeof(float));
+                    q.lds_bytes = lds;
+                    if (lds > kLdsMost) continue;
+                    if (bwd) {
+                        const double at_once = kWavesAtOnce * 64 / (double(slabs) * L);
+                        const int most = int(std::min<double>(g.B, std::max(1.0, at_once)));
+                        q.rows = (most + q.teams - 1) / q.teams;
+                        q.images = q.rows * q.teams;
+                        q.grid = int64_t(q.rows) * slabs;
+                    } else {
+                        q.grid = (int64_t(g.B) * slabs + q.teams - 1) / q.teams;
+                    }
+                    if (q.grid > 0x7FFFFFFF) continue;
+                    least = c;
+                    best = q;
+                }
+            if (least < 1e300 && k == g.G) break;   // whole images fit
+        }
+        if (least < 1e300) return true;             // shorter vectors only where longer ones fit nowhere
+    }
+    return false;
+}
+
+}  // namespace
+
+namespace {
+bool search(const NormGeom &g, int dtype, bool bwd, NormResPlan &q)
+{
+    const int size = dtype == GC_F32 ? 4 : 2, widest = 16 / size;
+    const bool ok = g.nhwc ? plan_nhwc(g, widest, size, bwd, q) : plan_nchw(g, widest, bwd, q);
+    if (ok && bwd) q.ws_bytes = size_t(q.rows) * g.C * 2 * sizeof(float);
+    return ok;
+}
+}  // namespace
+
+// The search costs more host time than a launch: its answers are kept by shape.
+bool plan_norm_res(const NormGeom &g, int dtype, bool bwd, NormResPlan &q)
+{
+    struct Answer {
+        bool ok;
+        NormResPlan q;
+    };
+    static SearchMemo<Answer> memo;
+    const int key[12] = {g.B, g.C, g.HW, g.G, g.nhwc, dtype, bwd};
+    const Answer a = memo.get(key, [&] {
+        Answer v{};
+        v.ok = search(g, dtype, bwd, v.q);
+        return v;
+    });
+    q = a.q;
+    return a.ok;
+}
+
+}  // namespace gc

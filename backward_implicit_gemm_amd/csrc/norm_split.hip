@@ -322,34 +322,32 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_apply(NormGeom g, NormSplit
     }
 }
 
-// dgamma and dbeta from rows partial[row][C][2]: a workgroup takes 16 channels,
-// 32 threads a row, and adds its 32 row lanes in order.
-constexpr int kParamCols = 32;
+// dgamma and dbeta from rows partial[row][C][2]: a workgroup takes 4 channels (8
+// values, one sector of memory a row), 128 rows at a time, and adds its row lanes
+// in order.
+constexpr int kParamCols = 8, kParamRows = 128, kParamUnroll = 8;
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_params(NormGeom g, int64_t rows, const float *__restrict__ part,
                                                     void *__restrict__ dgamma, void *__restrict__ dbeta)
 {
-    __shared__ float red[32][kParamCols + 1];
+    __shared__ float red[kParamRows][kParamCols + 1];
     const int col = threadIdx.x % kParamCols, row = threadIdx.x / kParamCols;
     const int e = blockIdx.x * kParamCols + col;
-    float s0 = 0, s1 = 0, s2 = 0, s3 = 0;
+    float s[kParamUnroll] = {};
     if (e < 2 * g.C) {
         int64_t r = row;
-        for (; r + 96 < rows; r += 128) {
-            s0 += part[r * 2 * g.C + e];
-            s1 += part[(r + 32) * 2 * g.C + e];
-            s2 += part[(r + 64) * 2 * g.C + e];
-            s3 += part[(r + 96) * 2 * g.C + e];
-        }
-        for (; r < rows; r += 32) s0 += part[r * 2 * g.C + e];
+        for (; r + (kParamUnroll - 1) * kParamRows < rows; r += kParamUnroll * kParamRows)
+#pragma unroll
+            for (int u = 0; u < kParamUnroll; ++u) s[u] += part[(r + u * kParamRows) * 2 * g.C + e];
+        for (; r < rows; r += kParamRows) s[0] += part[r * 2 * g.C + e];
     }
-    red[row][col] = (s0 + s1) + (s2 + s3);
+    red[row][col] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
     __syncthreads();
-    if (threadIdx.x < kParamCols && e < 2 * g.C) {
-        float s = 0;
-        for (int i = 0; i < 32; ++i) s += red[i][col];
-        set_param<T>(g, e % 2 ? dgamma : dbeta, e / 2, s);
+    for (int w = kParamRows / 2; w > 0; w >>= 1) {
+        if (row < w) red[row][col] += red[row + w][col];
+        __syncthreads();
     }
+    if (row == 0 && e < 2 * g.C) set_param<T>(g, e % 2 ? dgamma : dbeta, e / 2, red[0][col]);
 }
 
 // ------------------------------------------------------------------- host --
