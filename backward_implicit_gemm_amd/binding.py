@@ -428,10 +428,10 @@ def _arg(t, name, dtype, shape, device, fmt=torch.contiguous_format):
 
 def _on(t, name, device):
     """Address of tensor t, which has to be on this device."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's workspace is on {device}")
+    if t.device != device or device.type != "cuda":
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        raise ValueError(f"{name} is on {t.device}, the helper is for {device}")
     return t.data_ptr()
 
 
@@ -446,7 +446,8 @@ def _device(device):
 
 def _raw_stream(stream, device):
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        # the handle alone: building a Stream object costs as much host time as a launch
+        return torch._C._cuda_getCurrentRawStream(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -610,14 +611,20 @@ class GradClip:
             self._list[i] = gc_tensor(g.data_ptr(), o.data_ptr(), g.numel(), _code(g.dtype))
         if self.device.type != "cuda":
             raise ValueError("the gradients must be device tensors")
+        self._both = self.grads if out is None else self.grads + self.out
+        self._addresses, self._sizes = [t.data_ptr() for t in self._both], [t.numel() for t in self._both]
         self._ws = torch.empty(int(lib().gc_grad_clip_workspace_bytes(len(self.grads))),
                                dtype=torch.uint8, device=self.device)
 
     def _tensors(self):
-        for item, g, o in zip(self._list, self.grads, self.out):
-            if g.numel() != item.n or o.numel() != item.n:
-                raise ValueError("a gradient has changed its size")
-            item.src, item.dst = g.data_ptr(), o.data_ptr()
+        addresses, sizes = [t.data_ptr() for t in self._both], [t.numel() for t in self._both]
+        if sizes != self._sizes:
+            raise ValueError("a gradient has changed its size")
+        if addresses != self._addresses:
+            n = len(self.grads)
+            for item, src, dst in zip(self._list, addresses[:n], addresses[-n:]):
+                item.src, item.dst = src, dst
+            self._addresses = addresses
         return self._list
 
     def norm(self, stream=None):

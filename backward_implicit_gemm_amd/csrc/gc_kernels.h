@@ -135,6 +135,13 @@ template <typename T>
 hipError_t launch_embed_grad_sort(const EmbedGeom &g, const void *tok, const void *dout, void *dtable, float scale,
                                   void *ws, hipStream_t s);
 
+// The gradient as a one-hot matrix product, for small vocabularies
+// (embed_grad_onehot.hip); needs D >= 2 and at least one token.
+size_t embed_grad_onehot_ws_bytes(const EmbedGeom &g);
+template <typename T>
+hipError_t launch_embed_grad_onehot(const EmbedGeom &g, const void *tok, const void *dout, void *dtable, float scale,
+                                    void *ws, hipStream_t s);
+
 // Group norm with an activation.  The split kernels (norm_split.hip) take every
 // shape; plan_norm_split returns false past the largest grid.
 struct NormGeom;

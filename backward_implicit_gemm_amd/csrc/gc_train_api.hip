@@ -49,6 +49,24 @@ int check_embed(const gc_embed_desc *d, EmbedGeom *g)
     return GC_OK;
 }
 
+// The gradient's kernels: a one-hot product costs the same for every row of the
+// table, sorting the tokens the same for any number of rows.
+constexpr int kOnehotRows = 512;
+bool embed_onehot(const EmbedGeom &g) { return g.V <= kOnehotRows && g.D >= 2 && g.n > 0; }
+
+size_t embed_grad_ws_bytes(const EmbedGeom &g)
+{
+    return embed_onehot(g) ? embed_grad_onehot_ws_bytes(g) : embed_grad_sort_ws_bytes(g);
+}
+
+template <typename T>
+hipError_t embed_grad(const EmbedGeom &g, const void *tok, const void *dout, void *dtable, float scale, void *ws,
+                      hipStream_t s)
+{
+    return embed_onehot(g) ? launch_embed_grad_onehot<T>(g, tok, dout, dtable, scale, ws, s)
+                           : launch_embed_grad_sort<T>(g, tok, dout, dtable, scale, ws, s);
+}
+
 uintptr_t token_size(int itype) { return itype == GC_I32 ? 4 : itype == GC_I64 ? 8 : 1; }
 
 // ---------------------------------------------------------------- group norm --
@@ -170,7 +188,7 @@ size_t gc_embed_workspace_bytes(const gc_embed_desc *d, int dtype)
 {
     EmbedGeom g;
     if (check_embed(d, &g) != GC_OK || !valid_dtype(dtype)) return 0;
-    return embed_grad_sort_ws_bytes(g);
+    return embed_grad_ws_bytes(g);
 }
 
 int gc_embed_bwd(const void *tokens, const void *dout, void *dtable, void *workspace, size_t ws_bytes,
@@ -182,12 +200,11 @@ int gc_embed_bwd(const void *tokens, const void *dout, void *dtable, void *works
     if (!valid_dtype(dtype) || !dtable || !aligned_to(dtable, dtype)) return GC_ERR_INVALID_ARG;
     if (g.n && (!tokens || !dout || !aligned(tokens, token_size(d->itype)) || !aligned_to(dout, dtype)))
         return GC_ERR_INVALID_ARG;
-    st = check_workspace(workspace, ws_bytes, embed_grad_sort_ws_bytes(g));
+    st = check_workspace(workspace, ws_bytes, embed_grad_ws_bytes(g));
     if (st != GC_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    return hip_status(dtype == GC_F32
-                          ? launch_embed_grad_sort<float>(g, tokens, dout, dtable, scale, workspace, s)
-                          : launch_embed_grad_sort<bf16_t>(g, tokens, dout, dtable, scale, workspace, s));
+    return hip_status(dtype == GC_F32 ? embed_grad<float>(g, tokens, dout, dtable, scale, workspace, s)
+                                      : embed_grad<bf16_t>(g, tokens, dout, dtable, scale, workspace, s));
 }
 
 size_t gc_group_norm_workspace_bytes(int op, const gc_norm_desc *d, int dtype)

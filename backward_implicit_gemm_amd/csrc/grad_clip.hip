@@ -6,14 +6,16 @@
 // nothing is kept between calls and a captured graph holds its own copy.  Every
 // tensor is cut into chunks of one size; workgroup w of a launch takes chunks
 // w, w + grid, ... and finds a chunk's tensor by bisecting the chunk counts
-// (wave-uniform scalar loads).
+// (wave-uniform scalar loads).  (One run of consecutive chunks a workgroup was
+// slower, 160 against 151 us for 153 MB: neighbouring workgroups then read far apart.)
 //
 // Pass 1 adds up squares in fp64 (the product of two fp32 values is exact there
 // and cannot overflow or vanish; fp64 adds at the vector unit's full rate hide
-// behind the loads) and writes one partial per workgroup.  Pass 2 sums the
-// partials in the same fixed order in every workgroup, so the norm and the result
-// are bit-reproducible, and scales.  Both passes are bound by memory: the
-// gradients are read twice and written once.
+// behind the loads: fp32 squares time the same) and writes one partial per workgroup.
+// Pass 2 sums the partials in the same fixed order in every workgroup, so the norm
+// and the result are bit-reproducible, and scales, from the last chunk to the
+// first, as the last ones read are still in cache.  Both passes are bound by memory:
+// the gradients are read twice and written once.
 #include "gc_kernels.h"
 #include "gc_vec.h"
 
@@ -22,6 +24,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxGrid = 1024;     // workgroups of a launch: 4 per CU
+constexpr int kUnroll = 4;           // vectors a thread has in flight
+constexpr int kChunk = 8192;         // elements of a chunk
 constexpr int kFold = 2048;        // more partials than this are folded by a launch of their own
 
 struct ClipArgs {
@@ -47,54 +51,96 @@ __device__ __forceinline__ int tensor_of(const ClipArgs &a, int c)
     return lo;
 }
 
-template <typename T>
-__device__ __forceinline__ double chunk_squares(const T *p, int len)
+template <int K>
+__device__ __forceinline__ double sum_of(const double (&s)[K])
 {
-    constexpr int V = kVec<T>;
-    double s = 0;
-    const int whole = len / V;
-    for (int i = threadIdx.x; i < whole; i += kThreads) {
-        const Vec<T, V> v = load_vec<T, V>(p + size_t(i) * V);
+    double v = s[0];
 #pragma unroll
-        for (int j = 0; j < V; ++j) s = fma(double(v.get(j)), double(v.get(j)), s);
-    }
-    const int e = whole * V + threadIdx.x;
-    if (e < len) s = fma(double(to_f32(p[e])), double(to_f32(p[e])), s);
-    return s;
+    for (int k = 1; k < K; ++k) v += s[k];
+    return v;
 }
 
+// A thread takes kUnroll vectors at a time, kThreads vectors apart.
 template <typename T>
-__device__ __forceinline__ void chunk_scale(const T *p, T *q, int len, float c)
+__device__ __forceinline__ double squares(const T *p, int len)
 {
     constexpr int V = kVec<T>;
     const int whole = len / V;
-    for (int i = threadIdx.x; i < whole; i += kThreads) {
-        const Vec<T, V> v = load_vec<T, V>(p + size_t(i) * V);
-        float f[V];
+    double s[kUnroll] = {};
+    int i = threadIdx.x;
+    for (; i + (kUnroll - 1) * kThreads < whole; i += kUnroll * kThreads) {
+        Vec<T, V> v[kUnroll];
 #pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = c * v.get(j);
-        Vec<T, V> o;
-        o.put(f);
-        store_vec<T, V>(q + size_t(i) * V, o);
+        for (int u = 0; u < kUnroll; ++u) v[u] = load_vec<T, V>(p + (i + u * kThreads) * V);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[u] = fma(double(v[u].get(j)), double(v[u].get(j)), s[u]);
     }
+    for (; i < whole; i += kThreads) {
+        const Vec<T, V> v = load_vec<T, V>(p + i * V);
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[0] = fma(double(v.get(j)), double(v.get(j)), s[0]);
+    }
+    const int e = whole * V + threadIdx.x;
+    if (e < len) s[0] = fma(double(to_f32(p[e])), double(to_f32(p[e])), s[0]);
+    return sum_of(s);
+}
+
+template <bool PAST, typename T>
+__device__ __forceinline__ void scale_vec(T *q, const Vec<T, kVec<T>> &v, float c)
+{
+    constexpr int V = kVec<T>;
+    float f[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = c * v.get(j);
+    Vec<T, V> o;
+    o.put(f);
+    put_vec<PAST>(q, o);
+}
+
+template <bool PAST, typename T>
+__device__ __forceinline__ void scale(const T *p, T *q, int len, float c)
+{
+    constexpr int V = kVec<T>;
+    const int whole = len / V;
+    int i = threadIdx.x;
+    for (; i + (kUnroll - 1) * kThreads < whole; i += kUnroll * kThreads) {
+        Vec<T, V> v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) v[u] = load_vec<T, V>(p + (i + u * kThreads) * V);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) scale_vec<PAST>(q + (i + u * kThreads) * V, v[u], c);
+    }
+    for (; i < whole; i += kThreads) scale_vec<PAST>(q + i * V, load_vec<T, V>(p + i * V), c);
     const int e = whole * V + threadIdx.x;
     if (e < len) q[e] = from_f32<T>(c * to_f32(p[e]));
 }
 
+// Calls f(t, at, len) for this workgroup's chunks: blockIdx.x, + gridDim.x, ...,
+// counted from the last one when BACK.
+template <bool BACK, typename F>
+__device__ __forceinline__ void for_chunks(const ClipArgs &a, F f)
+{
+    const int chunks = a.first[a.count];
+    for (int k = blockIdx.x; k < chunks; k += gridDim.x) {
+        const int c = BACK ? chunks - 1 - k : k;
+        const int t = tensor_of(a, c);
+        const int64_t at = int64_t(c - a.first[t]) * a.chunk;
+        f(t, at, int(min(int64_t(a.chunk), a.n[t] - at)));
+    }
+}
+
+__device__ __forceinline__ bool is_bf16(const ClipArgs &a, int t) { return a.bf16[t >> 5] >> (t & 31) & 1; }
+
 __global__ void __launch_bounds__(kThreads) clip_squares(const ClipArgs a, double *__restrict__ part)
 {
     __shared__ double red[16];
-    const int chunks = a.first[a.count];
     double s = 0;
-    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const int t = tensor_of(a, c);
-        const int64_t at = int64_t(c - a.first[t]) * a.chunk;
-        const int len = int(min(int64_t(a.chunk), a.n[t] - at));
-        if (a.bf16[t >> 5] >> (t & 31) & 1)
-            s += chunk_squares(static_cast<const bf16_t *>(a.src[t]) + at, len);
-        else
-            s += chunk_squares(static_cast<const float *>(a.src[t]) + at, len);
-    }
+    for_chunks<false>(a, [&](int t, int64_t at, int len) {
+        if (is_bf16(a, t)) s += squares(static_cast<const bf16_t *>(a.src[t]) + at, len);
+        else s += squares(static_cast<const float *>(a.src[t]) + at, len);
+    });
     s = block_sum(s, red);
     if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
@@ -123,6 +169,7 @@ __global__ void __launch_bounds__(kThreads) clip_norm(const double *__restrict__
     if (threadIdx.x == 0) *norm = float(fabs(double(prescale)) * sqrt(s));
 }
 
+template <bool PAST>
 __global__ void __launch_bounds__(kThreads) clip_scale(const ClipArgs a, const double *__restrict__ part,
                                                        int np, float max_norm, float prescale, float eps,
                                                        float *__restrict__ norm)
@@ -133,33 +180,28 @@ __global__ void __launch_bounds__(kThreads) clip_scale(const ClipArgs a, const d
     // a NaN norm (or an infinite one against an infinite max_norm) stays NaN
     const double r = double(max_norm) / (total + double(eps));
     const float c = float(double(prescale) * (r >= 1.0 ? 1.0 : r));
-    const int chunks = a.first[a.count];
-    for (int k = blockIdx.x; k < chunks; k += gridDim.x) {
-        const int t = tensor_of(a, k);
-        if (c == 1.f && a.src[t] == a.dst[t]) continue;   // in place, and nothing changes
-        const int64_t at = int64_t(k - a.first[t]) * a.chunk;
-        const int len = int(min(int64_t(a.chunk), a.n[t] - at));
-        if (a.bf16[t >> 5] >> (t & 31) & 1)
-            chunk_scale(static_cast<const bf16_t *>(a.src[t]) + at, static_cast<bf16_t *>(a.dst[t]) + at,
-                        len, c);
+    for_chunks<true>(a, [&](int t, int64_t at, int len) {
+        if (c == 1.f && a.src[t] == a.dst[t]) return;   // in place, and nothing changes
+        if (is_bf16(a, t))
+            scale<PAST>(static_cast<const bf16_t *>(a.src[t]) + at, static_cast<bf16_t *>(a.dst[t]) + at, len, c);
         else
-            chunk_scale(static_cast<const float *>(a.src[t]) + at, static_cast<float *>(a.dst[t]) + at,
-                        len, c);
-    }
+            scale<PAST>(static_cast<const float *>(a.src[t]) + at, static_cast<float *>(a.dst[t]) + at, len, c);
+    });
 }
 
 int launches(int count) { return (count + kClipTensors - 1) / kClipTensors; }
 
-// Chunk size of a list of `total` elements: about four chunks for each of
-// kMaxGrid workgroups, within 4096 .. 65536 elements.
+// Chunk size of a list of `total` elements: kChunk, more only where a launch's
+// chunk numbers would not stay within 30 bits.
 int chunk_of(int64_t total)
 {
-    const int64_t c = (total / (4 * kMaxGrid) + 4095) / 4096 * 4096;
-    return int(c < 4096 ? 4096 : c > 65536 ? 65536 : c);
+    int64_t c = kChunk;
+    while (total / c > (int64_t(1) << 29)) c *= 2;
+    return int(c);
 }
 
-// Arguments of launch l (tensors l*kClipTensors ...); returns its grid, or 0
-// for tensors without elements, or -1 if the chunks pass 2^31.
+// Arguments of launch l (tensors l*kClipTensors ...); returns its grid, 0
+// for tensors without elements.
 int fill_args(const gc_tensor *list, int count, int l, int chunk, ClipArgs &a)
 {
     const int t0 = l * kClipTensors;
@@ -175,7 +217,6 @@ int fill_args(const gc_tensor *list, int count, int l, int chunk, ClipArgs &a)
         a.first[t] = int(chunks);
         if (x.dtype == GC_BF16) a.bf16[t >> 5] |= 1u << (t & 31);
         chunks += (x.n + chunk - 1) / chunk;
-        if (chunks > 0x7FFFFFFF) return -1;
     }
     a.first[a.count] = int(chunks);
     return int(chunks < kMaxGrid ? chunks : kMaxGrid);
@@ -193,13 +234,15 @@ hipError_t launch_grad_clip(const gc_tensor *list, int count, float max_norm, fl
                             bool scale, float *norm, void *ws, hipStream_t s)
 {
     double *part = static_cast<double *>(ws);
-    int64_t total = 0;
-    for (int t = 0; t < count; ++t) total += list[t].n;
+    int64_t total = 0, bytes = 0;
+    for (int t = 0; t < count; ++t) {
+        total += list[t].n;
+        bytes += 2 * list[t].n * (list[t].dtype == GC_F32 ? 4 : 2);
+    }
     const int chunk = chunk_of(total);
     const int nl = launches(count);
     ClipArgs a;
-    for (int l = 0; l < nl; ++l)           // before anything is enqueued
-        if (fill_args(list, count, l, chunk, a) < 0) return hipErrorInvalidValue;
+    const bool past = bytes >= int64_t(kStreamBytes);
     int np = 0;
     for (int l = 0; l < nl; ++l) {
         const int grid = fill_args(list, count, l, chunk, a);
@@ -222,8 +265,8 @@ hipError_t launch_grad_clip(const gc_tensor *list, int count, float max_norm, fl
     for (int l = 0; l < nl; ++l) {
         const int grid = fill_args(list, count, l, chunk, a);
         if (!grid) continue;
-        hipLaunchKernelGGL(clip_scale, dim3(grid), dim3(kThreads), 0, s, a, part, np, max_norm, prescale,
-                           eps, norm);
+        hipLaunchKernelGGL((past ? clip_scale<true> : clip_scale<false>), dim3(grid), dim3(kThreads), 0, s, a,
+                           part, np, max_norm, prescale, eps, norm);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
     return hipSuccess;

@@ -63,6 +63,10 @@ CASES = [
     (2, 3, 255, 5, "uniform", torch.int32, 0),
     (2, 300, 256, 16, "skewed", torch.int32, 0),        # keys 0 .. 256 need a second sorting pass
     (1200, 64, 257, 48, "skewed", torch.int32, 0),
+    (77, 13, 500, 70, "uniform", torch.int64, 5),       # several blocks of rows and columns of the one-hot product
+    (77, 13, 512, 2, "skewed", torch.int64, 0),
+    (40, 300, 33, 31, "uniform", torch.int32, 1),
+    (40, 300, 128, 1, "uniform", torch.int32, 1),
 ]
 
 
@@ -111,6 +115,37 @@ def test_no_tokens():
         e.fwd(tok, table, out)
         e.bwd(tok, out, table)
         assert bool((table == 0).all())
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("V,D", [(100, 40), (300, 33), (4000, 24)])
+def test_non_finite_gradients_stay_in_their_place(V, D, dtype):
+    """A NaN or an infinity of dout reaches its token's row and its column alone, and none from an empty token."""
+    t = TYPES[dtype]
+    gen = torch.Generator("cuda").manual_seed(10)
+    rows, T = 60, 31
+    tok = torch.randint(0, V, (rows, T), generator=gen, device="cuda", dtype=torch.int32)
+    dout = torch.randn((rows, T, D), generator=gen, device="cuda").to(t)
+    tok[7, 3] = tok[20, 1] = -1
+    dout[7, 3] = float("nan")
+    dout[20, 1] = float("inf")
+    clean = dout.clone()
+    clean[7, 3] = clean[20, 1] = 0
+    tok[50, 2], tok[9, 9], tok[9, 10] = 5, 6, 6
+    dout[50, 2, 4] = float("nan")
+    dout[9, 9, D - 1] = float("inf")
+    dout[9, 10, 1] = -float("inf")
+    clean[50, 2, 4] = clean[9, 9, D - 1] = clean[9, 10, 1] = 0
+    e = gb.Embedding(rows, T, V, D, t)
+    dtable = torch.empty((V, D), dtype=t, device="cuda")
+    e.bwd(tok, dout, dtable)
+    want, size, m = ref.embed_bwd(tok.long(), clean, V, 1.0)
+    assert bool(torch.isnan(dtable[5, 4])) and float(dtable[6, D - 1]) == float("inf")
+    assert float(dtable[6, 1]) == -float("inf")
+    for r, c in ((5, 4), (6, D - 1), (6, 1)):
+        dtable[r, c] = want[r, c] = 0
+    bound = (m[:, None] + 2) * ref.U * size
+    assert ref.over(dtable, want, bound + ref.half(t) * (want.abs() + bound)) <= 1
 
 
 def test_adjoint():
