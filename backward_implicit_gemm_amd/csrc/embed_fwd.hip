@@ -19,9 +19,9 @@ namespace gc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 2;
 
-template <typename T, int N>
+template <typename T, int N, bool PAST>
 __global__ void __launch_bounds__(kThreads) embed_rows(EmbedGeom g, const void *__restrict__ tok,
                                                        const T *__restrict__ table, T *__restrict__ out,
                                                        float scale, FastDiv fd_vec, int rows_wg)
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) embed_rows(EmbedGeom g, const void *
             }
             Vec<T, N> o;
             o.put(f);
-            store_vec<T, N>(out + g.row(k[u]) + at[u], o);
+            put_vec<PAST>(out + g.row(k[u]) + at[u], o);
         }
     }
 }
@@ -73,8 +73,9 @@ hipError_t launch(const EmbedGeom &g, const void *tok, const void *table, void *
     const int per_row = (g.D + N - 1) / N;
     const int rows_wg = std::max(1, kThreads * kUnroll / per_row);
     const unsigned grid = unsigned((int64_t(g.n) + rows_wg - 1) / rows_wg);
-    hipLaunchKernelGGL((embed_rows<T, N>), dim3(grid), dim3(kThreads), 0, s, g, tok, (const T *)table, (T *)out,
-                       scale, make_fastdiv(per_row), rows_wg);
+    const bool past = size_t(g.n) * g.D * sizeof(T) >= kStreamBytes;
+    hipLaunchKernelGGL((past ? embed_rows<T, N, true> : embed_rows<T, N, false>), dim3(grid), dim3(kThreads), 0, s, g,
+                       tok, (const T *)table, (T *)out, scale, make_fastdiv(per_row), rows_wg);
     return hipGetLastError();
 }
 

@@ -7,12 +7,14 @@
 //      per tile, (for many tiles a scan of the counts over the tiles,) then
 //      each tile ranks its keys and scatters them.  Tokens outside [0, V)
 //      carry the key V and end up behind all rows.
-//   2. Long runs of one token: every 64 sorted positions that hold one token
-//      are summed into a partial row, and every 64 partials of one token into a
-//      second-level partial, all tiles in parallel.  Other tiles cost nothing.
-//   3. Each row of the table bisects the sorted keys for its run and adds up:
-//      positions to the first tile boundary, partials, second-level partials,
-//      partials, positions.  Rows without a token are written as zeros.
+//   2. Long runs of one token: every kRun sorted positions that hold one token
+//      are summed into a partial row, and likewise every kRun partials of a level into
+//      one of the next, all tiles in parallel.  Other tiles cost nothing.  The
+//      first launch also notes where each token's run begins and ends.
+//   3. Each row of the table adds up its run: positions to the first tile
+//      boundary, partials to the first boundary of the next level, and so on up and
+//      down again.  Rows without a token are written as zeros; they are known by
+//      their noted place not being a run of theirs, so the notes need no clearing.
 // Bound by memory: dout is gathered once by rows, dtable written once; at few
 // tokens by the chain of launches.
 #include <algorithm>
@@ -25,9 +27,10 @@ namespace gc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRun = 64;             // sorted positions of a partial, and partials of a second-level one
-constexpr int kScanTiles = 16;       // more tiles than this are scanned by a launch of their own
-constexpr uint32_t kTwoLevels = 4 * kRun * kRun;   // tokens from which second-level partials are made
+constexpr int kRun = 32;             // sorted positions of a partial, and partials of one of the next level
+constexpr int kLevels = 3;           // partials of 32, 1024 and 32,768 positions
+constexpr int kScanTiles = 32;       // more tiles than this are scanned by a launch of their own
+constexpr int kInFlight = 8;         // rows a thread has requested at once
 
 // ---------------------------------------------------------------- sorting --
 // Key of position i: pass 0 reads the caller's tokens, later passes the
@@ -141,10 +144,11 @@ __global__ void __launch_bounds__(kThreads) sort_scatter(EmbedGeom g, SortIn in,
         total = totals[t];
         prefix = counts[size_t(blockIdx.x) * 256 + t];
     } else {
+#pragma unroll 8
         for (int i = 0; i < tiles; ++i) {
             const uint32_t c = counts[size_t(i) * 256 + t];
             total += c;
-            if (i < int(blockIdx.x)) prefix += c;
+            prefix += i < int(blockIdx.x) ? c : 0;
         }
     }
     scan[t] = total;
@@ -181,18 +185,18 @@ __device__ __forceinline__ void add_vec(float (&s)[N], const Vec<T, N> &v)
     for (int j = 0; j < N; ++j) s[j] += v.get(j);
 }
 
-// s += rows idx[a .. b) of dout at column c, in order, four rows in flight
+// s += rows idx[a .. b) of dout at column c, in order
 template <typename T, int N>
 __device__ __forceinline__ void add_positions(const EmbedGeom &g, const T *__restrict__ dout,
                                               const uint32_t *__restrict__ idx, uint32_t a, uint32_t b, int c,
                                               float (&s)[N])
 {
-    for (; a + 4 <= b; a += 4) {
-        Vec<T, N> v[4];
+    for (; a + kInFlight <= b; a += kInFlight) {
+        Vec<T, N> v[kInFlight];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = load_vec<T, N>(dout + g.row(idx[a + u]) + c);
+        for (int u = 0; u < kInFlight; ++u) v[u] = load_vec<T, N>(dout + g.row(idx[a + u]) + c);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) add_vec(s, v[u]);
+        for (int u = 0; u < kInFlight; ++u) add_vec(s, v[u]);
     }
     for (; a < b; ++a) add_vec(s, load_vec<T, N>(dout + g.row(idx[a]) + c));
 }
@@ -202,31 +206,46 @@ template <int N>
 __device__ __forceinline__ void add_partials(const float *__restrict__ part, int D, uint32_t a, uint32_t b, int c,
                                              float (&s)[N])
 {
-    for (; a + 4 <= b; a += 4) {
-        Vec<float, N> v[4];
+    for (; a + kInFlight <= b; a += kInFlight) {
+        Vec<float, N> v[kInFlight];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = load_vec<float, N>(part + size_t(a + u) * D + c);
+        for (int u = 0; u < kInFlight; ++u) v[u] = load_vec<float, N>(part + size_t(a + u) * D + c);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) add_vec(s, v[u]);
+        for (int u = 0; u < kInFlight; ++u) add_vec(s, v[u]);
     }
     for (; a < b; ++a) add_vec(s, load_vec<float, N>(part + size_t(a) * D + c));
 }
 
-// Partial p: the sum over sorted positions [p*kRun, (p+1)*kRun) if they all hold
-// one token; else nothing is written (and nothing reads it).
+// The partials of each level: row t of level l sums the kRun^(l+1) sorted positions
+// from t * kRun^(l+1) on, and is there if those hold one token of the table.
+struct Partials {
+    float *part[kLevels];
+    uint32_t rows[kLevels];
+    int levels;
+};
+
+// Level 0, and the runs' ends.
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads) run_partials(EmbedGeom g, const T *__restrict__ dout,
                                                          const uint32_t *__restrict__ key,
-                                                         const uint32_t *__restrict__ idx,
-                                                         float *__restrict__ part, uint32_t parts, int team)
+                                                         const uint32_t *__restrict__ idx, float *__restrict__ part,
+                                                         uint32_t *__restrict__ first, uint32_t *__restrict__ last,
+                                                         int team)
 {
     const uint32_t p = blockIdx.x * (kThreads / team) + threadIdx.x / team;
-    if (p >= parts) return;
     const uint32_t a = p * kRun;
+    const int lane = threadIdx.x % team;
+    for (uint32_t i = a + lane; i < min(a + kRun, g.n); i += team) {
+        const uint32_t k = key[i];
+        if (k >= uint32_t(g.V)) continue;
+        if (i == 0 || key[i - 1] != k) first[k] = i;
+        if (i + 1 == g.n || key[i + 1] != k) last[k] = i;
+    }
+    if (a + kRun > g.n) return;
     const uint32_t k = key[a];
     if (k != key[a + kRun - 1] || k >= uint32_t(g.V)) return;
     const int nvec = (g.D + N - 1) / N;
-    for (int i = threadIdx.x % team; i < nvec; i += team) {
+    for (int i = lane; i < nvec; i += team) {
         const int c = min(i * N, g.D - N);
         float s[N] = {};
         add_positions<T, N>(g, dout, idx, a, a + kRun, c, s);
@@ -236,83 +255,88 @@ __global__ void __launch_bounds__(kThreads) run_partials(EmbedGeom g, const T *_
     }
 }
 
-// Second-level partial q: partials [q*kRun, (q+1)*kRun) where they are all of one token.
+// A level from the one below; `span` positions a row.
 template <int N>
-__global__ void __launch_bounds__(kThreads) run_partials2(int V, int D, const uint32_t *__restrict__ key,
-                                                          const float *__restrict__ part,
-                                                          float *__restrict__ part2, uint32_t parts2, int team)
+__global__ void __launch_bounds__(kThreads) next_partials(int V, int D, const uint32_t *__restrict__ key,
+                                                          const float *__restrict__ below,
+                                                          float *__restrict__ part, uint32_t rows, uint32_t span,
+                                                          int team)
 {
     const uint32_t q = blockIdx.x * (kThreads / team) + threadIdx.x / team;
-    if (q >= parts2) return;
-    const uint32_t a = q * (kRun * kRun);
-    const uint32_t k = key[a];
-    if (k != key[a + kRun * kRun - 1] || k >= uint32_t(V)) return;
+    if (q >= rows) return;
+    const uint32_t k = key[q * span];
+    if (k != key[q * span + span - 1] || k >= uint32_t(V)) return;
     const int nvec = (D + N - 1) / N;
     for (int i = threadIdx.x % team; i < nvec; i += team) {
         const int c = min(i * N, D - N);
         float s[N] = {};
-        add_partials<N>(part, D, q * kRun, (q + 1) * kRun, c, s);
+        add_partials<N>(below, D, q * kRun, (q + 1) * kRun, c, s);
         Vec<float, N> o;
         o.put(s);
-        store_vec<float, N>(part2 + size_t(q) * D + c, o);
+        store_vec<float, N>(part + size_t(q) * D + c, o);
     }
-}
-
-// first sorted position whose key is at least v
-__device__ __forceinline__ uint32_t lower_bound(const uint32_t *__restrict__ key, uint32_t n, uint32_t v)
-{
-    uint32_t lo = 0, hi = n;
-    while (lo < hi) {
-        const uint32_t mid = lo + ((hi - lo) >> 1);
-        if (key[mid] < v) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo;
 }
 
 constexpr int kRowsMax = 256;   // table rows of a workgroup, at most
 
-template <typename T, int N>
+// Workgroup w takes rows w, w + grid, ...: frequent tokens often are neighbours.
+template <typename T, int N, bool PAST>
 __global__ void __launch_bounds__(kThreads) table_rows(EmbedGeom g, const T *__restrict__ dout,
                                                        const uint32_t *__restrict__ key,
-                                                       const uint32_t *__restrict__ idx,
-                                                       const float *__restrict__ part,
-                                                       const float *__restrict__ part2,
-                                                       T *__restrict__ dtable, float scale, int team, int rows_wg)
+                                                       const uint32_t *__restrict__ idx, Partials q,
+                                                       const uint32_t *__restrict__ first,
+                                                       const uint32_t *__restrict__ last, T *__restrict__ dtable,
+                                                       float scale, int team, int rows_wg)
 {
-    __shared__ uint32_t start[kRowsMax + 1];
-    const int v0 = blockIdx.x * rows_wg;
-    const int rows = min(rows_wg, g.V - v0);
-    for (int i = threadIdx.x; i <= rows; i += kThreads) start[i] = lower_bound(key, g.n, uint32_t(v0 + i));
+    __shared__ uint32_t begin[kRowsMax], end[kRowsMax];
+    for (int r = threadIdx.x; r < rows_wg; r += kThreads) {
+        const int64_t v = blockIdx.x + int64_t(r) * gridDim.x;
+        uint32_t a = 0, b = 0;
+        if (v < g.V) {
+            const uint32_t i = first[v], j = last[v];
+            if (i < g.n && key[i] == uint32_t(v) && (i == 0 || key[i - 1] != uint32_t(v))) {
+                a = i;
+                b = j + 1;
+            }
+        }
+        begin[r] = a;
+        end[r] = b;
+    }
     __syncthreads();
     const int nvec = (g.D + N - 1) / N;
     const int lane = threadIdx.x % team, teams = kThreads / team;
-    for (int r = threadIdx.x / team; r < rows; r += teams) {
-        const uint32_t a = start[r], b = start[r + 1];
-        // whole tiles [ta, tb) and whole second-level tiles [qa, qb) of the run
-        const uint32_t ta = (a + kRun - 1) / kRun, tb = b / kRun;
-        const uint32_t qa = (ta + kRun - 1) / kRun, qb = tb / kRun;
+    for (int r = threadIdx.x / team; r < rows_wg; r += teams) {
+        const int64_t v = blockIdx.x + int64_t(r) * gridDim.x;
+        if (v >= g.V) break;
+        const uint32_t a = begin[r], b = end[r];
         for (int i = lane; i < nvec; i += team) {
             const int c = min(i * N, g.D - N);
             float s[N] = {};
-            if (ta < tb) {
-                add_positions<T, N>(g, dout, idx, a, ta * kRun, c, s);
-                if (part2 && qa < qb) {
-                    add_partials<N>(part, g.D, ta, qa * kRun, c, s);
-                    add_partials<N>(part2, g.D, qa, qb, c, s);
-                    add_partials<N>(part, g.D, qb * kRun, tb, c, s);
-                } else {
-                    add_partials<N>(part, g.D, ta, tb, c, s);
-                }
-                add_positions<T, N>(g, dout, idx, tb * kRun, b, c, s);
-            } else {
-                add_positions<T, N>(g, dout, idx, a, b, c, s);
+            // up: [at, b) is left in units of level `up`; down: the rest of each level
+            uint32_t from[kLevels + 1], to[kLevels + 1];
+            uint32_t x = a, y = b;
+            int up = 0;
+            for (; up < q.levels; ++up) {
+                const uint32_t u = (x + kRun - 1) / kRun, w = y / kRun;
+                if (u >= w) break;
+                if (up == 0) add_positions<T, N>(g, dout, idx, x, u * kRun, c, s);
+                else add_partials<N>(q.part[up - 1], g.D, x, u * kRun, c, s);
+                from[up] = w * kRun;
+                to[up] = y;
+                x = u;
+                y = w;
+            }
+            from[up] = x;
+            to[up] = y;
+            for (; up >= 0; --up) {
+                if (up == 0) add_positions<T, N>(g, dout, idx, from[0], to[0], c, s);
+                else add_partials<N>(q.part[up - 1], g.D, from[up], to[up], c, s);
             }
 #pragma unroll
             for (int j = 0; j < N; ++j) s[j] = a < b ? scale * s[j] : 0.f;
             Vec<T, N> o;
             o.put(s);
-            store_vec<T, N>(dtable + size_t(v0 + r) * g.D + c, o);
+            put_vec<PAST>(dtable + v * g.D + c, o);
         }
     }
 }
@@ -321,8 +345,9 @@ __global__ void __launch_bounds__(kThreads) table_rows(EmbedGeom g, const T *__r
 struct SortPlan {
     int rounds;          // 64-key rounds of a wave: the tile is 256 * rounds keys
     int tiles, passes;
-    uint32_t parts, parts2;
-    size_t key[2], idx[2], counts, totals, part, part2, bytes;   // byte offsets
+    int levels;
+    uint32_t rows[kLevels];                                    // partials of each level
+    size_t key[2], idx[2], counts, totals, first, last, part[kLevels], bytes;   // byte offsets
 };
 
 size_t take(size_t &at, size_t bytes)
@@ -341,8 +366,9 @@ SortPlan plan(const EmbedGeom &g)
     int bits = 1;
     while ((uint64_t(1) << bits) <= uint64_t(g.V)) ++bits;   // keys 0 .. V
     p.passes = (bits + 7) / 8;
-    p.parts = g.n / kRun;
-    p.parts2 = g.n >= kTwoLevels ? g.n / (kRun * kRun) : 0;
+    // a level pays from a few rows on
+    uint32_t rows = g.n / kRun;
+    for (; p.levels < kLevels && rows >= (p.levels ? 4u : 1u); rows /= kRun) p.rows[p.levels++] = rows;
     size_t at = 0;
     for (int i = 0; i < 2; ++i) {
         p.key[i] = take(at, size_t(g.n) * 4);
@@ -350,8 +376,9 @@ SortPlan plan(const EmbedGeom &g)
     }
     p.counts = take(at, size_t(p.tiles) * 256 * 4);
     p.totals = take(at, 256 * 4);
-    p.part = take(at, size_t(p.parts) * g.D * 4);
-    p.part2 = take(at, size_t(p.parts2) * g.D * 4);
+    p.first = take(at, size_t(g.V) * 4);
+    p.last = take(at, size_t(g.V) * 4);
+    for (int l = 0; l < p.levels; ++l) p.part[l] = take(at, size_t(p.rows[l]) * g.D * 4);
     p.bytes = at;
     return p;
 }
@@ -374,25 +401,37 @@ hipError_t sort_pass(const EmbedGeom &g, const SortPlan &p, const SortIn &in, in
 
 template <typename T, int N>
 hipError_t sums(const EmbedGeom &g, const SortPlan &p, const void *dout, const uint32_t *key, const uint32_t *idx,
-                float *part, float *part2, void *dtable, float scale, hipStream_t s)
+                char *ws, void *dtable, float scale, hipStream_t s)
 {
     const int nvec = (g.D + N - 1) / N;
     int team = 1;
     while (team < nvec && team < kThreads) team <<= 1;
     const int teams = kThreads / team;
-    if (p.parts) {
-        hipLaunchKernelGGL((run_partials<T, N>), dim3((p.parts + teams - 1) / teams), dim3(kThreads), 0, s, g,
-                           (const T *)dout, key, idx, part, p.parts, team);
+    uint32_t *first = reinterpret_cast<uint32_t *>(ws + p.first), *last = reinterpret_cast<uint32_t *>(ws + p.last);
+    Partials q{};
+    q.levels = p.levels;
+    for (int l = 0; l < p.levels; ++l) {
+        q.part[l] = reinterpret_cast<float *>(ws + p.part[l]);
+        q.rows[l] = p.rows[l];
+    }
+    if (g.n) {
+        const uint32_t tiles = (g.n + kRun - 1) / kRun;
+        hipLaunchKernelGGL((run_partials<T, N>), dim3((tiles + teams - 1) / teams), dim3(kThreads), 0, s, g,
+                           (const T *)dout, key, idx, q.part[0], first, last, team);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
-    if (p.parts2) {
-        hipLaunchKernelGGL(run_partials2<N>, dim3((p.parts2 + teams - 1) / teams), dim3(kThreads), 0, s, g.V, g.D,
-                           key, part, part2, p.parts2, team);
+    uint32_t span = kRun;
+    for (int l = 1; l < p.levels; ++l) {
+        span *= kRun;
+        hipLaunchKernelGGL(next_partials<N>, dim3((p.rows[l] + teams - 1) / teams), dim3(kThreads), 0, s, g.V, g.D,
+                           key, q.part[l - 1], q.part[l], p.rows[l], span, team);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
     const int rows_wg = std::min(kRowsMax, teams * 8);
-    hipLaunchKernelGGL((table_rows<T, N>), dim3((g.V + rows_wg - 1) / rows_wg), dim3(kThreads), 0, s, g,
-                       (const T *)dout, key, idx, part, p.parts2 ? part2 : nullptr, (T *)dtable, scale, team, rows_wg);
+    const bool past = (size_t(g.n) + g.V) * g.D * sizeof(T) >= kStreamBytes;
+    hipLaunchKernelGGL((past ? table_rows<T, N, true> : table_rows<T, N, false>), dim3((g.V + rows_wg - 1) / rows_wg),
+                       dim3(kThreads), 0, s, g, (const T *)dout, key, idx, q, first, last, (T *)dtable, scale, team,
+                       rows_wg);
     return hipGetLastError();
 }
 
@@ -423,10 +462,8 @@ hipError_t launch_embed_grad_sort(const EmbedGeom &g, const void *tok, const voi
         in = SortIn{tok, key[out], idx[out]};
         out ^= 1;
     }
-    float *part = reinterpret_cast<float *>(base + p.part), *part2 = reinterpret_cast<float *>(base + p.part2);
-    if (g.D >= kVec<T>)
-        return sums<T, kVec<T>>(g, p, dout, in.key, in.idx, part, part2, dtable, scale, s);
-    return sums<T, 1>(g, p, dout, in.key, in.idx, part, part2, dtable, scale, s);
+    if (g.D >= kVec<T>) return sums<T, kVec<T>>(g, p, dout, in.key, in.idx, base, dtable, scale, s);
+    return sums<T, 1>(g, p, dout, in.key, in.idx, base, dtable, scale, s);
 }
 
 template hipError_t launch_embed_grad_sort<float>(const EmbedGeom &, const void *, const void *, void *, float,

@@ -149,6 +149,7 @@ struct NormSplitPlan {
     int N;                     // elements of a thread's vector
     int cols, blocks, slots;   // channels last: vectors of a workgroup's row, column blocks, rows at a time
     int chunks, len;           // pieces an image's positions are cut into, and their length
+    int past_fwd, past_bwd;    // the output goes past the cache
     int64_t grid;
     size_t part_bytes_fwd, part_bytes_bwd, ws_fwd, ws_bwd;
 };
@@ -167,6 +168,7 @@ struct NormResPlan {
     int L, teams, threads; // threads of a team, teams of a workgroup, threads of a workgroup
     int two;               // NCHW: vectors may straddle two channels
     int wave;              // channels last: a team is one wave
+    int past;              // the output goes past the cache
     int P;                 // lanes that add up one group (channels last) or channel (NCHW)
     int slots, CW, slabs, Gs;   // channels last: rows at a time; channels, number and groups of a slab
     int width, team_lds;   // channels last: LDS entries of a row, LDS words of a team

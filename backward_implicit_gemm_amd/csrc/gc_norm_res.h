@@ -3,6 +3,8 @@
 // statistics and their output, so every input is read once.
 #pragma once
 
+#include <type_traits>
+
 #include "gc_kernels.h"
 #include "gc_norm.h"
 
@@ -102,6 +104,16 @@ hipError_t with_nv(int nv, F f)
         return hipErrorInvalidValue;
     default: return hipErrorInvalidValue;
     }
+}
+
+// Calls f(PAST) with whether the output goes past the cache, where a vector is long
+// enough for that.
+template <bool CAN, typename F>
+hipError_t with_past(bool past, F f)
+{
+    if constexpr (CAN)
+        if (past) return f(std::true_type());
+    return f(std::false_type());
 }
 
 // Calls f(N) with the plan's vector length; 8 elements only in bf16.

@@ -63,13 +63,14 @@ __device__ __forceinline__ void store_vec(T *p, const Vec<T, N> &v)
     __builtin_memcpy(p, v.w, sizeof(T) * N);
 }
 
-// A store of bytes that will not be in cache when they are read next: a call
-// that moves kStreamBytes, half of the 256 MB last-level cache, and more writes its
-// output past it (PAST, a compile-time choice: as a branch the compiler merges both
-// stores into the plain one), so that dirty lines do not push out what the call
-// still reads (clipping 153 MB of gradients: 151 us with plain stores, 121 us past
-// the cache).  Smaller outputs stay cached for their reader.
-constexpr size_t kStreamBytes = size_t(128) << 20;
+// A store past the cache (PAST), for calls that move kStreamBytes and more: their
+// outputs leave the cache before they are read again, and as dirty lines they
+// push out what the call still reads and are written back in the way of later calls.
+// Clipping 153 MB of gradients took 151 us with plain stores and 121 us past the
+// cache, an embedding of 98 MB 32 and 16 us.  Smaller outputs stay cached for
+// their reader.  A compile-time choice: of two stores at the ends of a branch the
+// compiler makes one plain one.
+constexpr size_t kStreamBytes = size_t(64) << 20;
 
 template <bool PAST, typename T, int N>
 __device__ __forceinline__ void put_vec(T *p, const Vec<T, N> &v)

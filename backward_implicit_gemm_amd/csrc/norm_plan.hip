@@ -142,6 +142,7 @@ bool search(const NormGeom &g, int dtype, bool bwd, NormResPlan &q)
 {
     const int size = dtype == GC_F32 ? 4 : 2, widest = 16 / size;
     const bool ok = g.nhwc ? plan_nhwc(g, widest, size, bwd, q) : plan_nchw(g, widest, bwd, q);
+    q.past = size_t(g.B) * g.img * size * (bwd ? 3 : 2) >= kStreamBytes;
     if (ok && bwd) q.ws_bytes = size_t(q.rows) * g.C * 2 * sizeof(float);
     return ok;
 }

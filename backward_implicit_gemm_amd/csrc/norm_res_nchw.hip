@@ -47,7 +47,7 @@ __device__ __forceinline__ float pick(const float (&v)[2], int j, int cut)
     return TWO && j >= cut ? v[1] : v[0];
 }
 
-template <typename T, int N, int NV, bool TWO>
+template <typename T, int N, int NV, bool TWO, bool PAST>
 __global__ void __launch_bounds__(res_threads_fwd(N * NV))
     res_nchw_fwd(NormGeom g, NormResPlan q, const T *__restrict__ x, const void *__restrict__ gamma,
                  const void *__restrict__ beta, T *__restrict__ y, float *__restrict__ mean_out,
@@ -123,11 +123,11 @@ __global__ void __launch_bounds__(res_threads_fwd(N * NV))
         activate(g.act, z);
         Vec<T, N> o;
         o.put(z);
-        store_vec<T, N>(yp + w.at, o);
+        put_vec<PAST>(yp + w.at, o);
     }
 }
 
-template <typename T, int N, int NV, bool TWO>
+template <typename T, int N, int NV, bool TWO, bool PAST>
 __global__ void __launch_bounds__(res_threads_bwd(N * NV))
     res_nchw_bwd(NormGeom g, NormResPlan q, const T *__restrict__ x, const T *__restrict__ dy,
                  const void *__restrict__ gamma, const void *__restrict__ beta, const float *__restrict__ mean,
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(res_threads_bwd(N * NV))
                 o[j] = r[0] * (fmaf(pick<TWO>(a[i], j, w[i].cut), d[i][j], -c1) - h[i][j] * c2);
             Vec<T, N> ov;
             ov.put(o);
-            store_vec<T, N>(op + w[i].at, ov);
+            put_vec<PAST>(op + w[i].at, ov);
         }
     }
     if (!part) return;
@@ -281,17 +281,18 @@ hipError_t launch_norm_res_nchw_fwd(const NormGeom &g, const NormResPlan &q, con
     return with_n<T>(q.N, [&](auto n) {
         return with_nv<8>(q.NV, [&](auto nv) {
             constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
+            return with_past<(sizeof(T) * N >= 8)>(q.past, [&](auto past) {
+            constexpr bool P = decltype(past)::value;
             if (q.two) {
                 if constexpr (N == kVec<T>)
-                    hipLaunchKernelGGL((res_nchw_fwd<T, N, NV, true>), dim3(unsigned(q.grid)), dim3(q.threads), 0, s,
-                                       g, q, (const T *)x, gamma, beta, (T *)y, mean, rstd);
+                    hipLaunchKernelGGL((res_nchw_fwd<T, N, NV, true, P>), dim3(unsigned(q.grid)), dim3(q.threads), 0, s, g, q, (const T *)x, gamma, beta, (T *)y, mean, rstd);
                 else
                     return hipErrorInvalidValue;
             } else {
-                hipLaunchKernelGGL((res_nchw_fwd<T, N, NV, false>), dim3(unsigned(q.grid)), dim3(q.threads), 0, s, g,
-                                   q, (const T *)x, gamma, beta, (T *)y, mean, rstd);
+                hipLaunchKernelGGL((res_nchw_fwd<T, N, NV, false, P>), dim3(unsigned(q.grid)), dim3(q.threads), 0, s, g, q, (const T *)x, gamma, beta, (T *)y, mean, rstd);
             }
             return hipGetLastError();
+            });
         });
     });
 }
@@ -304,19 +305,20 @@ hipError_t launch_norm_res_nchw_bwd(const NormGeom &g, const NormResPlan &q, con
     return with_n<T>(q.N, [&](auto n) {
         return with_nv<kHeldMost / decltype(n)::value>(q.NV, [&](auto nv) {
             constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
+            return with_past<(sizeof(T) * N >= 8)>(q.past, [&](auto past) {
+            constexpr bool P = decltype(past)::value;
             if (q.two) {
                 if constexpr (N == kVec<T>)
-                    hipLaunchKernelGGL((res_nchw_bwd<T, N, NV, true>), dim3(unsigned(q.grid)), dim3(q.threads),
-                                       q.lds_bytes, s, g, q, (const T *)x, (const T *)dy, gamma, beta, mean, rstd,
+                    hipLaunchKernelGGL((res_nchw_bwd<T, N, NV, true, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s, g, q, (const T *)x, (const T *)dy, gamma, beta, mean, rstd,
                                        (T *)dx, part);
                 else
                     return hipErrorInvalidValue;
             } else {
-                hipLaunchKernelGGL((res_nchw_bwd<T, N, NV, false>), dim3(unsigned(q.grid)), dim3(q.threads),
-                                   q.lds_bytes, s, g, q, (const T *)x, (const T *)dy, gamma, beta, mean, rstd,
+                hipLaunchKernelGGL((res_nchw_bwd<T, N, NV, false, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s, g, q, (const T *)x, (const T *)dy, gamma, beta, mean, rstd,
                                    (T *)dx, part);
             }
             return hipGetLastError();
+            });
         });
     });
 }

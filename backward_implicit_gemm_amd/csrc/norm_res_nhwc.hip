@@ -39,7 +39,7 @@ __device__ __forceinline__ Place place(const NormResPlan &q, int slab)
     return p;
 }
 
-template <typename T, int N, int NV, bool ONE>
+template <typename T, int N, int NV, bool ONE, bool PAST>
 __global__ void __launch_bounds__(res_threads_fwd(N * NV))
     res_nhwc_fwd(NormGeom g, NormResPlan q, const T *__restrict__ x, const void *__restrict__ gamma,
                  const void *__restrict__ beta, T *__restrict__ y, float *__restrict__ mean_out,
@@ -126,11 +126,11 @@ __global__ void __launch_bounds__(res_threads_fwd(N * NV))
         activate(g.act, z);
         Vec<T, N> o;
         o.put(z);
-        store_vec<T, N>(yp + int64_t(row) * g.C, o);
+        put_vec<PAST>(yp + int64_t(row) * g.C, o);
     }
 }
 
-template <typename T, int N, int NV, bool ONE>
+template <typename T, int N, int NV, bool ONE, bool PAST>
 __global__ void __launch_bounds__(res_threads_bwd(N * NV))
     res_nhwc_bwd(NormGeom g, NormResPlan q, const T *__restrict__ x, const T *__restrict__ dy,
                  const void *__restrict__ gamma, const void *__restrict__ beta, const float *__restrict__ mean,
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(res_threads_bwd(N * NV))
                 o[j] = r[j] * (fmaf(a[j], d[i][j], -c1[ONE ? 0 : j]) - h[i][j] * c2[ONE ? 0 : j]);
             Vec<T, N> ov;
             ov.put(o);
-            store_vec<T, N>(dx + base + int64_t(row) * g.C, ov);
+            put_vec<PAST>(dx + base + int64_t(row) * g.C, ov);
         }
     }
     if (!part) return;
@@ -250,13 +250,14 @@ hipError_t launch_norm_res_nhwc_fwd(const NormGeom &g, const NormResPlan &q, con
     return with_n<T>(q.N, [&](auto n) {
         return with_nv<8>(q.NV, [&](auto nv) {
             constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
+            return with_past<(sizeof(T) * N >= 8)>(q.past, [&](auto past) {
+            constexpr bool P = decltype(past)::value;
             if (g.Cg % N == 0)
-                hipLaunchKernelGGL((res_nhwc_fwd<T, N, NV, true>), dim3(unsigned(q.grid)), dim3(q.threads),
-                                   q.lds_bytes, s, g, q, (const T *)x, gamma, beta, (T *)y, mean, rstd);
+                hipLaunchKernelGGL((res_nhwc_fwd<T, N, NV, true, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s, g, q, (const T *)x, gamma, beta, (T *)y, mean, rstd);
             else if constexpr (N > 1)
-                hipLaunchKernelGGL((res_nhwc_fwd<T, N, NV, false>), dim3(unsigned(q.grid)), dim3(q.threads),
-                                   q.lds_bytes, s, g, q, (const T *)x, gamma, beta, (T *)y, mean, rstd);
+                hipLaunchKernelGGL((res_nhwc_fwd<T, N, NV, false, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s, g, q, (const T *)x, gamma, beta, (T *)y, mean, rstd);
             return hipGetLastError();
+            });
         });
     });
 }
@@ -269,15 +270,16 @@ hipError_t launch_norm_res_nhwc_bwd(const NormGeom &g, const NormResPlan &q, con
     return with_n<T>(q.N, [&](auto n) {
         return with_nv<kHeldMost / decltype(n)::value>(q.NV, [&](auto nv) {
             constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
+            return with_past<(sizeof(T) * N >= 8)>(q.past, [&](auto past) {
+            constexpr bool P = decltype(past)::value;
             if (g.Cg % N == 0)
-                hipLaunchKernelGGL((res_nhwc_bwd<T, N, NV, true>), dim3(unsigned(q.grid)), dim3(q.threads),
-                                   q.lds_bytes, s, g, q, (const T *)x, (const T *)dy, gamma, beta, mean, rstd,
+                hipLaunchKernelGGL((res_nhwc_bwd<T, N, NV, true, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s, g, q, (const T *)x, (const T *)dy, gamma, beta, mean, rstd,
                                    (T *)dx, part);
             else if constexpr (N > 1)
-                hipLaunchKernelGGL((res_nhwc_bwd<T, N, NV, false>), dim3(unsigned(q.grid)), dim3(q.threads),
-                                   q.lds_bytes, s, g, q, (const T *)x, (const T *)dy, gamma, beta, mean, rstd,
+                hipLaunchKernelGGL((res_nhwc_bwd<T, N, NV, false, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s, g, q, (const T *)x, (const T *)dy, gamma, beta, mean, rstd,
                                    (T *)dx, part);
             return hipGetLastError();
+            });
         });
     });
 }

@@ -182,7 +182,7 @@ __device__ __forceinline__ void channel_constants(const NormGeom &g, int b, int 
     }
 }
 
-template <typename T, int N, bool NHWC>
+template <typename T, int N, bool NHWC, bool PAST>
 __global__ void __launch_bounds__(kThreads) norm_apply(NormGeom g, NormSplitPlan q, const T *__restrict__ x,
                                                        const void *__restrict__ gamma,
                                                        const void *__restrict__ beta,
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) norm_apply(NormGeom g, NormSplitPlan
         activate(g.act, z);
         Vec<T, N> out;
         out.put(z);
-        store_vec<T, N>(y + o, out);
+        put_vec<PAST>(y + o, out);
     }
 }
 
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_groups(NormGeom g, int chun
     }
 }
 
-template <typename T, int N, bool NHWC>
+template <typename T, int N, bool NHWC, bool PAST>
 __global__ void __launch_bounds__(kThreads) norm_bwd_apply(NormGeom g, NormSplitPlan q, const T *__restrict__ x,
                                                            const T *__restrict__ dy,
                                                            const void *__restrict__ gamma,
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_apply(NormGeom g, NormSplit
         }
         Vec<T, N> out;
         out.put(d);
-        store_vec<T, N>(dx + o, out);
+        put_vec<PAST>(dx + o, out);
     }
 }
 
@@ -398,6 +398,9 @@ bool plan_norm_split(const NormGeom &g, int dtype, NormSplitPlan &q)
         }
         q.grid = (units * q.chunks + kWaves - 1) / kWaves;
     }
+    const size_t bytes = size_t(g.B) * g.img * (dtype == GC_F32 ? 4 : 2);
+    q.past_fwd = 2 * bytes >= kStreamBytes;
+    q.past_bwd = 3 * bytes >= kStreamBytes;
     const size_t pairs = size_t(g.B) * q.chunks * g.C * 2;
     const size_t groups = size_t(g.B) * g.G * 2;
     q.part_bytes_fwd = (pairs * 8 + 255) & ~size_t(255);
@@ -407,23 +410,30 @@ bool plan_norm_split(const NormGeom &g, int dtype, NormSplitPlan &q)
     return q.grid <= 0x7FFFFFFF && int64_t(g.B) * g.G <= int64_t(0x7FFFFFFF) * kWaves;
 }
 
-#define GC_NORM_LAUNCH(KERNEL, N, lds, ...)                                                              \
+// Launches KERNEL<T, N, layout, ...> over the plan's grid.
+#define GC_NORM_LAUNCH(lds, args, KERNEL, ...)                                                           \
     do {                                                                                                 \
-        if (g.nhwc) hipLaunchKernelGGL((KERNEL<T, N, true>), dim3(unsigned(q.grid)), dim3(kThreads), lds, s, g, q, __VA_ARGS__);  \
-        else hipLaunchKernelGGL((KERNEL<T, N, false>), dim3(unsigned(q.grid)), dim3(kThreads), lds, s, g, q, __VA_ARGS__);        \
+        if (g.nhwc)                                                                                      \
+            hipLaunchKernelGGL((KERNEL<T, N, true __VA_ARGS__>), dim3(unsigned(q.grid)), dim3(kThreads), \
+                               lds, s, GC_NORM_ARGS args);                                               \
+        else                                                                                             \
+            hipLaunchKernelGGL((KERNEL<T, N, false __VA_ARGS__>), dim3(unsigned(q.grid)), dim3(kThreads), \
+                               lds, s, GC_NORM_ARGS args);                                               \
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;                           \
     } while (0)
+#define GC_NORM_ARGS(...) g, q, __VA_ARGS__
 
 namespace {
 template <typename T, int N>
 hipError_t split_fwd(const NormGeom &g, const NormSplitPlan &q, const T *x, const void *gamma, const void *beta,
                      T *y, float *mean, float *rstd, double *part, hipStream_t s)
 {
-    GC_NORM_LAUNCH(norm_stats, N, lds_bytes(g, q, 8), x, part);
+    GC_NORM_LAUNCH(lds_bytes(g, q, 8), (x, part), norm_stats);
     hipLaunchKernelGGL(norm_finish, dim3(unsigned((int64_t(g.B) * g.G + kWaves - 1) / kWaves)), dim3(kThreads), 0, s,
                        g, q.chunks, part, mean, rstd);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    GC_NORM_LAUNCH(norm_apply, N, 0, x, gamma, beta, mean, rstd, y);
+    if (q.past_fwd) GC_NORM_LAUNCH(0, (x, gamma, beta, mean, rstd, y), norm_apply, , true);
+    else GC_NORM_LAUNCH(0, (x, gamma, beta, mean, rstd, y), norm_apply, , false);
     return hipSuccess;
 }
 
@@ -432,11 +442,12 @@ hipError_t split_bwd(const NormGeom &g, const NormSplitPlan &q, const T *x, cons
                      const T *dy, const float *mean, const float *rstd, T *dx, void *dgamma, void *dbeta,
                      float *part, float *cc, hipStream_t s)
 {
-    GC_NORM_LAUNCH(norm_bwd_sums, N, lds_bytes(g, q, 4), x, dy, gamma, beta, mean, rstd, part);
+    GC_NORM_LAUNCH(lds_bytes(g, q, 4), (x, dy, gamma, beta, mean, rstd, part), norm_bwd_sums);
     hipLaunchKernelGGL(norm_bwd_groups<T>, dim3(unsigned((int64_t(g.B) * g.G + kWaves - 1) / kWaves)), dim3(kThreads),
                        0, s, g, q.chunks, part, gamma, cc);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    GC_NORM_LAUNCH(norm_bwd_apply, N, 0, x, dy, gamma, beta, mean, rstd, cc, dx);
+    if (q.past_bwd) GC_NORM_LAUNCH(0, (x, dy, gamma, beta, mean, rstd, cc, dx), norm_bwd_apply, , true);
+    else GC_NORM_LAUNCH(0, (x, dy, gamma, beta, mean, rstd, cc, dx), norm_bwd_apply, , false);
     return launch_norm_params<T>(g, int64_t(g.B) * q.chunks, part, dgamma, dbeta, s);
 }
 }  // namespace
