@@ -36,6 +36,13 @@ int pow2_at_most(int64_t v)
     return p;
 }
 
+// Image slots of the backward: each walks B / at_once images, an equal number.
+int slots_of(int B, double at_once)
+{
+    const int each = std::max(1, int(B / std::max(1.0, at_once)));
+    return (B + each - 1) / each;
+}
+
 bool plan_nchw(const NormGeom &g, int widest, bool bwd, NormResPlan &best)
 {
     // the longest vector that lies in one channel, if it has 8 bytes at least; else a
@@ -63,7 +70,7 @@ bool plan_nchw(const NormGeom &g, int widest, bool bwd, NormResPlan &best)
             if (bwd) {
                 q.lds_bytes = std::max<size_t>(256, size_t(q.teams) * nvec * 2 * (two ? 2 : 1) * sizeof(float));
                 if (q.lds_bytes > kLdsMost) continue;
-                q.images = int(std::min<double>(g.B, std::max(1.0, kWavesAtOnce * 64 / (double(g.G) * L))));
+                q.images = slots_of(g.B, kWavesAtOnce * 64 / (double(g.G) * L));
                 q.rows = q.images;
                 q.grid = (int64_t(q.images) * g.G + q.teams - 1) / q.teams;
             } else {
@@ -116,9 +123,8 @@ bool plan_nhwc(const NormGeom &g, int widest, int size, bool bwd, NormResPlan &b
                     q.lds_bytes = lds;
                     if (lds > kLdsMost) continue;
                     if (bwd) {
-                        const double at_once = kWavesAtOnce * 64 / (double(slabs) * L);
-                        const int most = int(std::min<double>(g.B, std::max(1.0, at_once)));
-                        q.rows = (most + q.teams - 1) / q.teams;
+                        const int slots = slots_of(g.B, kWavesAtOnce * 64 / (double(slabs) * L));
+                        q.rows = (slots + q.teams - 1) / q.teams;
                         q.images = q.rows * q.teams;
                         q.grid = int64_t(q.rows) * slabs;
                     } else {
@@ -128,7 +134,6 @@ bool plan_nhwc(const NormGeom &g, int widest, int size, bool bwd, NormResPlan &b
                     least = c;
                     best = q;
                 }
-            if (least < 1e300 && k == g.G) break;   // whole images fit
         }
         if (least < 1e300) return true;             // shorter vectors only where longer ones fit nowhere
     }

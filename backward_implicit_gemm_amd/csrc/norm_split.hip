@@ -2,8 +2,9 @@
 // groups too large to stay on one compute unit: three launches each.
 //
 //   1. channel sums over a chunk of positions, partial[image][chunk][channel]:
-//      forward (x, x^2) in fp64, which makes the variance's difference of two
-//      large sums exact enough for any mean; backward (g, g*hat) in fp32;
+//      forward (x, x^2) in fp64, so that the variance can be a difference of two large
+//      sums; fp64 is entered once for up to kBlock values, summed in fp32 around the
+//      first of them.  Backward (g, g*hat) in fp32;
 //   2. per (image, group) the statistics (forward: mean, rstd; backward: c1, c2),
 //      one wave each, and for the backward dgamma and dbeta, one workgroup for 16
 //      channels, all in fixed orders;
@@ -24,6 +25,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
+constexpr int kUnroll = 4;     // vectors a thread has in flight
+constexpr int kBlock = 32;     // vectors whose values are summed in fp32 around the first
 
 // Positions [p0, p1) of image b and the channels this thread works on.
 template <int N, bool NHWC>
@@ -128,15 +131,47 @@ __global__ void __launch_bounds__(kThreads) norm_stats(NormGeom g, NormSplitPlan
     const Part<N, NHWC> w = part_of<N, NHWC>(g, q, b);
     double s[NC] = {}, t[NC] = {};
     if (w.live) {
-        for (int p = w.p; p < w.p1; p += w.step) {
-            int skip = 0;
-            const int at = NHWC ? p : pulled_back<N>(p, w.p1, skip);
-            const Vec<T, N> v = load_vec<T, N>(x + w.base + (NHWC ? int64_t(at) * g.C : at));
+        int p = w.p;
+        while (p < w.p1) {
+            // sum of x = n*o + fs, of x^2 = n*o^2 + 2*o*fs + ft, o the first value.  An o far
+            // from the others adds n times its own square, so rounding relative to that is
+            // relative to the sum as well.
+            float o[NC], fs[NC] = {}, ft[NC] = {}, n = 0;
+            for (int k = 0; k < kBlock && p < w.p1; k += kUnroll) {
+                Vec<T, N> v[kUnroll];
+                int skip[kUnroll];
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const double d = j < skip ? 0.0 : double(v.get(j));
-                s[NC == 1 ? 0 : j] += d;
-                t[NC == 1 ? 0 : j] = fma(d, d, t[NC == 1 ? 0 : j]);
+                for (int u = 0; u < kUnroll; ++u) {
+                    skip[u] = N;   // nothing there
+                    v[u] = Vec<T, N>{};
+                    if (p + u * w.step < w.p1) {
+                        skip[u] = 0;
+                        const int at = NHWC ? p + u * w.step : pulled_back<N>(p + u * w.step, w.p1, skip[u]);
+                        v[u] = load_vec<T, N>(x + w.base + (NHWC ? int64_t(at) * g.C : at));
+                    }
+                }
+                if (k == 0) {
+#pragma unroll
+                    for (int e = 0; e < NC; ++e) o[e] = v[0].get(NC == 1 ? N - 1 : e);
+                }
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    n += NHWC ? (skip[u] ? 0.f : 1.f) : float(N - skip[u]);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        const int e = NC == 1 ? 0 : j;
+                        const float d = j < skip[u] ? 0.f : v[u].get(j) - o[e];
+                        fs[e] += d;
+                        ft[e] = fmaf(d, d, ft[e]);
+                    }
+                }
+                p += kUnroll * w.step;
+            }
+#pragma unroll
+            for (int e = 0; e < NC; ++e) {
+                const double od = o[e], sd = fs[e], nd = n;
+                s[e] += fma(nd, od, sd);
+                t[e] += fma(od, fma(nd, od, 2 * sd), double(ft[e]));
             }
         }
     }
@@ -195,21 +230,31 @@ __global__ void __launch_bounds__(kThreads) norm_apply(NormGeom g, NormSplitPlan
     if (!w.live) return;
     float cm[NC], cr[NC], cg[NC], cb[NC];
     channel_constants<T, N, NC>(g, b, w.c, gamma, beta, mean, rstd, cm, cr, cg, cb);
-    for (int p = w.p; p < w.p1; p += w.step) {
-        int skip = 0;
-        const int at = NHWC ? p : pulled_back<N>(p, w.p1, skip);
-        const int64_t o = w.base + (NHWC ? int64_t(at) * g.C : at);
-        const Vec<T, N> v = load_vec<T, N>(x + o);
-        float z[N];
+    for (int p = w.p; p < w.p1; p += kUnroll * w.step) {
+        Vec<T, N> v[kUnroll];
+        int64_t o[kUnroll];
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int k = NC == 1 ? 0 : j;
-            z[j] = norm_z(v.get(j), cm[k], cr[k], cg[k], cb[k]);
+        for (int u = 0; u < kUnroll; ++u) {
+            const int pu = p + u * w.step;
+            int skip = 0;
+            const int at = NHWC ? pu : pulled_back<N>(pu, w.p1, skip);
+            o[u] = w.base + (NHWC ? int64_t(at) * g.C : at);
+            if (pu < w.p1) v[u] = load_vec<T, N>(x + o[u]);
         }
-        activate(g.act, z);
-        Vec<T, N> out;
-        out.put(z);
-        put_vec<PAST>(y + o, out);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (p + u * w.step >= w.p1) break;
+            float z[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int k = NC == 1 ? 0 : j;
+                z[j] = norm_z(v[u].get(j), cm[k], cr[k], cg[k], cb[k]);
+            }
+            activate(g.act, z);
+            Vec<T, N> out;
+            out.put(z);
+            put_vec<PAST>(y + o[u], out);
+        }
     }
 }
 
