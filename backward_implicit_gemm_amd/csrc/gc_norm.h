@@ -96,14 +96,23 @@ __device__ __forceinline__ void act_grad(int act, float (&x)[N], float (&dy)[N],
             off |= z <= 0.f ? 1u << j : 0u;
             near |= fabsf(z) <= 4.8e-7f * fabsf(z - beta[k]) ? 1u << j : 0u;
         }
-        if (near) {
+        while (near) {   // one at a time: unrolled, fp64 would take 30 to 70 registers
+            const int i = __builtin_ctz(near);
+            near &= near - 1;
+            float v[5];
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const int k = NC == 1 ? 0 : j;
-                if (!(near >> j & 1)) continue;
-                const double z = (double(x[j]) - mean[k]) * rstd[k] * gamma[k] + beta[k];
-                off = (off & ~(1u << j)) | (z <= 0.0 ? 1u << j : 0u);
+                if (j == i) {
+                    v[0] = x[j];
+                    v[1] = mean[k];
+                    v[2] = rstd[k];
+                    v[3] = gamma[k];
+                    v[4] = beta[k];
+                }
             }
+            const double z = (double(v[0]) - v[1]) * v[2] * v[3] + v[4];
+            off = (off & ~(1u << i)) | (z <= 0.0 ? 1u << i : 0u);
         }
 #pragma unroll
         for (int j = 0; j < N; ++j) {
