@@ -5,4 +5,4 @@ gfx950, declared in ``include/gc.h``); :mod:`backward_implicit_gemm_amd.binding`
 marshals torch tensors into its calls.  Importing this package loads nothing;
 the binding loads the library on first use and raises if it is missing.
 """
-__all__ = ["binding", "inputs"]
+__all__ = ["binding", "encoder", "inputs"]

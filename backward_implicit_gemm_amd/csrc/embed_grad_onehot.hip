@@ -19,7 +19,8 @@
 //
 // The waves' sums are joined in LDS in order, each workgroup writes one partial, and a
 // second launch adds the partials in order: bit-reproducible.  Bound by memory in
-// bf16 at 128 rows (making O is next: 12 vector instructions for 16 rows of a step).
+// bf16 at 128 rows (making O is next: 12 vector instructions for 16 rows of a step):
+// the rollout's 98 MB take 28 us and the sums 5, in fp32 the minibatch's 6 MB 11 and 4.
 #include <algorithm>
 
 #include "gc_embed.h"
@@ -49,14 +50,22 @@ __host__ __device__ __forceinline__ int slab_column(int s, int D) { return D > k
 // Column of slot i (0 .. 31) of a slab; rows shorter than a slab repeat their last pair.
 __device__ __forceinline__ int slot_column(int c0, int i, int D) { return min(c0 + (i & ~1), D - 2) + (i & 1); }
 
-// ones (bf16) where the two tokens of t equal v, zeros elsewhere
+// Where the sum of row v (of a block) and slot i lies: as the matrix instructions
+// leave it, [16 rows][half of the column pairs][lane][4 rows].
+__device__ __forceinline__ int sum_place(int v, int i)
+{
+    return ((v / 16 * 2 + i % 2) * 64 + v % 16 / 4 * 16 + i / 2) * 4 + v % 4;
+}
+
+// ones (bf16) where the two tokens of t equal v, zeros elsewhere: 1 - x without going
+// below 0 is 1 only for x = 0.  In assembly, as the compiler makes two compares, two
+// selects and a byte shuffle of it (the rollout's gradient: 42 us that way, 36 this).
 __device__ __forceinline__ uint32_t onehot2(uint32_t t, uint32_t v2)
 {
-    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-    const u16x2 x = __builtin_bit_cast(u16x2, t ^ v2);
-    const u16x2 y = __builtin_elementwise_min(x, (u16x2){1, 1});   // 0 where equal
-    const u16x2 a = y * (u16x2){0xC080, 0xC080} + (u16x2){0x3F80, 0x3F80};
-    return __builtin_bit_cast(uint32_t, a);
+    uint32_t a;
+    asm("v_pk_sub_u16 %0, 1, %1 op_sel_hi:[0,1] clamp" : "=v"(a) : "v"(t ^ v2));
+    asm("v_pk_mul_lo_u16 %0, %1, %2" : "=v"(a) : "v"(a), "v"(0x3F803F80u));
+    return a;
 }
 
 // A chunk's tokens: STEPS steps for each wave.
@@ -164,99 +173,116 @@ __global__ void __launch_bounds__(kThreads, MB <= 8 ? 3 : 1) onehot_partials(Emb
             s.off[at] = g.row(min(chunk * TOKENS + i, g.n - 1));
         }
     };
-    Pair<T> p[2][8];
+    constexpr int RING = STEPS == 1 ? 1 : 4, AHEAD = STEPS == 1 ? 1 : 2;   // steps of rows in registers, and requested early
+    Pair<T> p[RING][8];
     auto load = [&](const Stage &s, int st, Pair<T>(&v)[8]) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = load_pair(col + s.off[st * kStep + q * 8 + j]);
     };
 
     // The tokens of the next chunk are staged, and its first rows requested, before
-    // the last step of this one: one barrier a chunk.
+    // the last steps of this one: one barrier a chunk.
     read_tokens(share);
     stage_tokens(share, lds.staged[0]);
     __syncthreads();
-    load(lds.staged[0], wave, p[0]);
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) load(lds.staged[0], u * kWaves + wave, p[u]);
     if (share + shares < chunks) read_tokens(share + shares);
     int b = 0;
     for (uint32_t chunk = share; chunk < chunks; chunk += shares) {
         const int next = b == kStaged - 1 ? 0 : b + 1;
+        const bool more = chunk + shares < chunks;
 #pragma unroll
         for (int u = 0; u < STEPS; ++u) {
-            if (u + 1 < STEPS) {
-                load(lds.staged[b], (u + 1) * kWaves + wave, p[(u + 1) & 1]);
-            } else if (chunk + shares < chunks) {
+            if (u == STEPS - AHEAD && more) {
                 stage_tokens(chunk + shares, lds.staged[next]);
                 __syncthreads();
-                if (STEPS > 1) load(lds.staged[next], wave, p[0]);
                 if (chunk + 2 * shares < chunks) read_tokens(chunk + 2 * shares);
             }
-            step<MB>(lds.staged[b], u * kWaves + wave, q, n, v0, p[u & 1], acc);
-            if (STEPS == 1 && chunk + shares < chunks) load(lds.staged[next], wave, p[0]);
+            if (STEPS == 1) {
+                step<MB>(lds.staged[b], wave, q, n, v0, p[0], acc);
+                if (more) load(lds.staged[next], wave, p[0]);
+                continue;
+            }
+            if (u + AHEAD < STEPS) load(lds.staged[b], (u + AHEAD) * kWaves + wave, p[(u + AHEAD) % RING]);
+            else if (more) load(lds.staged[next], (u + AHEAD - STEPS) * kWaves + wave, p[(u + AHEAD) % RING]);
+            step<MB>(lds.staged[b], u * kWaves + wave, q, n, v0, p[u], acc);
         }
         b = next;
     }
     __syncthreads();
 
-    // the waves in order
+    // the waves in order, in the accumulators' own layout
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) nan |= acc[i][e / 4][e % 4] != acc[i][e / 4][e % 4];
     nan = __ballot(nan) != 0;
-    for (int i = threadIdx.x; i < ROWS * kCols; i += kThreads) table[i] = 0.f;
+    f32x4 *sums = reinterpret_cast<f32x4 *>(table);
     for (int w = 0; w < kWaves; ++w) {
-        __syncthreads();
+        if (w) __syncthreads();
         if (w != wave) continue;
         if (!nan) {
 #pragma unroll
-            for (int i = 0; i < MB; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    table[(i * 16 + q * 4 + e % 4) * kCols + 2 * n + e / 4] += acc[i][e / 4][e % 4];
+            for (int i = 0; i < 2 * MB; ++i) {
+                f32x4 s = acc[i / 2][i % 2];
+                if (w) s += sums[i * 64 + lane];
+                sums[i * 64 + lane] = s;
+            }
             continue;
         }
         // non-finite values: token by token, lanes 0 .. 31 a column each
+        if (w == 0)
+            for (int i = lane; i < ROWS * kCols; i += 64) table[i] = 0.f;
         for (uint32_t chunk = share; chunk < chunks; chunk += shares)
             for (int i = 0; i < TOKENS; ++i) {
                 const uint32_t k = chunk * TOKENS + i;
                 if ((i / kStep) % kWaves != wave || k >= g.n) continue;
                 const int64_t t = g.token(tok, k) - v0;
                 if (t < 0 || t >= ROWS || t + v0 >= g.V || lane >= kCols) continue;
-                table[t * kCols + lane] += to_f32(dout[g.row(k) + slot_column(c0, lane, g.D)]);
+                table[sum_place(int(t), lane)] += to_f32(dout[g.row(k) + slot_column(c0, lane, g.D)]);
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             }
     }
     __syncthreads();
-    float *o = part + size_t(blockIdx.x) * (ROWS * kCols);
-    for (int i = threadIdx.x; i < ROWS * kCols; i += kThreads) o[i] = table[i];
+    f32x4 *o = reinterpret_cast<f32x4 *>(part) + size_t(blockIdx.x) * (ROWS * kCols / 4);
+    for (int i = threadIdx.x; i < ROWS * kCols / 4; i += kThreads) o[i] = sums[i];
 }
 
-// One workgroup a table row and slab: the sum over the shares, in order.
+// Sums over the shares, in order; a workgroup takes 32 neighbouring places of a
+// block of rows and a slab.
 template <typename T>
 __global__ void __launch_bounds__(1024) onehot_sum(int V, int D, const float *__restrict__ part,
                                                    T *__restrict__ dtable, float scale, int slabs, int shares,
                                                    int rows)
 {
-    __shared__ float red[32][kCols + 1];
-    const int i = threadIdx.x % kCols, lane = threadIdx.x / kCols;
-    const int slab = blockIdx.x % slabs, v = blockIdx.x / slabs;
-    const size_t stride = size_t(rows) * kCols;
-    const float *p = part + (size_t(v / rows) * slabs + slab) * shares * stride + size_t(v % rows) * kCols + i;
+    __shared__ float red[32][33];
+    const int i = threadIdx.x % 32, lane = threadIdx.x / 32;
+    const int stride = rows * kCols;                  // places of a block
+    const int place = int(blockIdx.x % rows) * 32 + i;
+    const int block = blockIdx.x / rows;              // (block of rows, slab)
+    const float *p = part + size_t(block) * shares * stride + place;
     float s[4] = {};
     int w = lane;
     for (; w + 96 < shares; w += 128)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) s[u] += p[(w + 32 * u) * stride];
-    for (; w < shares; w += 32) s[0] += p[w * stride];
+        for (int u = 0; u < 4; ++u) s[u] += p[size_t(w + 32 * u) * stride];
+    for (; w < shares; w += 32) s[0] += p[size_t(w) * stride];
     red[lane][i] = (s[0] + s[1]) + (s[2] + s[3]);
     __syncthreads();
     for (int h = 16; h > 0; h >>= 1) {
         if (lane < h) red[lane][i] += red[lane + h][i];
         __syncthreads();
     }
-    if (lane == 0)
-        dtable[size_t(v) * D + slot_column(slab_column(slab, D), i, D)] = from_f32<T>(scale * red[0][i]);
+    if (lane == 0) {
+        // the inverse of sum_place
+        const int frag = place / 256, l = place / 4 % 64;
+        const int v = block / slabs * rows + frag / 2 * 16 + l / 16 * 4 + place % 4;
+        const int slot = l % 16 * 2 + frag % 2;
+        if (v < V)
+            dtable[size_t(v) * D + slot_column(slab_column(block % slabs, D), slot, D)] = from_f32<T>(scale * red[0][i]);
+    }
 }
 
 OnehotPlan plan(const EmbedGeom &g)
@@ -308,7 +334,7 @@ hipError_t launch_embed_grad_onehot(const EmbedGeom &g, const void *tok, const v
     default: e = run<T, 16>(g, p, tok, dout, part, s); break;
     }
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(onehot_sum<T>, dim3(unsigned(g.V) * p.slabs), dim3(1024), 0, s, g.V, g.D, part, (T *)dtable, scale,
+    hipLaunchKernelGGL(onehot_sum<T>, dim3(unsigned(p.vblocks * p.slabs * p.rows)), dim3(1024), 0, s, g.V, g.D, part, (T *)dtable, scale,
                        p.slabs, p.shares, p.rows);
     return hipGetLastError();
 }

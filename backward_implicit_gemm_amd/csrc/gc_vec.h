@@ -66,7 +66,7 @@ __device__ __forceinline__ void store_vec(T *p, const Vec<T, N> &v)
 // A store past the cache (PAST), for calls that move kStreamBytes and more: their
 // outputs leave the cache before they are read again, and as dirty lines they
 // push out what the call still reads and are written back in the way of later calls.
-// Clipping 153 MB of gradients took 151 us with plain stores and 121 us past the
+// Clipping 238 MB of gradients took 151 us with plain stores and 121 us past the
 // cache, an embedding of 98 MB 32 and 16 us.  Smaller outputs stay cached for
 // their reader.  A compile-time choice: of two stores at the ends of a branch the
 // compiler makes one plain one.
