@@ -16,8 +16,18 @@ constexpr int kResThreads = 256;   // a workgroup of several teams
 // forward holds the packed elements (128 registers a thread at 1024 threads
 // do), the backward two fp32 values of each.
 constexpr int kHeldMost = 32;   // elements a thread of the backward holds, at most
+constexpr int kMixedMost = 8;   // vectors a thread of the forward holds when they mix groups, at most
 constexpr int res_threads_fwd(int) { return 1024; }
 constexpr int res_threads_bwd(int held) { return held <= 4 ? 1024 : 512; }
+
+// Workgroups are dealt to the chip's 8 dies in turn, each with its own L2.  Neighbouring
+// slabs of an image share memory lines: this order gives them to one die, one after
+// the other.
+__device__ __forceinline__ uint32_t die_order(uint32_t id, uint32_t grid)
+{
+    const uint32_t per = grid / 8;
+    return id < per * 8 ? id % 8 * per + id / 8 : id;
+}
 
 // A team is one wave, or the workgroup: LDS traffic within a wave is in order.
 __device__ __forceinline__ void team_sync(bool wave)
@@ -28,6 +38,19 @@ __device__ __forceinline__ void team_sync(bool wave)
     } else {
         __syncthreads();
     }
+}
+
+// Makes the compiler forget what it unpacked of bf16 vectors: between two passes over
+// them it would rather keep (and spill) the unpacked elements than unpack again.
+template <int N, int NV>
+__device__ __forceinline__ void keep_packed(Vec<float, N> (&)[NV]) {}
+template <int N, int NV>
+__device__ __forceinline__ void keep_packed(Vec<bf16_t, N> (&v)[NV])
+{
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < (N + 1) / 2; ++j) asm volatile("" : "+v"(v[i].w[j]));
 }
 
 // Sum over the L lanes of a team (L <= 64: lanes of a wave; else the
@@ -101,6 +124,9 @@ hipError_t with_nv(int nv, F f)
     case 4: return f(std::integral_constant<int, 4>());
     case 8:
         if constexpr (MOST >= 8) return f(std::integral_constant<int, 8>());
+        return hipErrorInvalidValue;
+    case 16:
+        if constexpr (MOST >= 16) return f(std::integral_constant<int, 16>());
         return hipErrorInvalidValue;
     default: return hipErrorInvalidValue;
     }

@@ -14,6 +14,7 @@
 // each vector's g and g*hat to running sums of its own; only after its last
 // image are those added up by channel, in LDS, into one row of partials a slot.
 // Bound by memory.
+#include <algorithm>
 #include <type_traits>
 
 #include "gc_norm_res.h"
@@ -76,6 +77,7 @@ __global__ void __launch_bounds__(res_threads_fwd(N * NV))
             if (!TWO || j >= skip) s[0] += v[i].get(j);
     }
     team_sum(s, q.L, red);
+    keep_packed(v);
     const float n = 1.f / float(M), m0 = s[0] * n;
     float t[2] = {};
 #pragma unroll
@@ -92,6 +94,7 @@ __global__ void __launch_bounds__(res_threads_fwd(N * NV))
         }
     }
     team_sum(t, q.L, red);
+    keep_packed(v);
     if (!live) return;
     const float off = t[0] * n, mean = m0 + off;
     const float var = fmaxf(fmaf(-off, off, t[1] * n), 0.f);
@@ -279,7 +282,7 @@ hipError_t launch_norm_res_nchw_fwd(const NormGeom &g, const NormResPlan &q, con
                                     const void *beta, void *y, float *mean, float *rstd, hipStream_t s)
 {
     return with_n<T>(q.N, [&](auto n) {
-        return with_nv<8>(q.NV, [&](auto nv) {
+        return with_nv<decltype(n)::value == kVec<T> ? 16 : 8>(q.NV, [&](auto nv) {
             constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
             return with_past<(sizeof(T) * N >= 8)>(q.past, [&](auto past) {
             constexpr bool P = decltype(past)::value;
@@ -303,7 +306,7 @@ hipError_t launch_norm_res_nchw_bwd(const NormGeom &g, const NormResPlan &q, con
                                     float *part, hipStream_t s)
 {
     return with_n<T>(q.N, [&](auto n) {
-        return with_nv<kHeldMost / decltype(n)::value>(q.NV, [&](auto nv) {
+        return with_nv<std::min(8, kHeldMost / decltype(n)::value)>(q.NV, [&](auto nv) {
             constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
             return with_past<(sizeof(T) * N >= 8)>(q.past, [&](auto past) {
             constexpr bool P = decltype(past)::value;

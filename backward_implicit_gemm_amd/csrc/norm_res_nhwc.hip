@@ -12,6 +12,7 @@
 // team walks images slot, slot + images, ..., keeping the channels' running sums of g
 // and g*hat in registers; the teams of a workgroup join them at the end into one
 // row of partials.  Bound by memory.
+#include <algorithm>
 #include <type_traits>
 
 #include "gc_norm_res.h"
@@ -47,7 +48,8 @@ __global__ void __launch_bounds__(res_threads_fwd(N * NV))
 {
     constexpr int E = ONE ? 1 : N;
     extern __shared__ float lds[];
-    const int64_t unit = int64_t(blockIdx.x) * q.teams + threadIdx.x / q.L;   // (image, slab)
+    const uint32_t id = q.slabs > 1 ? die_order(blockIdx.x, gridDim.x) : blockIdx.x;
+    const int64_t unit = int64_t(id) * q.teams + threadIdx.x / q.L;   // (image, slab)
     const int slab = int(unit % q.slabs);
     const int64_t b = unit / q.slabs;
     const Place p = place<N>(q, slab);
@@ -83,6 +85,7 @@ __global__ void __launch_bounds__(res_threads_fwd(N * NV))
 #pragma unroll
         for (int e = 0; e < E; ++e) m0[e] = stat[ge[e]] * n;
     }
+    keep_packed(v);
     {
         float s[2][E] = {};
 #pragma unroll
@@ -104,6 +107,7 @@ __global__ void __launch_bounds__(res_threads_fwd(N * NV))
             rstd[e] = sq != sq ? sq : 1.f / sqrtf(var + g.eps);
         }
     }
+    keep_packed(v);
     if (!live) return;
     // the thread with a group's first channel in the first row writes its statistics
     if (p.slot == 0) {
@@ -139,8 +143,9 @@ __global__ void __launch_bounds__(res_threads_bwd(N * NV))
     constexpr int E = ONE ? 1 : N;
     extern __shared__ float lds[];
     // a workgroup: one slab, `teams` image slots
-    const int slab = int(blockIdx.x % q.slabs);
-    const int row0 = int(blockIdx.x / q.slabs);
+    const uint32_t id = q.slabs > 1 ? die_order(blockIdx.x, gridDim.x) : blockIdx.x;
+    const int slab = int(id % q.slabs);
+    const int row0 = int(id / q.slabs);
     const Place p = place<N>(q, slab);
     const int first = row0 * q.teams + p.team;
     float *red = lds + p.team * q.team_lds, *stat = red + 2 * q.slots * q.width;
@@ -248,13 +253,13 @@ hipError_t launch_norm_res_nhwc_fwd(const NormGeom &g, const NormResPlan &q, con
                                     const void *beta, void *y, float *mean, float *rstd, hipStream_t s)
 {
     return with_n<T>(q.N, [&](auto n) {
-        return with_nv<8>(q.NV, [&](auto nv) {
+        return with_nv<decltype(n)::value == kVec<T> ? 16 : 8>(q.NV, [&](auto nv) {
             constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
             return with_past<(sizeof(T) * N >= 8)>(q.past, [&](auto past) {
             constexpr bool P = decltype(past)::value;
             if (g.Cg % N == 0)
                 hipLaunchKernelGGL((res_nhwc_fwd<T, N, NV, true, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s, g, q, (const T *)x, gamma, beta, (T *)y, mean, rstd);
-            else if constexpr (N > 1)
+            else if constexpr (N > 1 && NV <= kMixedMost)
                 hipLaunchKernelGGL((res_nhwc_fwd<T, N, NV, false, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s, g, q, (const T *)x, gamma, beta, (T *)y, mean, rstd);
             return hipGetLastError();
             });
@@ -268,7 +273,7 @@ hipError_t launch_norm_res_nhwc_bwd(const NormGeom &g, const NormResPlan &q, con
                                     float *part, hipStream_t s)
 {
     return with_n<T>(q.N, [&](auto n) {
-        return with_nv<kHeldMost / decltype(n)::value>(q.NV, [&](auto nv) {
+        return with_nv<std::min(8, kHeldMost / decltype(n)::value)>(q.NV, [&](auto nv) {
             constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
             return with_past<(sizeof(T) * N >= 8)>(q.past, [&](auto past) {
             constexpr bool P = decltype(past)::value;
