@@ -25,7 +25,7 @@ EXPORTED = (
     "gc_conv_plan_name", "gc_conv_fwd_noalloc", "gc_conv_bwd_weight_bias",
     "gc_embed_fwd", "gc_embed_bwd", "gc_embed_workspace_bytes", "gc_group_norm_fwd",
     "gc_group_norm_bwd", "gc_group_norm_workspace_bytes", "gc_grad_norm", "gc_grad_clip",
-    "gc_grad_clip_workspace_bytes",
+    "gc_grad_clip_workspace_bytes", "gc_group_norm_plan_name", "gc_embed_plan_name",
 )
 GC_I32, GC_I64, GC_U8 = 0, 1, 2
 GC_NCHW, GC_NHWC = 0, 1
@@ -117,6 +117,10 @@ def lib():
     L.gc_group_norm_bwd.restype = i
     L.gc_grad_clip_workspace_bytes.argtypes = [i]
     L.gc_grad_clip_workspace_bytes.restype = sz
+    L.gc_group_norm_plan_name.argtypes = [i, np_, i, ctypes.c_char_p, sz]
+    L.gc_group_norm_plan_name.restype = i
+    L.gc_embed_plan_name.argtypes = [ep, i, ctypes.c_char_p, sz]
+    L.gc_embed_plan_name.restype = i
     tp = ctypes.POINTER(gc_tensor)
     L.gc_grad_norm.argtypes = [tp, i, f, vp, vp, sz, vp]
     L.gc_grad_norm.restype = i
@@ -449,6 +453,21 @@ def _raw_stream(stream, device):
         # the handle alone: building a Stream object costs as much host time as a launch
         return torch._C._cuda_getCurrentRawStream(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def gc_group_norm_plan_name(op, desc, dtype):
+    """The kernels a group norm would run (host only, enqueues nothing)."""
+    buf = ctypes.create_string_buffer(256)
+    _check("gc_group_norm_plan_name",
+           lib().gc_group_norm_plan_name(int(op), ctypes.byref(desc), int(dtype), buf, len(buf)))
+    return buf.value.decode()
+
+
+def gc_embed_plan_name(desc, dtype):
+    """The kernels an embedding's gradient would run (host only, enqueues nothing)."""
+    buf = ctypes.create_string_buffer(256)
+    _check("gc_embed_plan_name", lib().gc_embed_plan_name(ctypes.byref(desc), int(dtype), buf, len(buf)))
+    return buf.value.decode()
 
 
 def _scratch(n, device):

@@ -128,6 +128,9 @@ hipError_t with_nv(int nv, F f)
     case 16:
         if constexpr (MOST >= 16) return f(std::integral_constant<int, 16>());
         return hipErrorInvalidValue;
+    case 32:
+        if constexpr (MOST >= 32) return f(std::integral_constant<int, 32>());
+        return hipErrorInvalidValue;
     default: return hipErrorInvalidValue;
     }
 }

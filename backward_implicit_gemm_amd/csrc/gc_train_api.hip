@@ -4,6 +4,7 @@
 // come before the first HIP call.
 #include <limits.h>
 #include <math.h>
+#include <stdio.h>
 
 #include "gc_embed.h"
 #include "gc_kernels.h"
@@ -259,6 +260,39 @@ int gc_group_norm_bwd(const void *x, const void *gamma, const void *beta, const 
                                                         workspace, s)
                                       : norm_bwd<bf16_t>(g, sel, x, gamma, beta, dy, mean, rstd, dx, dgamma, dbeta,
                                                          workspace, s));
+}
+
+int gc_group_norm_plan_name(int op, const gc_norm_desc *d, int dtype, char *buf, size_t buf_bytes)
+{
+    NormGeom g;
+    const int st = check_norm(d, &g);
+    if (st != GC_OK) return st;
+    if (!valid_dtype(dtype) || (op != GC_OP_FWD && op != GC_OP_BWD) || !buf || !buf_bytes) return GC_ERR_INVALID_ARG;
+    const bool bwd = op == GC_OP_BWD;
+    const NormSel s = select_norm(g, dtype, bwd);
+    const char *dir = bwd ? "bwd" : "fwd";
+    if (s.k == NormKind::Split)
+        snprintf(buf, buf_bytes, "norm_split_%s<N=%d,NHWC=%d> chunks=%d grid=%lld", dir, s.q.N, g.nhwc, s.q.chunks,
+                 (long long)s.q.grid);
+    else if (s.k == NormKind::None)
+        snprintf(buf, buf_bytes, "none");
+    else if (g.nhwc)
+        snprintf(buf, buf_bytes, "res_nhwc_%s<N=%d,NV=%d,ONE=%d> threads=%d teams=%d slab=%d grid=%lld", dir, s.r.N,
+                 s.r.NV, g.Cg % s.r.N == 0, s.r.L, s.r.teams, s.r.CW, (long long)s.r.grid);
+    else
+        snprintf(buf, buf_bytes, "res_nchw_%s<N=%d,NV=%d,TWO=%d> threads=%d teams=%d grid=%lld", dir, s.r.N, s.r.NV,
+                 s.r.two, s.r.L, s.r.teams, (long long)s.r.grid);
+    return GC_OK;
+}
+
+int gc_embed_plan_name(const gc_embed_desc *d, int dtype, char *buf, size_t buf_bytes)
+{
+    EmbedGeom g;
+    const int st = check_embed(d, &g);
+    if (st != GC_OK) return st;
+    if (!valid_dtype(dtype) || !buf || !buf_bytes) return GC_ERR_INVALID_ARG;
+    snprintf(buf, buf_bytes, "%s", embed_onehot(g) ? "embed_grad_onehot" : "embed_grad_sort");
+    return GC_OK;
 }
 
 size_t gc_grad_clip_workspace_bytes(int count) { return count < 0 ? 0 : grad_clip_ws_bytes(count); }

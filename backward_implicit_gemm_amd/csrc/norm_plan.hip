@@ -15,7 +15,7 @@ namespace gc {
 namespace {
 
 constexpr double kWavesAtOnce = 4096;
-constexpr int kVectors[] = {1, 2, 3, 4, 8, 16};
+constexpr int kVectors[] = {1, 2, 3, 4, 8, 16, 32};
 constexpr size_t kLdsMost = 64 * 1024;
 
 double cost(double units, int L, int NV, double waste)
@@ -24,10 +24,10 @@ double cost(double units, int L, int NV, double waste)
 }
 
 // whether a kernel of L threads that hold NV vectors of N elements each is built
-bool holds(bool bwd, int L, int N, int NV, int widest)
+bool holds(bool bwd, int L, int N, int NV)
 {
-    if (bwd) return N * NV <= kHeldMost && NV <= 8 && L <= res_threads_bwd(N * NV);
-    return (NV <= 8 || N == widest) && L <= res_threads_fwd(N * NV);
+    if (bwd) return N * NV <= kHeldMost && L <= res_threads_bwd(N * NV);
+    return NV <= 16 && L <= res_threads_fwd(N * NV);
 }
 
 int pow2_at_most(int64_t v)
@@ -57,7 +57,7 @@ bool plan_nchw(const NormGeom &g, int widest, bool bwd, NormResPlan &best)
     for (int NV : kVectors)
         for (int L = 1; L <= 1024; L *= 2) {
             if (int64_t(L) * NV < nvec || (L > 1 && int64_t(L) * NV >= 4 * nvec)) continue;
-            if (!holds(bwd, L, N, NV, widest)) continue;
+            if (NV > 16 || !holds(bwd, L, N, NV)) continue;
             const double c = cost(double(g.B) * g.G, L, NV, 1.0);
             if (c >= least) continue;
             NormResPlan q{};
@@ -97,7 +97,7 @@ bool plan_nhwc(const NormGeom &g, int widest, int size, bool bwd, NormResPlan &b
             const int CV = CW / N, slabs = g.G / k;
             for (int NV : kVectors)
                 for (int L = 64; L <= 1024; L *= 2) {
-                    if (!holds(bwd, L, N, NV, widest) || CV > L) continue;
+                    if (!holds(bwd, L, N, NV) || CV > L) continue;
                     if (!bwd && g.Cg % N && NV > kMixedMost) continue;
                     const int slots = L / CV;
                     if (int64_t(slots) * NV < g.HW) continue;

@@ -14,7 +14,6 @@
 // each vector's g and g*hat to running sums of its own; only after its last
 // image are those added up by channel, in LDS, into one row of partials a slot.
 // Bound by memory.
-#include <algorithm>
 #include <type_traits>
 
 #include "gc_norm_res.h"
@@ -282,7 +281,7 @@ hipError_t launch_norm_res_nchw_fwd(const NormGeom &g, const NormResPlan &q, con
                                     const void *beta, void *y, float *mean, float *rstd, hipStream_t s)
 {
     return with_n<T>(q.N, [&](auto n) {
-        return with_nv<decltype(n)::value == kVec<T> ? 16 : 8>(q.NV, [&](auto nv) {
+        return with_nv<16>(q.NV, [&](auto nv) {
             constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
             return with_past<(sizeof(T) * N >= 8)>(q.past, [&](auto past) {
             constexpr bool P = decltype(past)::value;
@@ -306,7 +305,7 @@ hipError_t launch_norm_res_nchw_bwd(const NormGeom &g, const NormResPlan &q, con
                                     float *part, hipStream_t s)
 {
     return with_n<T>(q.N, [&](auto n) {
-        return with_nv<std::min(8, kHeldMost / decltype(n)::value)>(q.NV, [&](auto nv) {
+        return with_nv<(decltype(n)::value > 1 ? kHeldMost / decltype(n)::value : 16)>(q.NV, [&](auto nv) {
             constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
             return with_past<(sizeof(T) * N >= 8)>(q.past, [&](auto past) {
             constexpr bool P = decltype(past)::value;

@@ -12,7 +12,6 @@
 // team walks images slot, slot + images, ..., keeping the channels' running sums of g
 // and g*hat in registers; the teams of a workgroup join them at the end into one
 // row of partials.  Bound by memory.
-#include <algorithm>
 #include <type_traits>
 
 #include "gc_norm_res.h"
@@ -253,7 +252,7 @@ hipError_t launch_norm_res_nhwc_fwd(const NormGeom &g, const NormResPlan &q, con
                                     const void *beta, void *y, float *mean, float *rstd, hipStream_t s)
 {
     return with_n<T>(q.N, [&](auto n) {
-        return with_nv<decltype(n)::value == kVec<T> ? 16 : 8>(q.NV, [&](auto nv) {
+        return with_nv<16>(q.NV, [&](auto nv) {
             constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
             return with_past<(sizeof(T) * N >= 8)>(q.past, [&](auto past) {
             constexpr bool P = decltype(past)::value;
@@ -273,7 +272,7 @@ hipError_t launch_norm_res_nhwc_bwd(const NormGeom &g, const NormResPlan &q, con
                                     float *part, hipStream_t s)
 {
     return with_n<T>(q.N, [&](auto n) {
-        return with_nv<std::min(8, kHeldMost / decltype(n)::value)>(q.NV, [&](auto nv) {
+        return with_nv<kHeldMost / decltype(n)::value>(q.NV, [&](auto nv) {
             constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
             return with_past<(sizeof(T) * N >= 8)>(q.past, [&](auto past) {
             constexpr bool P = decltype(past)::value;

@@ -252,6 +252,11 @@ int gc_group_norm_fwd(const void *x, const void *gamma, const void *beta, void *
                       void *workspace, size_t ws_bytes, const gc_norm_desc *d, int dtype, int param_dtype,
                       void *stream);
 
+/* Which kernels a group norm or an embedding's gradient would run (pure host, as
+ * gc_conv_plan_name): op GC_OP_FWD or GC_OP_BWD. */
+int gc_group_norm_plan_name(int op, const gc_norm_desc *d, int dtype, char *buf, size_t buf_bytes);
+int gc_embed_plan_name(const gc_embed_desc *d, int dtype, char *buf, size_t buf_bytes);
+
 /* With g = dy * act'(gamma*hat + beta) (relu's derivative is 0 at 0):
  *   dbeta = sum g,  dgamma = sum g*hat  (over images and positions)
  *   dx = rstd * (gamma*g - mean(gamma*g) - hat * mean(gamma*g*hat))  (means over the group)

@@ -253,3 +253,44 @@ def test_more_than_2_31_elements():
     want = ref.norm_bwd(x[-2:], gamma, beta, dy[-2:], mean[-2:], rstd[-2:], G, "silu")[0]
     bound = ref.norm_bwd_bounds(x[-2:], gamma, beta, dy[-2:], mean[-2:], rstd[-2:], G, "silu")[0]
     assert ref.over(dx[-2:], want, bound) <= 1
+
+
+def instances(most=4_000_000):
+    """The smallest shape of a grid that runs each kernel instance: {(instance, type, direction): (shape, G, layout)}."""
+    found = {}
+    for HW, W in ((1, 1), (2, 2), (3, 1), (4, 2), (5, 1), (6, 2), (7, 7), (8, 4), (12, 4), (15, 5), (16, 4), (20, 5),
+                  (33, 3), (49, 7), (64, 8), (100, 10), (165, 15), (256, 16), (400, 20), (1024, 32), (2048, 32),
+                  (4096, 64), (5000, 50)):
+        for Cg in (1, 2, 3, 4, 5, 6, 8, 12, 16, 24, 32, 64, 128):
+            for G in (1, 2, 3, 8, 32):
+                for B in (1, 5, 600, 5000):
+                    size = B * Cg * G * HW
+                    if size > most:
+                        continue
+                    for layout, code in (("nchw", gb.GC_NCHW), ("nhwc", gb.GC_NHWC)):
+                        d = gb.gc_norm_desc(B, Cg * G, HW // W, W, G, code, gb.GC_ACT_SILU, EPS)
+                        for name, dt in (("f32", gb.GC_F32), ("bf16", gb.GC_BF16)):
+                            for op in (gb.GC_OP_FWD, gb.GC_OP_BWD):
+                                key = (gb.gc_group_norm_plan_name(op, d, dt).split(" ")[0], name)
+                                if key not in found or size < found[key][0]:
+                                    found[key] = (size, (B, Cg * G, HW // W, W), G, layout)
+    return found
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("family", ["norm_split", "res_nchw", "res_nhwc"])
+def test_every_instance(family, dtype):
+    cases = {v[1:] for k, v in instances().items() if k[0].startswith(family) and k[1] == dtype}
+    assert len(cases) >= {"norm_split": 2, "res_nchw": 20, "res_nhwc": 20}[family]
+    for i, (shape, G, layout) in enumerate(sorted(cases)):
+        check(shape, G, ("silu", "relu", "gelu", "none")[i % 4], layout, TYPES[dtype], seed=20 + i)
+
+
+@pytest.mark.parametrize("shape,G,layout,dtype", [
+    ((8192, 128, 3, 4), 8, "nchw", "bf16"), ((8192, 128, 3, 4), 16, "nhwc", "bf16"),
+    ((3, 256, 64, 67), 8, "nhwc", "f32"), ((4, 128, 128, 127), 4, "nchw", "bf16"),
+    ((500, 96, 11, 15), 32, "nchw", "f32"),
+], ids=str)
+def test_outputs_past_the_cache(shape, G, layout, dtype):
+    """Calls that move 64 MiB and more store their output past the cache."""
+    check(shape, G, "gelu", layout, TYPES[dtype], seed=30)

@@ -194,3 +194,43 @@ def test_binding_refuses_invalid_descriptors():
         gb.GroupNorm((2, 8, 3, 4), 3, "relu", torch.float32, device="cpu")
     with pytest.raises(ValueError):
         gb.Embedding(2, 3, 0, 4, torch.float32, device="cpu")
+
+
+# ------------------------------------------------------------------- the plans --
+def norm_plan(op, shape, groups, layout, dtype):
+    B, C, H, W = shape
+    return gb.gc_group_norm_plan_name(op, gb.gc_norm_desc(B, C, H, W, groups, layout, 0, 1e-5), dtype)
+
+
+@pytest.mark.parametrize("op", [gb.GC_OP_FWD, gb.GC_OP_BWD])
+@pytest.mark.parametrize("dtype", [gb.GC_F32, gb.GC_BF16])
+@pytest.mark.parametrize("layout", [gb.GC_NCHW, gb.GC_NHWC])
+def test_the_policy_layers_stay_resident(op, dtype, layout):
+    for B in (1, 37, 256, 1024, 16384, 32768):
+        for shape, groups in (((B, 128, 3, 4), 8), ((B, 128, 1, 2), 16), ((B, 59, 11, 15), 1)):
+            assert norm_plan(op, shape, groups, layout, dtype).startswith("res_"), (shape, groups)
+
+
+def test_large_groups_are_split():
+    for layout in (gb.GC_NCHW, gb.GC_NHWC):
+        for op in (gb.GC_OP_FWD, gb.GC_OP_BWD):
+            assert norm_plan(op, (2, 64, 300, 300), 1, layout, gb.GC_BF16).startswith("norm_split")
+
+
+def test_embedding_plans():
+    for V, D, name in ((128, 32, "onehot"), (512, 2, "onehot"), (513, 32, "sort"), (128, 1, "sort"), (40960, 1024, "sort")):
+        assert gb.gc_embed_plan_name(embed_desc(V=V, D=D, ld=3 * D), gb.GC_BF16) == "embed_grad_" + name
+    assert gb.gc_embed_plan_name(embed_desc(rows=0), gb.GC_F32) == "embed_grad_sort"
+
+
+def test_plan_name_errors():
+    d, L = norm_desc(), gb.lib()
+    buf = ctypes.create_string_buffer(16)
+    assert L.gc_group_norm_plan_name(gb.GC_OP_FWD, ctypes.byref(d), 0, None, 16) == BAD
+    assert L.gc_group_norm_plan_name(gb.GC_OP_FWD, ctypes.byref(d), 0, buf, 0) == BAD
+    assert L.gc_group_norm_plan_name(gb.GC_OP_BWD_BIAS, ctypes.byref(d), 0, buf, 16) == BAD
+    assert L.gc_group_norm_plan_name(gb.GC_OP_FWD, ctypes.byref(d), 5, buf, 16) == BAD
+    assert L.gc_embed_plan_name(ctypes.byref(embed_desc(V=0)), 0, buf, 16) == BAD
+    assert L.gc_embed_plan_name(ctypes.byref(embed_desc()), 0, None, 16) == BAD
+    assert L.gc_group_norm_plan_name(gb.GC_OP_FWD, ctypes.byref(d), 0, buf, 16) == gb.GC_OK
+    assert len(buf.value) == 15        # truncated, with its end
