@@ -285,11 +285,17 @@ __global__ void __launch_bounds__(1024) onehot_sum(int V, int D, const float *__
     }
 }
 
+int block_rows(int V)
+{
+    int rows = 32;
+    while (rows < 256 && rows < V) rows *= 2;
+    return rows;
+}
+
 OnehotPlan plan(const EmbedGeom &g)
 {
     OnehotPlan p{};
-    p.rows = 32;
-    while (p.rows < 256 && p.rows < g.V) p.rows *= 2;
+    p.rows = block_rows(g.V);
     p.vblocks = (g.V + p.rows - 1) / p.rows;
     p.slabs = (g.D + kCols - 1) / kCols;
     // three workgroups a CU (what their registers allow); with few tokens, chunks of one
@@ -317,6 +323,12 @@ hipError_t run(const EmbedGeom &g, const OnehotPlan &p, const void *tok, const v
 }
 
 }  // namespace
+
+int embed_grad_onehot_rows(int V)
+{
+    const int rows = block_rows(V);
+    return (V + rows - 1) / rows * rows;
+}
 
 size_t embed_grad_onehot_ws_bytes(const EmbedGeom &g) { return plan(g).bytes; }
 

@@ -5,8 +5,9 @@
 //
 //   1. A stable radix sort of (token, position), 8 bits a pass: digit counts
 //      per tile, (for many tiles a scan of the counts over the tiles,) then
-//      each tile ranks its keys and scatters them.  Tokens outside [0, V)
-//      carry the key V and end up behind all rows.
+//      each tile ranks its keys and scatters them; up to 4096 tokens are sorted by one
+//      workgroup in one launch.  Tokens outside [0, V) carry the key V and end up
+//      behind all rows.
 //   2. Long runs of one token: every kRun sorted positions that hold one token
 //      are summed into a partial row, and likewise every kRun partials of a level into
 //      one of the next, all tiles in parallel.  Other tiles cost nothing.  The
@@ -90,10 +91,30 @@ __global__ void __launch_bounds__(kThreads) sort_scan(uint32_t *__restrict__ cou
     if (t == 0) totals[d] = run;
 }
 
-// Ranks a tile's keys by their digit (stable) and scatters them.  A wave takes
-// 64 consecutive keys a round; the lanes of one digit find each other by
-// ballots over the digit's bits, and the wave's own counters give the rank
-// among its earlier rounds.
+// The rank of a lane's digit among its wave's lanes before it and its wave's
+// earlier calls, whose counts `hist` (the wave's own, 256 counters) keeps.  The lanes
+// of one digit find each other by ballots over the digit's bits.
+__device__ __forceinline__ uint32_t digit_rank(bool valid, uint32_t d, int lane, uint32_t *hist)
+{
+    uint64_t peers = __ballot(valid);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+        const uint64_t set = __ballot(d >> b & 1);
+        peers &= (d >> b & 1) ? set : ~set;
+    }
+    const uint32_t before = __popcll(peers & ((uint64_t(1) << lane) - 1));
+    uint32_t seen = 0;
+    if (valid) seen = hist[d];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (valid && before == 0) hist[d] = seen + __popcll(peers);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    return seen + before;
+}
+
+// Ranks a tile's keys by their digit (stable) and scatters them; a wave takes 64
+// consecutive keys a round.
 template <int ROUNDS>
 __global__ void __launch_bounds__(kThreads) sort_scatter(EmbedGeom g, SortIn in, int shift,
                                                          const uint32_t *__restrict__ counts,
@@ -118,24 +139,7 @@ __global__ void __launch_bounds__(kThreads) sort_scatter(EmbedGeom g, SortIn in,
     }
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r) {
-        const bool valid = base + r * 64 + lane < g.n;
-        const uint32_t d = key[r] >> shift & 255;
-        uint64_t peers = __ballot(valid);
-#pragma unroll
-        for (int b = 0; b < 8; ++b) {
-            const uint64_t set = __ballot(d >> b & 1);
-            peers &= (d >> b & 1) ? set : ~set;
-        }
-        const uint64_t below = (uint64_t(1) << lane) - 1;
-        const uint32_t before = __popcll(peers & below);
-        uint32_t seen = 0;
-        if (valid) seen = hist[wave][d];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        if (valid && before == 0) hist[wave][d] = seen + __popcll(peers);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        rank[r] = seen + before;
+        rank[r] = digit_rank(base + r * 64 + lane < g.n, key[r] >> shift & 255, lane, hist[wave]);
     }
 
     // thread d: where digit d of this tile starts in the output
@@ -172,6 +176,75 @@ __global__ void __launch_bounds__(kThreads) sort_scatter(EmbedGeom g, SortIn in,
         const uint32_t dst = hist[wave][key[r] >> shift & 255] + rank[r];
         key_out[dst] = key[r];
         idx_out[dst] = idx[r];
+    }
+}
+
+// All passes for up to kSmall tokens by one workgroup, in LDS, and the runs' ends.
+constexpr int kSmall = 4096, kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
+__global__ void __launch_bounds__(kSmallThreads) sort_small(EmbedGeom g, const void *__restrict__ tok, int passes,
+                                                            uint32_t *__restrict__ key_out,
+                                                            uint32_t *__restrict__ idx_out,
+                                                            uint32_t *__restrict__ first,
+                                                            uint32_t *__restrict__ last)
+{
+    __shared__ uint32_t key[2][kSmall];
+    __shared__ uint16_t idx[2][kSmall];
+    __shared__ uint32_t hist[kSmallWaves][256];
+    __shared__ uint32_t scan[256];
+    const int t = threadIdx.x, wave = t >> 6, lane = t & 63, n = int(g.n);
+    const SortIn in{tok, nullptr, nullptr};
+    for (int i = t; i < n; i += kSmallThreads) {
+        key[0][i] = sort_key(g, in, i);
+        idx[0][i] = uint16_t(i);
+    }
+    const int rounds = (n + kSmallThreads - 1) / kSmallThreads;   // of 64 keys a wave, at most 4
+    int src = 0;
+    for (int pass = 0; pass < passes; ++pass, src ^= 1) {
+        const int shift = 8 * pass;
+        for (int i = t; i < kSmallWaves * 256; i += kSmallThreads) hist[i / 256][i % 256] = 0;
+        __syncthreads();
+        uint32_t rank[kSmall / kSmallThreads];
+#pragma unroll
+        for (int r = 0; r < kSmall / kSmallThreads; ++r) {
+            if (r >= rounds) break;
+            const int i = (wave * rounds + r) * 64 + lane;
+            rank[r] = digit_rank(i < n, i < n ? key[src][i] >> shift & 255 : 0, lane, hist[wave]);
+        }
+        __syncthreads();
+        uint32_t total = 0;
+        if (t < 256) {
+            for (int w = 0; w < kSmallWaves; ++w) {
+                const uint32_t c = hist[w][t];
+                hist[w][t] = total;
+                total += c;
+            }
+            scan[t] = total;
+        }
+        __syncthreads();
+        for (int w = 1; w < 256; w <<= 1) {
+            const uint32_t v = t < 256 && t >= w ? scan[t - w] : 0;
+            __syncthreads();
+            if (t < 256) scan[t] += v;
+            __syncthreads();
+        }
+#pragma unroll
+        for (int r = 0; r < kSmall / kSmallThreads; ++r) {
+            const int i = (wave * rounds + r) * 64 + lane;
+            if (r >= rounds || i >= n) break;
+            const uint32_t d = key[src][i] >> shift & 255;
+            const uint32_t dst = (d ? scan[d - 1] : 0) + hist[wave][d] + rank[r];
+            key[src ^ 1][dst] = key[src][i];
+            idx[src ^ 1][dst] = idx[src][i];
+        }
+        __syncthreads();
+    }
+    for (int i = t; i < n; i += kSmallThreads) {
+        const uint32_t k = key[src][i];
+        key_out[i] = k;
+        idx_out[i] = idx[src][i];
+        if (k >= uint32_t(g.V)) continue;
+        if (i == 0 || key[src][i - 1] != k) first[k] = i;
+        if (i + 1 == n || key[src][i + 1] != k) last[k] = i;
     }
 }
 
@@ -224,7 +297,7 @@ struct Partials {
     int levels;
 };
 
-// Level 0, and the runs' ends.
+// Level 0, and the runs' ends where `first` is not NULL.
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads) run_partials(EmbedGeom g, const T *__restrict__ dout,
                                                          const uint32_t *__restrict__ key,
@@ -235,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) run_partials(EmbedGeom g, const T *_
     const uint32_t p = blockIdx.x * (kThreads / team) + threadIdx.x / team;
     const uint32_t a = p * kRun;
     const int lane = threadIdx.x % team;
-    for (uint32_t i = a + lane; i < min(a + kRun, g.n); i += team) {
+    for (uint32_t i = a + lane; first && i < min(a + kRun, g.n); i += team) {
         const uint32_t k = key[i];
         if (k >= uint32_t(g.V)) continue;
         if (i == 0 || key[i - 1] != k) first[k] = i;
@@ -367,8 +440,7 @@ SortPlan plan(const EmbedGeom &g)
     while ((uint64_t(1) << bits) <= uint64_t(g.V)) ++bits;   // keys 0 .. V
     p.passes = (bits + 7) / 8;
     // a level pays from a few rows on
-    uint32_t rows = g.n / kRun;
-    for (; p.levels < kLevels && rows >= (p.levels ? 4u : 1u); rows /= kRun) p.rows[p.levels++] = rows;
+    for (uint32_t rows = g.n / kRun; p.levels < kLevels && rows >= 4; rows /= kRun) p.rows[p.levels++] = rows;
     size_t at = 0;
     for (int i = 0; i < 2; ++i) {
         p.key[i] = take(at, size_t(g.n) * 4);
@@ -414,10 +486,11 @@ hipError_t sums(const EmbedGeom &g, const SortPlan &p, const void *dout, const u
         q.part[l] = reinterpret_cast<float *>(ws + p.part[l]);
         q.rows[l] = p.rows[l];
     }
-    if (g.n) {
+    const bool noted = g.n <= uint32_t(kSmall);   // the runs' ends, by the sort
+    if (p.levels || !noted) {
         const uint32_t tiles = (g.n + kRun - 1) / kRun;
         hipLaunchKernelGGL((run_partials<T, N>), dim3((tiles + teams - 1) / teams), dim3(kThreads), 0, s, g,
-                           (const T *)dout, key, idx, q.part[0], first, last, team);
+                           (const T *)dout, key, idx, q.part[0], noted ? nullptr : first, last, team);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
     uint32_t span = kRun;
@@ -453,8 +526,15 @@ hipError_t launch_embed_grad_sort(const EmbedGeom &g, const void *tok, const voi
     uint32_t *counts = reinterpret_cast<uint32_t *>(base + p.counts);
     uint32_t *totals = reinterpret_cast<uint32_t *>(base + p.totals);
     SortIn in{tok, nullptr, nullptr};
+    const bool small = g.n <= uint32_t(kSmall);
+    if (small && g.n) {
+        hipLaunchKernelGGL(sort_small, dim3(1), dim3(kSmallThreads), 0, s, g, tok, p.passes, key[0], idx[0],
+                           reinterpret_cast<uint32_t *>(base + p.first), reinterpret_cast<uint32_t *>(base + p.last));
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+        in = SortIn{tok, key[0], idx[0]};
+    }
     int out = 0;
-    for (int pass = 0; pass < p.passes && g.n; ++pass) {
+    for (int pass = 0; pass < p.passes && !small; ++pass) {
         const hipError_t e = p.rounds == 16
             ? sort_pass<16>(g, p, in, 8 * pass, counts, totals, key[out], idx[out], s)
             : sort_pass<4>(g, p, in, 8 * pass, counts, totals, key[out], idx[out], s);

@@ -137,6 +137,7 @@ hipError_t launch_embed_grad_sort(const EmbedGeom &g, const void *tok, const voi
 
 // The gradient as a one-hot matrix product, for small vocabularies
 // (embed_grad_onehot.hip); needs D >= 2 and at least one token.
+int embed_grad_onehot_rows(int V);   // table rows, padded to its blocks
 size_t embed_grad_onehot_ws_bytes(const EmbedGeom &g);
 template <typename T>
 hipError_t launch_embed_grad_onehot(const EmbedGeom &g, const void *tok, const void *dout, void *dtable, float scale,

@@ -50,21 +50,32 @@ int check_embed(const gc_embed_desc *d, EmbedGeom *g)
     return GC_OK;
 }
 
-// The gradient's kernels: a one-hot product costs the same for every row of the
-// table, sorting the tokens the same for any number of rows.
-constexpr int kOnehotRows = 512;
-bool embed_onehot(const EmbedGeom &g) { return g.V <= kOnehotRows && g.D >= 2 && g.n > 0; }
-
-size_t embed_grad_ws_bytes(const EmbedGeom &g)
+// The gradient's kernels.  The one-hot product costs rows * slabs (of 32 columns) *
+// tokens, sorting hardly depends on the number of rows.  Measured (us, one-hot and
+// sort, bf16): 20,000 tokens, 32 columns, 1024 rows 36 and 65, 4096 rows 57 and 52;
+// 256 columns, 512 rows 55 and 79, 1024 rows 79 and 63; 400,000 tokens, 32 columns,
+// 1024 rows 79 and 147, 4096 rows 224 and 156; 500 tokens, 256 columns, 512 rows 21 and
+// 27, 1024 rows 32 and 24.  In fp32 the matrix cores take longer: 400,000 tokens, 32
+// columns, 256 rows 102 and 222, 1024 rows 284 and 196; 20,000 tokens, 256 columns, 256
+// rows 66 and 74, 512 rows 98 and 64.
+bool embed_onehot(const EmbedGeom &g, int dtype)
 {
-    return embed_onehot(g) ? embed_grad_onehot_ws_bytes(g) : embed_grad_sort_ws_bytes(g);
+    if (g.D < 2 || g.n == 0 || g.V > 4096) return false;
+    const int64_t cells = int64_t(embed_grad_onehot_rows(g.V)) * ((g.D + 31) / 32);
+    return dtype == GC_BF16 ? cells <= 4096 && cells * g.n <= 800000000
+                            : cells <= 2048 && cells * g.n <= 150000000;
+}
+
+size_t embed_grad_ws_bytes(const EmbedGeom &g, int dtype)
+{
+    return embed_onehot(g, dtype) ? embed_grad_onehot_ws_bytes(g) : embed_grad_sort_ws_bytes(g);
 }
 
 template <typename T>
 hipError_t embed_grad(const EmbedGeom &g, const void *tok, const void *dout, void *dtable, float scale, void *ws,
                       hipStream_t s)
 {
-    return embed_onehot(g) ? launch_embed_grad_onehot<T>(g, tok, dout, dtable, scale, ws, s)
+    return embed_onehot(g, sizeof(T) == 4 ? GC_F32 : GC_BF16) ? launch_embed_grad_onehot<T>(g, tok, dout, dtable, scale, ws, s)
                            : launch_embed_grad_sort<T>(g, tok, dout, dtable, scale, ws, s);
 }
 
@@ -189,7 +200,7 @@ size_t gc_embed_workspace_bytes(const gc_embed_desc *d, int dtype)
 {
     EmbedGeom g;
     if (check_embed(d, &g) != GC_OK || !valid_dtype(dtype)) return 0;
-    return embed_grad_ws_bytes(g);
+    return embed_grad_ws_bytes(g, dtype);
 }
 
 int gc_embed_bwd(const void *tokens, const void *dout, void *dtable, void *workspace, size_t ws_bytes,
@@ -201,7 +212,7 @@ int gc_embed_bwd(const void *tokens, const void *dout, void *dtable, void *works
     if (!valid_dtype(dtype) || !dtable || !aligned_to(dtable, dtype)) return GC_ERR_INVALID_ARG;
     if (g.n && (!tokens || !dout || !aligned(tokens, token_size(d->itype)) || !aligned_to(dout, dtype)))
         return GC_ERR_INVALID_ARG;
-    st = check_workspace(workspace, ws_bytes, embed_grad_ws_bytes(g));
+    st = check_workspace(workspace, ws_bytes, embed_grad_ws_bytes(g, dtype));
     if (st != GC_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     return hip_status(dtype == GC_F32 ? embed_grad<float>(g, tokens, dout, dtable, scale, workspace, s)
@@ -291,7 +302,7 @@ int gc_embed_plan_name(const gc_embed_desc *d, int dtype, char *buf, size_t buf_
     const int st = check_embed(d, &g);
     if (st != GC_OK) return st;
     if (!valid_dtype(dtype) || !buf || !buf_bytes) return GC_ERR_INVALID_ARG;
-    snprintf(buf, buf_bytes, "%s", embed_onehot(g) ? "embed_grad_onehot" : "embed_grad_sort");
+    snprintf(buf, buf_bytes, "%s", embed_onehot(g, dtype) ? "embed_grad_onehot" : "embed_grad_sort");
     return GC_OK;
 }
 

@@ -67,6 +67,15 @@ CASES = [
     (77, 13, 512, 2, "skewed", torch.int64, 0),
     (40, 300, 33, 31, "uniform", torch.int32, 1),
     (40, 300, 128, 1, "uniform", torch.int32, 1),
+    (16, 256, 9000, 300, "skewed", torch.int32, 0),     # 4096 tokens: the most that one workgroup sorts
+    (17, 241, 9000, 300, "skewed", torch.int32, 0),     # 4097
+    (1, 127, 70000, 130, "equal", torch.int64, 0),      # too few tokens for partial sums
+    (1, 128, 70000, 130, "equal", torch.int64, 0),
+    (3, 1365, 200000, 20, "uniform", torch.int32, 7),   # three sorting passes in one workgroup
+    (4, 2000, 200000, 20, "skewed", torch.int32, 0),    # and in several
+    (1, 1, 100000, 64, "uniform", torch.int32, 0),
+    (9, 100, 2500, 40, "skewed", torch.int32, 0),       # ten blocks of rows of the one-hot product
+    (1100, 1000, 5000, 4, "equal", torch.int32, 0),     # three levels of partial sums
 ]
 
 

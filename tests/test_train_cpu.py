@@ -218,8 +218,13 @@ def test_large_groups_are_split():
 
 
 def test_embedding_plans():
-    for V, D, name in ((128, 32, "onehot"), (512, 2, "onehot"), (513, 32, "sort"), (128, 1, "sort"), (40960, 1024, "sort")):
-        assert gb.gc_embed_plan_name(embed_desc(V=V, D=D, ld=3 * D), gb.GC_BF16) == "embed_grad_" + name
+    """Few cells (padded rows x 32-column slabs x tokens) are a one-hot product, others are sorted."""
+    for n, V, D, dtype, name in ((48128, 128, 32, 0, "onehot"), (1540096, 128, 32, 1, "onehot"), (12, 1024, 2, 0, "onehot"),
+                                 (12, 4000, 32, 1, "onehot"), (12, 4097, 32, 1, "sort"), (12, 4000, 32, 0, "sort"),
+                                 (400000, 512, 32, 0, "sort"), (400000, 512, 32, 1, "onehot"),
+                                 (12, 128, 1, 1, "sort"), (32768, 40960, 1024, 1, "sort")):
+        d = embed_desc(rows=n, tokens=1, V=V, D=D)
+        assert gb.gc_embed_plan_name(d, dtype) == "embed_grad_" + name, (n, V, D, dtype)
     assert gb.gc_embed_plan_name(embed_desc(rows=0), gb.GC_F32) == "embed_grad_sort"
 
 

@@ -35,12 +35,15 @@ def embed_bwd(tok, dout, V, scale):
     """The gradient, the sum of absolute values behind it and each row's number of tokens."""
     D = dout.shape[-1]
     ok = ((tok >= 0) & (tok < V)).reshape(-1)
-    t = tok.reshape(-1)[ok].long()
-    rows = dout.double().reshape(-1, D)[ok]
-    total, size = (torch.zeros((V, D), dtype=torch.float64, device=dout.device) for _ in range(2))
-    total.index_add_(0, t, rows * scale)
-    size.index_add_(0, t, (rows * scale).abs())
-    return total, size, torch.bincount(t, minlength=V)
+    # by sorted tokens: 64-bit atomics on one row take minutes where all tokens are equal
+    t, order = tok.reshape(-1)[ok].long().sort(stable=True)
+    rows = (dout.reshape(-1, D)[ok].double() * scale)[order]
+    counts = torch.searchsorted(t, torch.arange(V + 1, device=t.device)).diff()
+
+    def total(v):
+        return torch.segment_reduce(v, "sum", lengths=counts, axis=0, unsafe=True, initial=0.0)
+
+    return total(rows), total(rows.abs()), counts
 
 
 # -------------------------------------------------------------- group norm --
