@@ -167,6 +167,8 @@ hipError_t launch_norm_split_bwd(const NormGeom &g, const NormSplitPlan &q, cons
 struct NormResPlan {
     int N, NV;             // elements of a vector, vectors a thread holds
     int L, teams, threads; // threads of a team, teams of a workgroup, threads of a workgroup
+    int small;             // the small-group kernels (norm_res_small.hip)
+    int join;              // their backward writes one row of partials a workgroup
     int two;               // NCHW: vectors may straddle two channels
     int wave;              // channels last: a team is one wave
     int past;              // the output goes past the cache
@@ -194,6 +196,13 @@ template <typename T>
 hipError_t launch_norm_res_nhwc_bwd(const NormGeom &g, const NormResPlan &q, const void *x, const void *gamma,
                                     const void *beta, const void *dy, const float *mean, const float *rstd, void *dx,
                                     float *part, hipStream_t s);
+template <typename T>
+hipError_t launch_norm_res_small_fwd(const NormGeom &g, const NormResPlan &q, const void *x, const void *gamma,
+                                     const void *beta, void *y, float *mean, float *rstd, hipStream_t s);
+template <typename T>
+hipError_t launch_norm_res_small_bwd(const NormGeom &g, const NormResPlan &q, const void *x, const void *gamma,
+                                     const void *beta, const void *dy, const float *mean, const float *rstd, void *dx,
+                                     float *part, hipStream_t s);
 // dgamma and dbeta from `rows` rows of per-channel pairs (dbeta's, dgamma's)
 template <typename T>
 hipError_t launch_norm_params(const NormGeom &g, int64_t rows, const float *part, void *dgamma, void *dbeta,

@@ -36,6 +36,26 @@ __device__ __forceinline__ void set_param(const NormGeom &g, void *p, int c, flo
     else static_cast<T *>(p)[c] = from_f32<T>(v);
 }
 
+// gamma (or beta) of K neighbouring channels, each for N/K elements of v in a row.  One
+// wide load: lanes whose channels lie a vector apart would make a memory line of every
+// few lanes of each element load (50,000 x 128 x 1 x 2 bf16 forward 30 us that way, 13 this).
+template <int K, typename T, int N>
+__device__ __forceinline__ void near_params(const NormGeom &g, const void *p, int c, float none, float (&v)[N])
+{
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = none;
+    if (!p) return;
+    if (g.pf32) {
+        const Vec<float, K> w = load_vec<float, K>(static_cast<const float *>(p) + c);
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = w.get(j / (N / K));
+    } else {
+        const Vec<T, K> w = load_vec<T, K>(static_cast<const T *>(p) + c);
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = w.get(j / (N / K));
+    }
+}
+
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
 // Phi(z), the normal distribution function, and e = exp(-z^2/2): Abramowitz and

@@ -29,6 +29,10 @@ __device__ __forceinline__ uint32_t die_order(uint32_t id, uint32_t grid)
     return id < per * 8 ? id % 8 * per + id / 8 : id;
 }
 
+// Most vectors of N elements a thread of the small-group kernels holds: with constants
+// (and running sums) for each (NCHW), or for all of them (channels last).
+constexpr int small_vectors(int N, bool last) { return (last ? 32 : 16) / N; }
+
 // A team is one wave, or the workgroup: LDS traffic within a wave is in order.
 __device__ __forceinline__ void team_sync(bool wave)
 {
@@ -120,8 +124,12 @@ hipError_t with_nv(int nv, F f)
     switch (nv) {
     case 1: return f(std::integral_constant<int, 1>());
     case 2: return f(std::integral_constant<int, 2>());
-    case 3: return f(std::integral_constant<int, 3>());
-    case 4: return f(std::integral_constant<int, 4>());
+    case 3:
+        if constexpr (MOST >= 3) return f(std::integral_constant<int, 3>());
+        return hipErrorInvalidValue;
+    case 4:
+        if constexpr (MOST >= 4) return f(std::integral_constant<int, 4>());
+        return hipErrorInvalidValue;
     case 8:
         if constexpr (MOST >= 8) return f(std::integral_constant<int, 8>());
         return hipErrorInvalidValue;

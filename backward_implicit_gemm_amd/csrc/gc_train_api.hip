@@ -97,9 +97,8 @@ int check_norm(const gc_norm_desc *d, NormGeom *g)
         g->HW = int(hw);
         g->G = d->groups;
         g->Cg = d->C / d->groups;
-        // with one position or one channel both layouts are the same memory: taken as
-        // the one whose rows are long
-        g->nhwc = hw == 1 || (d->layout == GC_NHWC && d->C > 1);
+        // with one position or one channel both layouts are the same memory
+        g->nhwc = d->layout == GC_NHWC && hw > 1 && d->C > 1;
         g->act = d->act;
         g->eps = d->eps;
         g->img = hw * d->C;
@@ -145,6 +144,7 @@ hipError_t norm_fwd(const NormGeom &g, const NormSel &s, const void *x, const vo
                     float *mean, float *rstd, void *ws, hipStream_t st)
 {
     if (s.k == NormKind::Split) return launch_norm_split_fwd<T>(g, s.q, x, gamma, beta, y, mean, rstd, ws, st);
+    if (s.r.small) return launch_norm_res_small_fwd<T>(g, s.r, x, gamma, beta, y, mean, rstd, st);
     return g.nhwc ? launch_norm_res_nhwc_fwd<T>(g, s.r, x, gamma, beta, y, mean, rstd, st)
                   : launch_norm_res_nchw_fwd<T>(g, s.r, x, gamma, beta, y, mean, rstd, st);
 }
@@ -157,8 +157,9 @@ hipError_t norm_bwd(const NormGeom &g, const NormSel &s, const void *x, const vo
     if (s.k == NormKind::Split)
         return launch_norm_split_bwd<T>(g, s.q, x, gamma, beta, dy, mean, rstd, dx, dgamma, dbeta, ws, st);
     float *part = dgamma || dbeta ? static_cast<float *>(ws) : nullptr;
-    const hipError_t e = g.nhwc ? launch_norm_res_nhwc_bwd<T>(g, s.r, x, gamma, beta, dy, mean, rstd, dx, part, st)
-                                : launch_norm_res_nchw_bwd<T>(g, s.r, x, gamma, beta, dy, mean, rstd, dx, part, st);
+    const hipError_t e = s.r.small ? launch_norm_res_small_bwd<T>(g, s.r, x, gamma, beta, dy, mean, rstd, dx, part, st)
+                         : g.nhwc  ? launch_norm_res_nhwc_bwd<T>(g, s.r, x, gamma, beta, dy, mean, rstd, dx, part, st)
+                                   : launch_norm_res_nchw_bwd<T>(g, s.r, x, gamma, beta, dy, mean, rstd, dx, part, st);
     return e == hipSuccess && part ? launch_norm_params<T>(g, s.r.rows, part, dgamma, dbeta, st) : e;
 }
 
@@ -287,6 +288,9 @@ int gc_group_norm_plan_name(int op, const gc_norm_desc *d, int dtype, char *buf,
                  (long long)s.q.grid);
     else if (s.k == NormKind::None)
         snprintf(buf, buf_bytes, "none");
+    else if (s.r.small)
+        snprintf(buf, buf_bytes, "res_small_%s<N=%d,NV=%d,LAST=%d> threads=%d teams=%d grid=%lld", dir, s.r.N, s.r.NV,
+                 g.nhwc, s.r.L, s.r.teams, (long long)s.r.grid);
     else if (g.nhwc)
         snprintf(buf, buf_bytes, "res_nhwc_%s<N=%d,NV=%d,ONE=%d> threads=%d teams=%d slab=%d grid=%lld", dir, s.r.N,
                  s.r.NV, g.Cg % s.r.N == 0, s.r.L, s.r.teams, s.r.CW, (long long)s.r.grid);

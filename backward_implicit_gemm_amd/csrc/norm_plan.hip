@@ -37,11 +37,14 @@ int pow2_at_most(int64_t v)
     return p;
 }
 
-// Image slots of the backward: each walks B / at_once images, an equal number.
-int slots_of(int B, double at_once)
+// Image slots of the backward: each walks B / at_once images, an equal number, and
+// enough for its row of partials (8 bytes a channel) to be an eighth of their bytes at
+// most (`joined` slots share a row).
+int slots_of(const NormGeom &g, int size, double at_once, int joined = 1)
 {
-    const int each = std::max(1, int(B / std::max(1.0, at_once)));
-    return (B + each - 1) / each;
+    const int fill = (64 + 3 * g.HW * size * joined - 1) / (3 * g.HW * size * joined);
+    const int each = std::max(fill, int(g.B / std::max(1.0, at_once)));
+    return (g.B + each - 1) / each;
 }
 
 bool plan_nchw(const NormGeom &g, int widest, bool bwd, NormResPlan &best)
@@ -58,7 +61,9 @@ bool plan_nchw(const NormGeom &g, int widest, bool bwd, NormResPlan &best)
         for (int L = 1; L <= 1024; L *= 2) {
             if (int64_t(L) * NV < nvec || (L > 1 && int64_t(L) * NV >= 4 * nvec)) continue;
             if (NV > 16 || !holds(bwd, L, N, NV)) continue;
-            const double c = cost(double(g.B) * g.G, L, NV, 1.0);
+            // lanes of several teams read stretches of memory apart from each other
+            const double run = double(L) * N * (16 / widest);
+            const double c = cost(double(g.B) * g.G, L, NV, NV > 1 && run < 64 ? 64 / run : 1.0);
             if (c >= least) continue;
             NormResPlan q{};
             q.N = N;
@@ -71,9 +76,58 @@ bool plan_nchw(const NormGeom &g, int widest, bool bwd, NormResPlan &best)
             if (bwd) {
                 q.lds_bytes = std::max<size_t>(256, size_t(q.teams) * nvec * 2 * (two ? 2 : 1) * sizeof(float));
                 if (q.lds_bytes > kLdsMost) continue;
-                q.images = slots_of(g.B, kWavesAtOnce * 64 / (double(g.G) * L));
+                q.images = slots_of(g, 16 / widest, kWavesAtOnce * 64 / (double(g.G) * L));
                 q.rows = q.images;
                 q.grid = (int64_t(q.images) * g.G + q.teams - 1) / q.teams;
+            } else {
+                q.grid = (int64_t(g.B) * g.G + q.teams - 1) / q.teams;
+            }
+            if (q.grid > 0x7FFFFFFF) continue;
+            least = c;
+            best = q;
+        }
+    return least < 1e300;
+}
+
+// Small groups whose vectors hold several channels: NCHW planes shorter than a vector,
+// or channels last with rows of 1, 2, 4, ... whole vectors a group.
+bool plan_small(const NormGeom &g, int widest, bool bwd, NormResPlan &best)
+{
+    const int N = widest;
+    const int64_t M = int64_t(g.Cg) * g.HW;
+    int cv = 1;
+    if (g.nhwc) {
+        cv = g.Cg / N;
+        if (bwd || g.Cg % N || cv > 64 || (cv & (cv - 1))) return false;
+    } else if (g.HW >= N || M < N) {
+        return false;
+    }
+    const int64_t nvec = (M + N - 1) / N;
+    double least = 1e300;
+    for (int NV : kVectors)
+        for (int L = cv; L <= 64; L *= 2) {
+            if (NV > small_vectors(N, g.nhwc) || int64_t(L) * NV < nvec || (L > cv && int64_t(L) * NV >= 4 * nvec)) continue;
+            if (g.nhwc && int64_t(L / cv) * NV < g.HW) continue;
+            // the stretch of memory a wave reads at once
+            const double run = double(g.nhwc ? std::min<int64_t>(g.C, int64_t(64 / L) * g.Cg) : int64_t(L) * N) * (16 / widest);
+            if (g.nhwc && run < 64) continue;
+            const double c = cost(double(g.B) * g.G, L, NV, NV > 1 && run < 64 ? 64 / run : 1.0);
+            if (c >= least) continue;
+            NormResPlan q{};
+            q.small = 1;
+            q.N = N;
+            q.NV = NV;
+            q.L = L;
+            q.threads = kResThreads;
+            q.teams = kResThreads / L;
+            if (bwd) {
+                q.lds_bytes = size_t(q.teams) * M * 2 * sizeof(float);
+                if (q.lds_bytes > kLdsMost) continue;
+                const int joined = q.teams % g.G == 0 ? q.teams / g.G : 1;
+                q.join = joined > 1;
+                q.images = slots_of(g, 16 / widest, kWavesAtOnce * 64 / (double(g.G) * L), joined);
+                q.grid = (int64_t(q.images) * g.G + q.teams - 1) / q.teams;
+                q.rows = q.join ? int(q.grid) : q.images;
             } else {
                 q.grid = (int64_t(g.B) * g.G + q.teams - 1) / q.teams;
             }
@@ -125,7 +179,7 @@ bool plan_nhwc(const NormGeom &g, int widest, int size, bool bwd, NormResPlan &b
                     q.lds_bytes = lds;
                     if (lds > kLdsMost) continue;
                     if (bwd) {
-                        const int slots = slots_of(g.B, kWavesAtOnce * 64 / (double(slabs) * L));
+                        const int slots = slots_of(g, size, kWavesAtOnce * 64 / (double(slabs) * L), q.teams);
                         q.rows = (slots + q.teams - 1) / q.teams;
                         q.images = q.rows * q.teams;
                         q.grid = int64_t(q.rows) * slabs;
@@ -148,7 +202,7 @@ namespace {
 bool search(const NormGeom &g, int dtype, bool bwd, NormResPlan &q)
 {
     const int size = dtype == GC_F32 ? 4 : 2, widest = 16 / size;
-    const bool ok = g.nhwc ? plan_nhwc(g, widest, size, bwd, q) : plan_nchw(g, widest, bwd, q);
+    const bool ok = plan_small(g, widest, bwd, q) || (g.nhwc ? plan_nhwc(g, widest, size, bwd, q) : plan_nchw(g, widest, bwd, q));
     q.past = size_t(g.B) * g.img * size * (bwd ? 3 : 2) >= kStreamBytes;
     if (ok && bwd) q.ws_bytes = size_t(q.rows) * g.C * 2 * sizeof(float);
     return ok;

@@ -54,10 +54,11 @@ __global__ void __launch_bounds__(res_threads_fwd(N * NV))
                  float *__restrict__ rstd_out)
 {
     __shared__ float red[32];
+    const int64_t block = blockIdx.x;
     const int lane = threadIdx.x & (q.L - 1);
-    const int64_t k = int64_t(blockIdx.x) * q.teams + threadIdx.x / q.L;
-    const bool live = k < int64_t(g.B) * g.G;
     const int M = g.Cg * g.HW, nvec = (M + N - 1) / N;
+    const int64_t k = block * q.teams + threadIdx.x / q.L;
+    const bool live = k < int64_t(g.B) * g.G;
     const T *xp = x + k * M;
     Vec<T, N> v[NV];
 #pragma unroll

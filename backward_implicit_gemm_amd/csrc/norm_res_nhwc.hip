@@ -45,10 +45,10 @@ __global__ void __launch_bounds__(res_threads_fwd(N * NV))
                  const void *__restrict__ beta, T *__restrict__ y, float *__restrict__ mean_out,
                  float *__restrict__ rstd_out)
 {
-    constexpr int E = ONE ? 1 : N;
     extern __shared__ float lds[];
-    const uint32_t id = q.slabs > 1 ? die_order(blockIdx.x, gridDim.x) : blockIdx.x;
-    const int64_t unit = int64_t(id) * q.teams + threadIdx.x / q.L;   // (image, slab)
+    const int64_t block = q.slabs > 1 ? die_order(blockIdx.x, gridDim.x) : blockIdx.x;
+    constexpr int E = ONE ? 1 : N;
+    const int64_t unit = block * q.teams + threadIdx.x / q.L;   // (image, slab)
     const int slab = int(unit % q.slabs);
     const int64_t b = unit / q.slabs;
     const Place p = place<N>(q, slab);
@@ -66,11 +66,8 @@ __global__ void __launch_bounds__(res_threads_fwd(N * NV))
     int ge[E];   // groups of the thread's entries, within the slab
 #pragma unroll
     for (int e = 0; e < E; ++e) ge[e] = int(fdiv(uint32_t(p.c + e), g.fd_Cg)) - slab * q.Gs;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        a[j] = param<T>(g, gamma, p.c + j, 1.f);
-        be[j] = param<T>(g, beta, p.c + j, 0.f);
-    }
+    near_params<N, T>(g, gamma, p.c, 1.f, a);
+    near_params<N, T>(g, beta, p.c, 0.f, be);
 
     const float n = 1.f / (float(g.Cg) * float(g.HW));
     float m0[E], mean[E], rstd[E];
@@ -152,11 +149,8 @@ __global__ void __launch_bounds__(res_threads_bwd(N * NV))
     int ge[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) ge[e] = int(fdiv(uint32_t(p.c + e), g.fd_Cg)) - slab * q.Gs;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        a[j] = param<T>(g, gamma, p.c + j, 1.f);
-        be[j] = param<T>(g, beta, p.c + j, 0.f);
-    }
+    near_params<N, T>(g, gamma, p.c, 1.f, a);
+    near_params<N, T>(g, beta, p.c, 0.f, be);
     const float n = 1.f / (float(g.Cg) * float(g.HW));
     // a team that is a workgroup makes uniform trips; one that is a wave syncs by itself
     for (int img = first; img < g.B; img += q.images) {

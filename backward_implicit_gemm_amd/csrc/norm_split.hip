@@ -212,9 +212,9 @@ __device__ __forceinline__ void channel_constants(const NormGeom &g, int b, int 
         const int64_t k = int64_t(b) * g.G + fdiv(uint32_t(c + j), g.fd_Cg);
         cm[j] = mean[k];
         cr[j] = rstd[k];
-        cg[j] = param<T>(g, gamma, c + j, 1.f);
-        cb[j] = param<T>(g, beta, c + j, 0.f);
     }
+    near_params<NC, T>(g, gamma, c, 1.f, cg);
+    near_params<NC, T>(g, beta, c, 0.f, cb);
 }
 
 template <typename T, int N, bool NHWC, bool PAST>

@@ -278,10 +278,10 @@ def instances(most=4_000_000):
 
 
 @pytest.mark.parametrize("dtype", sorted(TYPES))
-@pytest.mark.parametrize("family", ["norm_split", "res_nchw", "res_nhwc"])
+@pytest.mark.parametrize("family", ["norm_split", "res_nchw", "res_nhwc", "res_small"])
 def test_every_instance(family, dtype):
     cases = {v[1:] for k, v in instances().items() if k[0].startswith(family) and k[1] == dtype}
-    assert len(cases) >= {"norm_split": 2, "res_nchw": 20, "res_nhwc": 20}[family]
+    assert len(cases) >= {"norm_split": 2, "res_nchw": 10, "res_nhwc": 20, "res_small": 5}[family]
     for i, (shape, G, layout) in enumerate(sorted(cases)):
         check(shape, G, ("silu", "relu", "gelu", "none")[i % 4], layout, TYPES[dtype], seed=20 + i)
 
@@ -289,7 +289,8 @@ def test_every_instance(family, dtype):
 @pytest.mark.parametrize("shape,G,layout,dtype", [
     ((8192, 128, 3, 4), 8, "nchw", "bf16"), ((8192, 128, 3, 4), 16, "nhwc", "bf16"),
     ((3, 256, 64, 67), 8, "nhwc", "f32"), ((4, 128, 128, 127), 4, "nchw", "bf16"),
-    ((500, 96, 11, 15), 32, "nchw", "f32"),
+    ((500, 96, 11, 15), 32, "nchw", "f32"), ((60000, 128, 1, 2), 16, "nchw", "bf16"),
+    ((60000, 128, 1, 2), 16, "nhwc", "f32"),
 ], ids=str)
 def test_outputs_past_the_cache(shape, G, layout, dtype):
     """Calls that move 64 MiB and more store their output past the cache."""
