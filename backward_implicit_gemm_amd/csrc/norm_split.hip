@@ -6,7 +6,7 @@
 //      sums; fp64 is entered once for up to kBlock values, summed in fp32 around the
 //      first of them.  Backward (g, g*hat) in fp32;
 //   2. per (image, group) the statistics (forward: mean, rstd; backward: c1, c2),
-//      one wave each, and for the backward dgamma and dbeta, one workgroup for 16
+//      one workgroup each, and for the backward dgamma and dbeta, one workgroup for 4
 //      channels, all in fixed orders;
 //   3. the elementwise pass over the same chunks.
 //
@@ -178,23 +178,33 @@ __global__ void __launch_bounds__(kThreads) norm_stats(NormGeom g, NormSplitPlan
     write_sums<double, N, NHWC>(g, q, w, b, s, t, part);
 }
 
-// One wave per (image, group).
+// One workgroup per (image, group): sums of w(c) * pair over the group's channels and
+// chunks, in a fixed order.
+template <typename V, typename W>
+__device__ __forceinline__ void group_pair(const NormGeom &g, int chunks, const V *__restrict__ part, int64_t b,
+                                           int c0, W w, V *red, V &s, V &t)
+{
+    s = t = 0;
+    for (int i = threadIdx.x; i < chunks * g.Cg; i += kThreads) {
+        uint32_t k, c;
+        fdivmod(uint32_t(i), g.fd_Cg, k, c);
+        const V *p = part + ((b * chunks + k) * g.C + c0 + c) * 2;
+        const V v = w(c0 + int(c));
+        s += v * p[0];
+        t += v * p[1];
+    }
+    s = block_sum(s, red);
+    t = block_sum(t, red);
+}
+
 __global__ void __launch_bounds__(kThreads) norm_finish(NormGeom g, int chunks, const double *__restrict__ part,
                                                         float *__restrict__ mean, float *__restrict__ rstd)
 {
-    const int64_t k = int64_t(blockIdx.x) * kWaves + (threadIdx.x >> 6);
-    if (k >= int64_t(g.B) * g.G) return;
-    const int b = int(k / g.G), lane = threadIdx.x & 63;
-    const int c0 = int(k % g.G) * g.Cg;
-    double s = 0, t = 0;
-    for (int i = lane; i < chunks * g.Cg; i += 64) {
-        const double *p = part + ((int64_t(b) * chunks + i / g.Cg) * g.C + c0 + i % g.Cg) * 2;
-        s += p[0];
-        t += p[1];
-    }
-    s = lanes_sum(s, 64);
-    t = lanes_sum(t, 64);
-    if (lane == 0) {
+    __shared__ double red[16];
+    const int64_t k = blockIdx.x;
+    double s, t;
+    group_pair(g, chunks, part, k / g.G, int(k % g.G) * g.Cg, [](int) { return 1.0; }, red, s, t);
+    if (threadIdx.x == 0) {
         const double n = double(g.Cg) * g.HW, m = s / n;
         const double var = fma(-m, m, t / n);
         mean[k] = float(m);
@@ -297,26 +307,16 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_sums(NormGeom g, NormSplitP
     write_sums<float, N, NHWC>(g, q, w, b, s, t, part);
 }
 
-// c1, c2 per (image, group), one wave each.
+// c1, c2 per (image, group).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) norm_bwd_groups(NormGeom g, int chunks, const float *__restrict__ part,
                                                             const void *__restrict__ gamma, float *__restrict__ cc)
 {
-    const int64_t k = int64_t(blockIdx.x) * kWaves + (threadIdx.x >> 6);
-    if (k >= int64_t(g.B) * g.G) return;
-    const int b = int(k / g.G), lane = threadIdx.x & 63;
-    const int c0 = int(k % g.G) * g.Cg;
-    float s = 0, t = 0;
-    for (int i = lane; i < chunks * g.Cg; i += 64) {
-        const int c = c0 + i % g.Cg;
-        const float *p = part + ((int64_t(b) * chunks + i / g.Cg) * g.C + c) * 2;
-        const float w = param<T>(g, gamma, c, 1.f);
-        s = fmaf(w, p[0], s);
-        t = fmaf(w, p[1], t);
-    }
-    s = lanes_sum(s, 64);
-    t = lanes_sum(t, 64);
-    if (lane == 0) {
+    __shared__ float red[16];
+    const int64_t k = blockIdx.x;
+    float s, t;
+    group_pair(g, chunks, part, k / g.G, int(k % g.G) * g.Cg, [&](int c) { return param<T>(g, gamma, c, 1.f); }, red, s, t);
+    if (threadIdx.x == 0) {
         const float n = 1.f / (float(g.Cg) * float(g.HW));
         cc[2 * k] = s * n;
         cc[2 * k + 1] = t * n;
@@ -416,7 +416,7 @@ size_t lds_bytes(const NormGeom &g, const NormSplitPlan &q, size_t size)
 bool plan_norm_split(const NormGeom &g, int dtype, NormSplitPlan &q)
 {
     q.N = vec_of(g, dtype == GC_F32 ? 4 : 8);
-    // about four workgroups a CU, and no chunk under 16 visits a thread
+    // about four workgroups a CU, and no chunk under 8 (NCHW 16) visits a thread
     if (g.nhwc) {
         const int cv = g.C / q.N;
         q.cols = std::min(cv, kThreads);
@@ -424,7 +424,7 @@ bool plan_norm_split(const NormGeom &g, int dtype, NormSplitPlan &q)
         q.slots = kThreads / q.cols;
         const int64_t units = int64_t(g.B) * q.blocks;
         int64_t chunks = std::max<int64_t>(1, 1024 / std::max<int64_t>(1, units));
-        chunks = std::min<int64_t>(chunks, std::max(1, g.HW / (16 * q.slots)));
+        chunks = std::min<int64_t>(chunks, std::max(1, g.HW / (8 * q.slots)));
         q.len = int((g.HW + chunks - 1) / chunks);
         q.chunks = (g.HW + q.len - 1) / q.len;
         q.grid = units * q.chunks;
@@ -452,7 +452,7 @@ bool plan_norm_split(const NormGeom &g, int dtype, NormSplitPlan &q)
     q.part_bytes_bwd = (pairs * 4 + 255) & ~size_t(255);
     q.ws_fwd = q.part_bytes_fwd + groups * 4;   // mean and rstd where the caller wants neither
     q.ws_bwd = q.part_bytes_bwd + groups * 4;
-    return q.grid <= 0x7FFFFFFF && int64_t(g.B) * g.G <= int64_t(0x7FFFFFFF) * kWaves;
+    return q.grid <= 0x7FFFFFFF && int64_t(g.B) * g.G <= 0x7FFFFFFF && int64_t(q.chunks) * g.Cg <= 0x7FFFFFFF;
 }
 
 // Launches KERNEL<T, N, layout, ...> over the plan's grid.
@@ -474,7 +474,7 @@ hipError_t split_fwd(const NormGeom &g, const NormSplitPlan &q, const T *x, cons
                      T *y, float *mean, float *rstd, double *part, hipStream_t s)
 {
     GC_NORM_LAUNCH(lds_bytes(g, q, 8), (x, part), norm_stats);
-    hipLaunchKernelGGL(norm_finish, dim3(unsigned((int64_t(g.B) * g.G + kWaves - 1) / kWaves)), dim3(kThreads), 0, s,
+    hipLaunchKernelGGL(norm_finish, dim3(unsigned(int64_t(g.B) * g.G)), dim3(kThreads), 0, s,
                        g, q.chunks, part, mean, rstd);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     if (q.past_fwd) GC_NORM_LAUNCH(0, (x, gamma, beta, mean, rstd, y), norm_apply, , true);
@@ -488,7 +488,7 @@ hipError_t split_bwd(const NormGeom &g, const NormSplitPlan &q, const T *x, cons
                      float *part, float *cc, hipStream_t s)
 {
     GC_NORM_LAUNCH(lds_bytes(g, q, 4), (x, dy, gamma, beta, mean, rstd, part), norm_bwd_sums);
-    hipLaunchKernelGGL(norm_bwd_groups<T>, dim3(unsigned((int64_t(g.B) * g.G + kWaves - 1) / kWaves)), dim3(kThreads),
+    hipLaunchKernelGGL(norm_bwd_groups<T>, dim3(unsigned(int64_t(g.B) * g.G)), dim3(kThreads),
                        0, s, g, q.chunks, part, gamma, cc);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     if (q.past_bwd) GC_NORM_LAUNCH(0, (x, dy, gamma, beta, mean, rstd, cc, dx), norm_bwd_apply, , true);
