@@ -171,6 +171,7 @@ struct NormResPlan {
     int join;              // their backward writes one row of partials a workgroup
     int two;               // NCHW: vectors may straddle two channels
     int wave;              // channels last: a team is one wave
+    int mix;               // channels last: 0 vectors mix groups, 1 lie in one, 2 do and the last of a row is moved back
     int past;              // the output goes past the cache
     int P;                 // lanes that add up one group (channels last) or channel (NCHW)
     int slots, CW, slabs, Gs;   // channels last: rows at a time; channels, number and groups of a slab

@@ -292,8 +292,8 @@ int gc_group_norm_plan_name(int op, const gc_norm_desc *d, int dtype, char *buf,
         snprintf(buf, buf_bytes, "res_small_%s<N=%d,NV=%d,LAST=%d> threads=%d teams=%d grid=%lld", dir, s.r.N, s.r.NV,
                  g.nhwc, s.r.L, s.r.teams, (long long)s.r.grid);
     else if (g.nhwc)
-        snprintf(buf, buf_bytes, "res_nhwc_%s<N=%d,NV=%d,ONE=%d> threads=%d teams=%d slab=%d grid=%lld", dir, s.r.N,
-                 s.r.NV, g.Cg % s.r.N == 0, s.r.L, s.r.teams, s.r.CW, (long long)s.r.grid);
+        snprintf(buf, buf_bytes, "res_nhwc_%s<N=%d,NV=%d,MIX=%d> threads=%d teams=%d slab=%d grid=%lld", dir, s.r.N,
+                 s.r.NV, s.r.mix, s.r.L, s.r.teams, s.r.CW, (long long)s.r.grid);
     else
         snprintf(buf, buf_bytes, "res_nchw_%s<N=%d,NV=%d,TWO=%d> threads=%d teams=%d grid=%lld", dir, s.r.N, s.r.NV,
                  s.r.two, s.r.L, s.r.teams, (long long)s.r.grid);

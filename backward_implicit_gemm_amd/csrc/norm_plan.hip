@@ -142,17 +142,18 @@ bool plan_nhwc(const NormGeom &g, int widest, int size, bool bwd, NormResPlan &b
 {
     double least = 1e300;
     for (int N = widest; N >= 1; N >>= 1) {
-        if (g.C % N) continue;
         // slabs of k whole groups, as wide as fits and no narrower than 64 bytes
         for (int k = g.G; k >= 1; --k) {
             if (g.G % k) continue;
             const int CW = k * g.Cg;
-            if (CW % N || (k < g.G && CW * size < 64)) continue;
-            const int CV = CW / N, slabs = g.G / k;
+            if (k == 1 ? CW < N : CW % N != 0) continue;
+            if (k < g.G && CW * size < 64) continue;
+            const int CV = (CW + N - 1) / N, slabs = g.G / k;
+            const int mix = CW % N ? 2 : g.Cg % N == 0 || k == 1;
             for (int NV : kVectors)
                 for (int L = 64; L <= 1024; L *= 2) {
                     if (!holds(bwd, L, N, NV) || CV > L) continue;
-                    if (!bwd && g.Cg % N && NV > kMixedMost) continue;
+                    if (!bwd && !mix && NV > kMixedMost) continue;
                     const int slots = L / CV;
                     if (int64_t(slots) * NV < g.HW) continue;
                     const double c = cost(double(g.B) * slabs, L, NV, CW * size < 128 && k < g.G ? 1.5 : 1.0);
@@ -168,10 +169,10 @@ bool plan_nhwc(const NormGeom &g, int widest, int size, bool bwd, NormResPlan &b
                     q.CW = CW;
                     q.slabs = slabs;
                     q.Gs = k;
-                    const bool one = g.Cg % N == 0;
-                    q.width = one ? CV : CW;
+                    q.mix = mix;
+                    q.width = mix ? CV : CW;
                     q.fd_cols = make_fastdiv(CV);
-                    q.fd_Eg = make_fastdiv(one ? g.Cg / N : g.Cg);
+                    q.fd_Eg = make_fastdiv(mix ? CV / k : g.Cg);
                     q.P = pow2_at_most(std::max(1, std::min(64, L / k)));
                     q.team_lds = 2 * q.slots * q.width + 2 * k;
                     size_t lds = size_t(q.teams) * q.team_lds * sizeof(float);

@@ -6,8 +6,10 @@
 // vector col of the slab and holds positions slot, slot + slots, ..., so its
 // channel constants stay in registers and a row is read by neighbouring threads.
 // Group sums go through LDS: one entry a thread where a vector lies in one
-// group (ONE), else one for each of its channels, added up by P lanes a group in
-// a fixed order.  The forward takes the mean, then the squares around it (with
+// group (kOne), else one for each of its channels (kMixed), added up by P lanes a
+// group in a fixed order.  A slab that is one group need not be whole vectors wide: the
+// last one of a row is moved back to end with it (kTail; its first `skip` elements are
+// another vector's).  The forward takes the mean, then the squares around it (with
 // the remaining sum, so the mean's own rounding drops out).  The backward's
 // team walks images slot, slot + images, ..., keeping the channels' running sums of g
 // and g*hat in registers; the teams of a workgroup join them at the end into one
@@ -19,12 +21,15 @@
 namespace gc {
 namespace {
 
+enum { kMixed, kOne, kTail };
+
 struct Place {
     int tt, team, slot, col, c;   // thread of the team, team, row slot, vector, first channel
+    int skip;                     // kTail: leading elements that another vector holds
     bool live;
 };
 
-template <int N>
+template <int N, int MIX>
 __device__ __forceinline__ Place place(const NormResPlan &q, int slab)
 {
     Place p;
@@ -35,11 +40,13 @@ __device__ __forceinline__ Place place(const NormResPlan &q, int slab)
     p.slot = int(s);
     p.col = int(c);
     p.live = p.slot < q.slots;
-    p.c = slab * q.CW + (p.live ? p.col * N : 0);
+    const int at = p.live ? MIX == kTail ? min(p.col * N, q.CW - N) : p.col * N : 0;
+    p.skip = MIX == kTail && p.live ? p.col * N - at : 0;
+    p.c = slab * q.CW + at;
     return p;
 }
 
-template <typename T, int N, int NV, bool ONE, bool PAST>
+template <typename T, int N, int NV, int MIX, bool PAST>
 __global__ void __launch_bounds__(res_threads_fwd(N * NV))
     res_nhwc_fwd(NormGeom g, NormResPlan q, const T *__restrict__ x, const void *__restrict__ gamma,
                  const void *__restrict__ beta, T *__restrict__ y, float *__restrict__ mean_out,
@@ -47,11 +54,12 @@ __global__ void __launch_bounds__(res_threads_fwd(N * NV))
 {
     extern __shared__ float lds[];
     const int64_t block = q.slabs > 1 ? die_order(blockIdx.x, gridDim.x) : blockIdx.x;
+    constexpr bool ONE = MIX != kMixed;
     constexpr int E = ONE ? 1 : N;
     const int64_t unit = block * q.teams + threadIdx.x / q.L;   // (image, slab)
     const int slab = int(unit % q.slabs);
     const int64_t b = unit / q.slabs;
-    const Place p = place<N>(q, slab);
+    const Place p = place<N, MIX>(q, slab);
     const bool live = p.live && b < g.B;
     float *red = lds + p.team * q.team_lds, *stat = red + 2 * q.slots * q.width;
     const T *xp = x + b * g.img + p.c;
@@ -76,7 +84,8 @@ __global__ void __launch_bounds__(res_threads_fwd(N * NV))
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < N; ++j) s[0][ONE ? 0 : j] += v[i].get(j);
+            for (int j = 0; j < N; ++j)
+                if (MIX != kTail || j >= p.skip) s[0][ONE ? 0 : j] += v[i].get(j);
         team_groups<1, E>(q, p.live, p.tt, p.slot, p.col, s, red, stat);
 #pragma unroll
         for (int e = 0; e < E; ++e) m0[e] = stat[ge[e]] * n;
@@ -89,6 +98,7 @@ __global__ void __launch_bounds__(res_threads_fwd(N * NV))
             if (p.slot + i * q.slots >= g.HW) continue;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
+                if (MIX == kTail && j < p.skip) continue;
                 const float d = v[i].get(j) - m0[ONE ? 0 : j];
                 s[0][ONE ? 0 : j] += d;
                 s[1][ONE ? 0 : j] = fmaf(d, d, s[1][ONE ? 0 : j]);
@@ -130,19 +140,20 @@ __global__ void __launch_bounds__(res_threads_fwd(N * NV))
     }
 }
 
-template <typename T, int N, int NV, bool ONE, bool PAST>
+template <typename T, int N, int NV, int MIX, bool PAST>
 __global__ void __launch_bounds__(res_threads_bwd(N * NV))
     res_nhwc_bwd(NormGeom g, NormResPlan q, const T *__restrict__ x, const T *__restrict__ dy,
                  const void *__restrict__ gamma, const void *__restrict__ beta, const float *__restrict__ mean,
                  const float *__restrict__ rstd, T *__restrict__ dx, float *__restrict__ part)
 {
+    constexpr bool ONE = MIX != kMixed;
     constexpr int E = ONE ? 1 : N;
     extern __shared__ float lds[];
     // a workgroup: one slab, `teams` image slots
     const uint32_t id = q.slabs > 1 ? die_order(blockIdx.x, gridDim.x) : blockIdx.x;
     const int slab = int(id % q.slabs);
     const int row0 = int(id / q.slabs);
-    const Place p = place<N>(q, slab);
+    const Place p = place<N, MIX>(q, slab);
     const int first = row0 * q.teams + p.team;
     float *red = lds + p.team * q.team_lds, *stat = red + 2 * q.slots * q.width;
     float a[N], be[N], sg[N] = {}, st[N] = {};
@@ -189,6 +200,7 @@ __global__ void __launch_bounds__(res_threads_bwd(N * NV))
             act_grad<N, N>(g.act, h[i], d[i], m, r, a, be);
 #pragma unroll
             for (int j = 0; j < N; ++j) {
+                if (MIX == kTail && j < p.skip) continue;
                 s[j] += d[i][j];
                 t[j] = fmaf(d[i][j], h[i][j], t[j]);
             }
@@ -224,9 +236,10 @@ __global__ void __launch_bounds__(res_threads_bwd(N * NV))
     if (!part) return;
     __syncthreads();
     if (p.live) {
-        float *mine = lds + ((p.team * q.slots + p.slot) * q.CW + p.col * N) * 2;
+        float *mine = lds + ((p.team * q.slots + p.slot) * q.CW + p.c - slab * q.CW) * 2;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
+            if (MIX == kTail && j < p.skip) continue;
             mine[2 * j] = sg[j];
             mine[2 * j + 1] = st[j];
         }
@@ -250,10 +263,22 @@ hipError_t launch_norm_res_nhwc_fwd(const NormGeom &g, const NormResPlan &q, con
             constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
             return with_past<(sizeof(T) * N >= 8)>(q.past, [&](auto past) {
             constexpr bool P = decltype(past)::value;
-            if (g.Cg % N == 0)
-                hipLaunchKernelGGL((res_nhwc_fwd<T, N, NV, true, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s, g, q, (const T *)x, gamma, beta, (T *)y, mean, rstd);
-            else if constexpr (N > 1 && NV <= kMixedMost)
-                hipLaunchKernelGGL((res_nhwc_fwd<T, N, NV, false, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s, g, q, (const T *)x, gamma, beta, (T *)y, mean, rstd);
+            if (q.mix == kOne) {
+                hipLaunchKernelGGL((res_nhwc_fwd<T, N, NV, kOne, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s,
+                                   g, q, (const T *)x, gamma, beta, (T *)y, mean, rstd);
+            } else if (q.mix == kTail) {
+                if constexpr (N > 1)
+                    hipLaunchKernelGGL((res_nhwc_fwd<T, N, NV, kTail, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s,
+                                   g, q, (const T *)x, gamma, beta, (T *)y, mean, rstd);
+                else
+                    return hipErrorInvalidValue;
+            } else {
+                if constexpr (N > 1 && NV <= kMixedMost)
+                    hipLaunchKernelGGL((res_nhwc_fwd<T, N, NV, kMixed, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s,
+                                   g, q, (const T *)x, gamma, beta, (T *)y, mean, rstd);
+                else
+                    return hipErrorInvalidValue;
+            }
             return hipGetLastError();
             });
         });
@@ -270,12 +295,22 @@ hipError_t launch_norm_res_nhwc_bwd(const NormGeom &g, const NormResPlan &q, con
             constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
             return with_past<(sizeof(T) * N >= 8)>(q.past, [&](auto past) {
             constexpr bool P = decltype(past)::value;
-            if (g.Cg % N == 0)
-                hipLaunchKernelGGL((res_nhwc_bwd<T, N, NV, true, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s, g, q, (const T *)x, (const T *)dy, gamma, beta, mean, rstd,
-                                   (T *)dx, part);
-            else if constexpr (N > 1)
-                hipLaunchKernelGGL((res_nhwc_bwd<T, N, NV, false, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s, g, q, (const T *)x, (const T *)dy, gamma, beta, mean, rstd,
-                                   (T *)dx, part);
+            if (q.mix == kOne) {
+                hipLaunchKernelGGL((res_nhwc_bwd<T, N, NV, kOne, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s,
+                                   g, q, (const T *)x, (const T *)dy, gamma, beta, mean, rstd, (T *)dx, part);
+            } else if (q.mix == kTail) {
+                if constexpr (N > 1)
+                    hipLaunchKernelGGL((res_nhwc_bwd<T, N, NV, kTail, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s,
+                                   g, q, (const T *)x, (const T *)dy, gamma, beta, mean, rstd, (T *)dx, part);
+                else
+                    return hipErrorInvalidValue;
+            } else {
+                if constexpr (N > 1)
+                    hipLaunchKernelGGL((res_nhwc_bwd<T, N, NV, kMixed, P>), dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s,
+                                   g, q, (const T *)x, (const T *)dy, gamma, beta, mean, rstd, (T *)dx, part);
+                else
+                    return hipErrorInvalidValue;
+            }
             return hipGetLastError();
             });
         });
