@@ -36,6 +36,7 @@ struct Part {
     int p, p1, step;   // first position, end, distance between visits
     int64_t base;      // element offset of (image, channel c, position 0)
     int chunk, slot;   // NHWC: the thread's row slot
+    int mine;          // NHWC: first of the N channels that no other vector holds
 };
 
 template <int N, bool NHWC>
@@ -53,7 +54,9 @@ __device__ __forceinline__ Part<N, NHWC> part_of(const NormGeom &g, const NormSp
         w.slot = threadIdx.x / q.cols;
         const int col = block * q.cols + threadIdx.x % q.cols;
         w.live = w.slot < q.slots && col * N < g.C;
-        w.c = col * N;
+        // the last vector of a row is moved back to end with it
+        w.c = min(col * N, g.C - N);
+        w.mine = col * N - w.c;
         w.p = w.chunk * q.len + w.slot;
         w.step = q.slots;
         w.base = int64_t(b) * g.img + w.c;
@@ -66,7 +69,7 @@ __device__ __forceinline__ Part<N, NHWC> part_of(const NormGeom &g, const NormSp
         k /= q.chunks;
         w.live = k < uint64_t(g.B);
         b = int(k);
-        w.slot = 0;
+        w.slot = w.mine = 0;
         w.p = w.chunk * q.len + lane * N;
         w.step = 64 * N;
         w.base = int64_t(b) * g.img + int64_t(w.c) * g.HW;
@@ -95,21 +98,23 @@ __device__ __forceinline__ void write_sums(const NormGeom &g, const NormSplitPla
         extern __shared__ char lds[];
         V *red = reinterpret_cast<V *>(lds);   // [slot][cols*N][2]
         const int width = q.cols * N;
-        if (w.slot < q.slots) {
+        const int c0 = int(blockIdx.x % q.blocks) * width;
+        if (w.live) {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const int e = (w.slot * width + (threadIdx.x % q.cols) * N + j) * 2;
-                red[e] = w.live ? s[NHWC ? j : 0] : V(0);
-                red[e + 1] = w.live ? t[NHWC ? j : 0] : V(0);
+                if (j < w.mine) continue;
+                const int e = (w.slot * width + w.c - c0 + j) * 2;
+                red[e] = s[NHWC ? j : 0];
+                red[e + 1] = t[NHWC ? j : 0];
             }
         }
         __syncthreads();
-        const int c0 = int(blockIdx.x % q.blocks) * width;
         for (int e = threadIdx.x; e < 2 * width; e += kThreads) {
+            const int c = c0 + e / 2;
+            if (c >= g.C) continue;
             V v = 0;
             for (int r = 0; r < q.slots; ++r) v += red[r * 2 * width + e];
-            const int c = c0 + e / 2;
-            if (c < g.C) part[((int64_t(b) * q.chunks + w.chunk) * g.C + c) * 2 + e % 2] = v;
+            part[((int64_t(b) * q.chunks + w.chunk) * g.C + c) * 2 + e % 2] = v;
         }
     } else {
         const V a = lanes_sum(s[0], 64), d = lanes_sum(t[0], 64);
@@ -399,10 +404,7 @@ __global__ void __launch_bounds__(1024) norm_params(NormGeom g, int64_t rows, co
 int vec_of(const NormGeom &g, int widest)
 {
     int n = widest;
-    if (g.nhwc)
-        while (n > 1 && g.C % n) n >>= 1;
-    else
-        while (n > 1 && g.HW < n) n >>= 1;
+    while (n > 1 && (g.nhwc ? g.C : g.HW) < n) n >>= 1;
     return n;
 }
 
@@ -418,7 +420,7 @@ bool plan_norm_split(const NormGeom &g, int dtype, NormSplitPlan &q)
     q.N = vec_of(g, dtype == GC_F32 ? 4 : 8);
     // about four workgroups a CU, and no chunk under 8 (NCHW 16) visits a thread
     if (g.nhwc) {
-        const int cv = g.C / q.N;
+        const int cv = (g.C + q.N - 1) / q.N;
         q.cols = std::min(cv, kThreads);
         q.blocks = (cv + q.cols - 1) / q.cols;
         q.slots = kThreads / q.cols;
