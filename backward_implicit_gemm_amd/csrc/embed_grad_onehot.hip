@@ -20,7 +20,7 @@
 // The waves' sums are joined in LDS in order, each workgroup writes one partial, and a
 // second launch adds the partials in order: bit-reproducible.  Bound by memory in
 // bf16 at 128 rows (making O is next: 12 vector instructions for 16 rows of a step):
-// the rollout's 98 MB take 28 us and the sums 5, in fp32 the minibatch's 6 MB 11 and 4.
+// the rollout's 98 MB take 28 us and the sums 5, in fp32 the minibatch's 6 MB 13 and 4.
 #include <algorithm>
 
 #include "gc_embed.h"

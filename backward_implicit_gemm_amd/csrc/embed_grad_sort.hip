@@ -16,8 +16,10 @@
 //      boundary, partials to the first boundary of the next level, and so on up and
 //      down again.  Rows without a token are written as zeros; they are known by
 //      their noted place not being a run of theirs, so the notes need no clearing.
-// Bound by memory: dout is gathered once by rows, dtable written once; at few
-// tokens by the chain of launches.
+// Bound by memory: dout is gathered once by rows, dtable written once (32,768 tokens, 40,960
+// rows of 1024 bf16: rows 35 us for 146 MB, runs 7 and 5, sort 22); at few tokens by the chain
+// of launches.  Bisecting the keys for every row, with rows in order and runs of 64, took
+// 222 us for the call instead of 64.
 #include <algorithm>
 
 #include "gc_embed.h"

@@ -146,6 +146,8 @@ hipError_t launch_embed_grad_onehot(const EmbedGeom &g, const void *tok, const v
 // Group norm with an activation.  The split kernels (norm_split.hip) take every
 // shape; plan_norm_split returns false past the largest grid.
 struct NormGeom;
+// A launch has to stay below 2^32 threads.
+inline bool launchable(int64_t grid, int threads) { return grid * threads < int64_t(1) << 32; }
 struct NormSplitPlan {
     int N;                     // elements of a thread's vector
     int cols, blocks, slots;   // channels last: vectors of a workgroup's row, column blocks, rows at a time

@@ -82,6 +82,8 @@ hipError_t embed_grad(const EmbedGeom &g, const void *tok, const void *dout, voi
 uintptr_t token_size(int itype) { return itype == GC_I32 ? 4 : itype == GC_I64 ? 8 : 1; }
 
 // ---------------------------------------------------------------- group norm --
+constexpr int kNormMost = 1 << 30, kNormChannels = 1 << 23;
+
 int check_norm(const gc_norm_desc *d, NormGeom *g)
 {
     if (!d || d->B < 1 || d->C < 1 || d->H < 1 || d->W < 1 || d->groups < 1) return GC_ERR_INVALID_ARG;
@@ -90,7 +92,9 @@ int check_norm(const gc_norm_desc *d, NormGeom *g)
     if (d->act < GC_ACT_NONE || d->act > GC_ACT_GELU) return GC_ERR_INVALID_ARG;
     if (!(d->eps >= 0.f) || isinf(d->eps)) return GC_ERR_INVALID_ARG;
     const int64_t hw = (int64_t)d->H * d->W;
-    if (hw > INT_MAX || (__int128)hw * d->C > INT_MAX) return GC_ERR_INVALID_ARG;
+    // so that the kernels' counters, a stride past the end, stay within 31 bits and no
+    // launch over the channels reaches 2^32 threads
+    if (d->B > kNormMost || d->C > kNormChannels || hw > kNormMost || hw * d->C > kNormMost) return GC_ERR_INVALID_ARG;
     if (g) {
         g->B = d->B;
         g->C = d->C;

@@ -82,7 +82,7 @@ bool plan_nchw(const NormGeom &g, int widest, bool bwd, NormResPlan &best)
             } else {
                 q.grid = (int64_t(g.B) * g.G + q.teams - 1) / q.teams;
             }
-            if (q.grid > 0x7FFFFFFF) continue;
+            if (!launchable(q.grid, q.threads)) continue;
             least = c;
             best = q;
         }
@@ -131,7 +131,7 @@ bool plan_small(const NormGeom &g, int widest, bool bwd, NormResPlan &best)
             } else {
                 q.grid = (int64_t(g.B) * g.G + q.teams - 1) / q.teams;
             }
-            if (q.grid > 0x7FFFFFFF) continue;
+            if (!launchable(q.grid, q.threads)) continue;
             least = c;
             best = q;
         }
@@ -143,7 +143,8 @@ bool plan_nhwc(const NormGeom &g, int widest, int size, bool bwd, NormResPlan &b
     double least = 1e300;
     for (int N = widest; N >= 1; N >>= 1) {
         // slabs of k whole groups, as wide as fits and no narrower than 64 bytes
-        for (int k = g.G; k >= 1; --k) {
+        const int most = std::max(1, std::min(g.G, 1024 * N / g.Cg));   // a row is 1024 vectors at most
+        for (int k = most; k >= 1; --k) {
             if (g.G % k) continue;
             const int CW = k * g.Cg;
             if (k == 1 ? CW < N : CW % N != 0) continue;
@@ -187,7 +188,7 @@ bool plan_nhwc(const NormGeom &g, int widest, int size, bool bwd, NormResPlan &b
                     } else {
                         q.grid = (int64_t(g.B) * slabs + q.teams - 1) / q.teams;
                     }
-                    if (q.grid > 0x7FFFFFFF) continue;
+                    if (!launchable(q.grid, q.threads)) continue;
                     least = c;
                     best = q;
                 }

@@ -13,7 +13,8 @@
 // group's channel constants, walks images slot, slot + slots, ..., and adds
 // each vector's g and g*hat to running sums of its own; only after its last
 // image are those added up by channel, in LDS, into one row of partials a slot.
-// Bound by memory.
+// Bound by memory: 1024 x 128 x 3 x 4 forward fp32 5.5 us (12.6 MB), backward bf16 6.9 (9.4 MB);
+// 300 x 32 x 32 x 32 fp32 forward 13.6 us, 5.8 TB/s.
 #include <type_traits>
 
 #include "gc_norm_res.h"

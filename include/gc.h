@@ -230,7 +230,8 @@ int gc_embed_bwd(const void *tokens, const void *dout, void *dtable, void *works
  * beta, dgamma and dbeta [C] have param_dtype, GC_F32 or dtype; gamma == NULL
  * stands for ones, beta == NULL for zeros.  mean and rstd are fp32
  * [B][groups]; the forward writes them where they are not NULL, the backward
- * reads them.  C*H*W is below 2^31; B*C*H*W may be larger. */
+ * reads them.  C is at most 2^23, C*H*W and B at most 2^30; B*C*H*W may be
+ * larger: GC_ERR_UNSUPPORTED only where a launch would need 2^32 threads. */
 typedef enum { GC_NCHW = 0, GC_NHWC = 1 } gc_layout;
 typedef enum {
     GC_ACT_NONE = 0,

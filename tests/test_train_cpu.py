@@ -3,6 +3,8 @@ invalid call is turned away before the first HIP call, by the binding or by
 the C ABI, so these run without a GPU.
 """
 import ctypes
+import re
+import time
 
 import pytest
 import torch
@@ -74,6 +76,7 @@ def norm_bwd(d, ws=FAKE, n=BIG, dtype=0, pt=0, **p):
     dict(B=0), dict(C=0), dict(H=0), dict(W=-1), dict(groups=0), dict(groups=5), dict(groups=24), dict(layout=2),
     dict(act=4), dict(act=-1), dict(eps=-1e-9), dict(eps=float("nan")), dict(eps=float("inf")),
     dict(H=1 << 16, W=1 << 16), dict(C=1 << 12, groups=1, H=1 << 10, W=1 << 10),
+    dict(B=(1 << 30) + 1), dict(H=1, W=(1 << 30) + 1, C=1, groups=1), dict(C=(1 << 23) + 1, groups=1, H=1, W=1),
 ])
 def test_norm_descriptors(change):
     d = norm_desc(**change)
@@ -215,6 +218,25 @@ def test_large_groups_are_split():
     for layout in (gb.GC_NCHW, gb.GC_NHWC):
         for op in (gb.GC_OP_FWD, gb.GC_OP_BWD):
             assert norm_plan(op, (2, 64, 300, 300), 1, layout, gb.GC_BF16).startswith("norm_split")
+
+
+def test_plans_of_extreme_shapes():
+    """The most images, channels, groups and positions: grids and workspaces without overflow, found without a walk."""
+    most, wide = 2 ** 30, 2 ** 23
+    for shape, groups in (((1, wide, 1, 1), wide), ((1, wide, 1, 1), 1), ((1, 1, 1, most), 1), ((1, wide, 1, 1), wide // 2),
+                          ((most, 1, 1, 1), 1), ((most, 8, 16, 16), 8), ((1, wide, 1, 2), 1), ((most, 64, 1, 2), 8),
+                          ((3, 7, 1, most // 7), 7), ((most, 512, 3, 4), 1), ((2 ** 20, wide, 8, 16), 1)):
+        for layout in (gb.GC_NCHW, gb.GC_NHWC):
+            for dtype in (gb.GC_F32, gb.GC_BF16):
+                for op in (gb.GC_OP_FWD, gb.GC_OP_BWD):
+                    start = time.monotonic()
+                    name = norm_plan(op, shape, groups, layout, dtype)
+                    d = gb.gc_norm_desc(*shape, groups, layout, 0, 1e-5)
+                    need = gb.lib().gc_group_norm_workspace_bytes(op, ctypes.byref(d), dtype)
+                    assert time.monotonic() - start < 0.5, (shape, groups)
+                    assert need < 2 ** 45, (shape, groups, need)
+                    numbers = [int(v) for v in re.findall(r"(?:grid|chunks)=(-?[0-9]+)", name)]
+                    assert name == "none" or (numbers and min(numbers) >= 1 and max(numbers) < 2 ** 31), name
 
 
 def test_embedding_plans():
