@@ -3,8 +3,10 @@
 //
 //   1. channel sums over a chunk of positions, partial[image][chunk][channel]:
 //      forward (x, x^2) in fp64, so that the variance can be a difference of two large
-//      sums; fp64 is entered once for up to kBlock values, summed in fp32 around the
-//      first of them.  Backward (g, g*hat) in fp32;
+//      sums; fp64 is entered once for the kUnroll vectors that a thread has in flight, summed
+//      in fp32 around their mean.  Around the first of 32 vectors' values the time is the same
+//      within 5 % (64 x 64 x 128 x 128 fp32 135 us, 16 x 320 x 64 x 64 channels last bf16 35),
+//      but a first value far from the others put 3e-5 on rstd.  Backward (g, g*hat) in fp32;
 //   2. per (image, group) the statistics (forward: mean, rstd; backward: c1, c2),
 //      one workgroup each, and for the backward dgamma and dbeta, one workgroup for 4
 //      channels, all in fixed orders;
@@ -27,7 +29,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kUnroll = 4;     // vectors a thread has in flight
-constexpr int kBlock = 32;     // vectors whose values are summed in fp32 around the first
 
 // Positions [p0, p1) of image b and the channels this thread works on.
 template <int N, bool NHWC>
@@ -137,42 +138,40 @@ __global__ void __launch_bounds__(kThreads) norm_stats(NormGeom g, NormSplitPlan
     const Part<N, NHWC> w = part_of<N, NHWC>(g, q, b);
     double s[NC] = {}, t[NC] = {};
     if (w.live) {
-        int p = w.p;
-        while (p < w.p1) {
-            // sum of x = n*o + fs, of x^2 = n*o^2 + 2*o*fs + ft, o the first value.  An o far
-            // from the others adds n times its own square, so rounding relative to that is
-            // relative to the sum as well.
-            float o[NC], fs[NC] = {}, ft[NC] = {}, n = 0;
-            for (int k = 0; k < kBlock && p < w.p1; k += kUnroll) {
-                Vec<T, N> v[kUnroll];
-                int skip[kUnroll];
+        for (int p = w.p; p < w.p1; p += kUnroll * w.step) {
+            Vec<T, N> v[kUnroll];
+            int skip[kUnroll];
+            float n = 0;
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    skip[u] = N;   // nothing there
-                    v[u] = Vec<T, N>{};
-                    if (p + u * w.step < w.p1) {
-                        skip[u] = 0;
-                        const int at = NHWC ? p + u * w.step : pulled_back<N>(p + u * w.step, w.p1, skip[u]);
-                        v[u] = load_vec<T, N>(x + w.base + (NHWC ? int64_t(at) * g.C : at));
-                    }
+            for (int u = 0; u < kUnroll; ++u) {
+                skip[u] = N;   // nothing there
+                v[u] = Vec<T, N>{};
+                if (p + u * w.step < w.p1) {
+                    skip[u] = 0;
+                    const int at = NHWC ? p + u * w.step : pulled_back<N>(p + u * w.step, w.p1, skip[u]);
+                    v[u] = load_vec<T, N>(x + w.base + (NHWC ? int64_t(at) * g.C : at));
                 }
-                if (k == 0) {
-#pragma unroll
-                    for (int e = 0; e < NC; ++e) o[e] = v[0].get(NC == 1 ? N - 1 : e);
-                }
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    n += NHWC ? (skip[u] ? 0.f : 1.f) : float(N - skip[u]);
-#pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        const int e = NC == 1 ? 0 : j;
-                        const float d = j < skip[u] ? 0.f : v[u].get(j) - o[e];
-                        fs[e] += d;
-                        ft[e] = fmaf(d, d, ft[e]);
-                    }
-                }
-                p += kUnroll * w.step;
+                n += NHWC ? (skip[u] ? 0.f : 1.f) : float(N - skip[u]);
             }
+            // sum of x = n*o + fs, of x^2 = n*o^2 + 2*o*fs + ft, o the mean of these n values (or
+            // nearly: its own rounding drops out).  n*o^2 is at most their sum of squares whatever
+            // they are, so what fp32 rounds here is small against the sum.
+            const float each = __builtin_amdgcn_rcpf(n);
+            float o[NC] = {}, fs[NC] = {}, ft[NC] = {};
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (j >= skip[u]) o[NC == 1 ? 0 : j] = fmaf(v[u].get(j), each, o[NC == 1 ? 0 : j]);
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const int e = NC == 1 ? 0 : j;
+                    const float d = j < skip[u] ? 0.f : v[u].get(j) - o[e];
+                    fs[e] += d;
+                    ft[e] = fmaf(d, d, ft[e]);
+                }
 #pragma unroll
             for (int e = 0; e < NC; ++e) {
                 const double od = o[e], sd = fs[e], nd = n;
