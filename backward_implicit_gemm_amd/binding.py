@@ -400,6 +400,12 @@ class Conv:
 
 # ---------------------------------------------------------------------------
 # The operators around the convolutions
+#
+# A call is enqueued on `stream` (a torch stream or a raw handle), torch's current
+# one if None.  Its tensors are the caller's: as with any work on a second stream,
+# that stream first has to wait for what fills them, and they have to live (or be
+# recorded on it with record_stream) until it is done with them.  What a helper
+# allocates by itself follows the call's stream.
 # ---------------------------------------------------------------------------
 _ACTS = {"none": GC_ACT_NONE, "relu": GC_ACT_RELU, "silu": GC_ACT_SILU, "gelu": GC_ACT_GELU}
 _LAYOUTS = {"nchw": (GC_NCHW, torch.contiguous_format), "nhwc": (GC_NHWC, torch.channels_last)}
@@ -471,10 +477,36 @@ def gc_embed_plan_name(desc, dtype):
     return buf.value.decode()
 
 
-def _scratch(n, device):
-    """(address, bytes, tensor) of a workspace of n bytes."""
-    t = torch.empty(n, dtype=torch.uint8, device=device) if n else None
-    return (t.data_ptr() if n else None), n, t
+def _empty(shape, dtype, device, raw):
+    """Memory for work on the stream of this handle: torch's allocator gives it to nobody else
+    before that stream's work so far is done, however early it is freed."""
+    if raw == torch._C._cuda_getCurrentRawStream(device.index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+class _Workspace:
+    """A helper's scratch memory of n bytes: one buffer for the stream that was current when
+    the helper was made, and for a call on another stream (a captured one among them) memory
+    of that stream's own, so that neither a dropped helper nor two streams share a buffer in use."""
+
+    def __init__(self, n, device):
+        self.n, self.device, self.home = n, device, None
+        self._kept = self._args(torch.empty(n, dtype=torch.uint8, device=device)) if n else (None, 0, None)
+        if device.type == "cuda":
+            self.home = torch._C._cuda_getCurrentRawStream(device.index)
+
+    def _args(self, t):
+        return t.data_ptr(), self.n, t
+
+    def on(self, raw):
+        """(address, bytes, owner) for a call on the stream of this handle; the owner has to live
+        until the call returns."""
+        if not self.n or raw == self.home:
+            return self._kept
+        return self._args(_empty(self.n, torch.uint8, self.device, raw))
 
 
 class Embedding:
@@ -485,8 +517,7 @@ class Embedding:
     Tokens are int32, int64 or uint8; a token outside [0, vocab) is empty: zeros
     out, no gradient.  ``out`` and ``dout`` have shape (rows, tokens, dim); the
     rows, and those of the tokens, may lie further apart than they are long
-    (a part of a wider feature row).  Calls of one helper share its workspace
-    and must not overlap in time."""
+    (a part of a wider feature row)."""
 
     def __init__(self, rows, tokens, vocab, dim, dtype, scale=1.0, device="cuda"):
         self.dtype, self.dt, self.scale = dtype, _code(dtype), float(scale)
@@ -499,7 +530,7 @@ class Embedding:
         self._ref = ctypes.byref(self.desc)
         if int(vocab) < 1 or int(dim) < 1 or int(rows) < 0 or int(tokens) < 0:
             raise ValueError(f"invalid embedding: rows {rows}, tokens {tokens}, vocab {vocab}, dim {dim}")
-        self._ws = _scratch(int(lib().gc_embed_workspace_bytes(self._ref, self.dt)), self.device)
+        self._ws = _Workspace(int(lib().gc_embed_workspace_bytes(self._ref, self.dt)), self.device)
 
     def _describe(self, tok, rows_like, name):
         """Fills the descriptor from the tokens' type and both row distances."""
@@ -540,8 +571,9 @@ class Embedding:
         self._describe(tok, dout, "dout")
         dp = _arg(dtable, "dtable", self.dtype, self.table_shape, self.device)
         tp, op = _on(tok, "tokens", self.device), _on(dout, "dout", self.device)
-        st = lib().gc_embed_bwd(tp, op, dp, *self._ws[:2], self._ref, self.scale, self.dt,
-                                _raw_stream(stream, self.device))
+        raw = _raw_stream(stream, self.device)
+        ws, n, _owner = self._ws.on(raw)
+        st = lib().gc_embed_bwd(tp, op, dp, ws, n, self._ref, self.scale, self.dt, raw)
         _check("gc_embed_bwd", st)
         return dtable
 
@@ -554,8 +586,7 @@ class GroupNorm:
 
     act is "none", "relu", "silu" or "gelu"; gamma and beta (C) have
     param_dtype, float32 or the storage type, or are None; mean and rstd are
-    float32 (B, groups), in the forward None where they are not wanted.  Calls
-    of one helper share its workspace and must not overlap in time."""
+    float32 (B, groups), in the forward None where they are not wanted."""
 
     def __init__(self, shape, groups, act, dtype, layout="nchw", eps=1e-5, param_dtype=torch.float32,
                  device="cuda"):
@@ -573,8 +604,8 @@ class GroupNorm:
         self.desc = gc_norm_desc(B, C, H, W, int(groups), code, _named(_ACTS, act, "act"), float(eps))
         self._ref = ctypes.byref(self.desc)
         need = lib().gc_group_norm_workspace_bytes
-        self._ws = _scratch(max(int(need(op, self._ref, self.dt)) for op in (GC_OP_FWD, GC_OP_BWD)),
-                            self.device)
+        self._ws = _Workspace(max(int(need(op, self._ref, self.dt)) for op in (GC_OP_FWD, GC_OP_BWD)),
+                              self.device)
 
     def _image(self, t, name):
         return _arg(t, name, self.dtype, self.shape, self.device, self.format)
@@ -588,8 +619,9 @@ class GroupNorm:
     def fwd(self, x, gamma, beta, y, mean=None, rstd=None, stream=None):
         args = (self._image(x, "x"), self._param(gamma, "gamma"), self._param(beta, "beta"),
                 self._image(y, "y"), self._stat(mean, "mean"), self._stat(rstd, "rstd"))
-        st = lib().gc_group_norm_fwd(*args, *self._ws[:2], self._ref, self.dt, self.pt,
-                                     _raw_stream(stream, self.device))
+        raw = _raw_stream(stream, self.device)
+        ws, n, _owner = self._ws.on(raw)
+        st = lib().gc_group_norm_fwd(*args, ws, n, self._ref, self.dt, self.pt, raw)
         _check("gc_group_norm_fwd", st)
         return y, mean, rstd
 
@@ -597,8 +629,9 @@ class GroupNorm:
         args = (self._image(x, "x"), self._param(gamma, "gamma"), self._param(beta, "beta"),
                 self._image(dy, "dy"), self._stat(mean, "mean"), self._stat(rstd, "rstd"),
                 self._image(dx, "dx"), self._param(dgamma, "dgamma"), self._param(dbeta, "dbeta"))
-        st = lib().gc_group_norm_bwd(*args, *self._ws[:2], self._ref, self.dt, self.pt,
-                                     _raw_stream(stream, self.device))
+        raw = _raw_stream(stream, self.device)
+        ws, n, _owner = self._ws.on(raw)
+        st = lib().gc_group_norm_bwd(*args, ws, n, self._ref, self.dt, self.pt, raw)
         _check("gc_group_norm_bwd", st)
         return dx, dgamma, dbeta
 
@@ -638,9 +671,10 @@ class GradClip:
 
     Made once for a program's gradient tensors, which it keeps; each call reads
     the tensors' present addresses, and refuses them (ValueError) where one has
-    another size, type, device or layout than it was made for.  The norm comes back as a float32 device
-    tensor with one value; nothing is copied to the host.  prescale multiplies the
-    gradients first (the mean over accumulated steps, or an undone loss scale)."""
+    another size, type, device or layout than it was made for.  The norm comes back as
+    a float32 device tensor with one value, in memory of the call's stream; nothing is
+    copied to the host.  prescale multiplies the gradients first (the mean over accumulated steps, or
+    an undone loss scale)."""
 
     def __init__(self, grads, out=None, prescale=1.0, eps=1e-6, device="cuda"):
         self.grads, self.out = list(grads), list(grads if out is None else out)
@@ -663,8 +697,7 @@ class GradClip:
             raise ValueError("the gradients must be device tensors")
         self._both = _Tensors(self.grads if out is None else self.grads + self.out)
         self._addresses = self._both.addresses()
-        self._ws = torch.empty(int(lib().gc_grad_clip_workspace_bytes(len(self.grads))),
-                               dtype=torch.uint8, device=self.device)
+        self._ws = _Workspace(int(lib().gc_grad_clip_workspace_bytes(len(self.grads))), self.device)
 
     def _tensors(self):
         addresses = self._both.addresses()
@@ -676,16 +709,18 @@ class GradClip:
         return self._list
 
     def norm(self, stream=None):
-        norm = torch.empty((), dtype=torch.float32, device=self.device)
-        st = lib().gc_grad_norm(self._tensors(), len(self.grads), self.prescale, norm.data_ptr(),
-                                self._ws.data_ptr(), self._ws.numel(), _raw_stream(stream, self.device))
+        raw = _raw_stream(stream, self.device)
+        norm = _empty((), torch.float32, self.device, raw)
+        ws, n, _owner = self._ws.on(raw)
+        st = lib().gc_grad_norm(self._tensors(), len(self.grads), self.prescale, norm.data_ptr(), ws, n, raw)
         _check("gc_grad_norm", st)
         return norm
 
     def clip(self, max_norm, stream=None):
-        norm = torch.empty((), dtype=torch.float32, device=self.device)
+        raw = _raw_stream(stream, self.device)
+        norm = _empty((), torch.float32, self.device, raw)
+        ws, n, _owner = self._ws.on(raw)
         st = lib().gc_grad_clip(self._tensors(), len(self.grads), float(max_norm), self.prescale, self.eps,
-                                norm.data_ptr(), self._ws.data_ptr(), self._ws.numel(),
-                                _raw_stream(stream, self.device))
+                                norm.data_ptr(), ws, n, raw)
         _check("gc_grad_clip", st)
         return norm
