@@ -45,7 +45,7 @@ struct OnehotPlan {
     size_t bytes;
 };
 
-// First column of slab `s`: the last one ends with the row.
+// First column of slab `s`: the last one ends with the row, and shares columns with the one before.
 __host__ __device__ __forceinline__ int slab_column(int s, int D) { return D > kCols ? min(s * kCols, D - kCols) : 0; }
 // Column of slot i (0 .. 31) of a slab; rows shorter than a slab repeat their last pair.
 __device__ __forceinline__ int slot_column(int c0, int i, int D) { return min(c0 + (i & ~1), D - 2) + (i & 1); }
@@ -279,9 +279,11 @@ __global__ void __launch_bounds__(1024) onehot_sum(int V, int D, const float *__
         // the inverse of sum_place
         const int frag = place / 256, l = place / 4 % 64;
         const int v = block / slabs * rows + frag / 2 * 16 + l / 16 * 4 + place % 4;
-        const int slot = l % 16 * 2 + frag % 2;
-        if (v < V)
-            dtable[size_t(v) * D + slot_column(slab_column(block % slabs, D), slot, D)] = from_f32<T>(scale * red[0][i]);
+        const int slot = l % 16 * 2 + frag % 2, slab = block % slabs;
+        const int c = slot_column(slab_column(slab, D), slot, D);
+        // columns of the last slab that the one before holds too are that one's: a non-finite value
+        // in either gives the two other sums in another order
+        if (v < V && c >= slab * kCols) dtable[size_t(v) * D + c] = from_f32<T>(scale * red[0][i]);
     }
 }
 
