@@ -410,6 +410,7 @@ class Conv:
 _ACTS = {"none": GC_ACT_NONE, "relu": GC_ACT_RELU, "silu": GC_ACT_SILU, "gelu": GC_ACT_GELU}
 _LAYOUTS = {"nchw": (GC_NCHW, torch.contiguous_format), "nhwc": (GC_NHWC, torch.channels_last)}
 _DTYPES = {torch.float32: GC_F32, torch.bfloat16: GC_BF16}
+_INT_MAX = 2 ** 31 - 1
 _INDEX_TYPES = {torch.int32: GC_I32, torch.int64: GC_I64, torch.uint8: GC_U8}
 
 
@@ -525,11 +526,13 @@ class Embedding:
         self.tok_shape = torch.Size((int(rows), int(tokens)))
         self.out_shape = torch.Size((int(rows), int(tokens), int(dim)))
         self.table_shape = torch.Size((int(vocab), int(dim)))
+        # ctypes would cut off what a descriptor's field does not hold
+        if int(vocab) < 1 or int(dim) < 1 or int(rows) < 0 or int(tokens) < 0 or \
+                int(rows) >= 2 ** 60 or max(int(vocab), int(tokens), int(dim)) > _INT_MAX:
+            raise ValueError(f"invalid embedding: rows {rows}, tokens {tokens}, vocab {vocab}, dim {dim}")
         self.desc = gc_embed_desc(int(rows), int(tokens), int(vocab), int(dim), GC_I32,
                                   int(tokens) * int(dim), int(tokens))
         self._ref = ctypes.byref(self.desc)
-        if int(vocab) < 1 or int(dim) < 1 or int(rows) < 0 or int(tokens) < 0:
-            raise ValueError(f"invalid embedding: rows {rows}, tokens {tokens}, vocab {vocab}, dim {dim}")
         self._ws = _Workspace(int(lib().gc_embed_workspace_bytes(self._ref, self.dt)), self.device)
 
     def _describe(self, tok, rows_like, name):
@@ -599,7 +602,7 @@ class GroupNorm:
         B, C, H, W = (int(v) for v in shape)
         self.shape, self.param_shape = torch.Size((B, C, H, W)), torch.Size((C,))
         self.stat_shape = torch.Size((B, int(groups)))
-        if min(B, C, H, W, int(groups)) < 1 or C % int(groups):
+        if min(B, C, H, W, int(groups)) < 1 or max(B, C, H, W) > _INT_MAX or C % int(groups):
             raise ValueError(f"invalid group norm: shape {tuple(self.shape)}, {groups} groups")
         self.desc = gc_norm_desc(B, C, H, W, int(groups), code, _named(_ACTS, act, "act"), float(eps))
         self._ref = ctypes.byref(self.desc)

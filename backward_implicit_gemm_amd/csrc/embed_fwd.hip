@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) embed_rows(EmbedGeom g, const void *
 template <typename T, int N>
 hipError_t launch(const EmbedGeom &g, const void *tok, const void *table, void *out, float scale, hipStream_t s)
 {
-    const int per_row = (g.D + N - 1) / N;
+    const int per_row = vectors_of<N>(g.D);
     // one round of the loop, and more only to keep the launch below 2^32 threads
     const int rows_wg = std::max(std::max(1, kThreads * kUnroll / per_row), int(g.n >> 23));
     const unsigned grid = unsigned((int64_t(g.n) + rows_wg - 1) / rows_wg);

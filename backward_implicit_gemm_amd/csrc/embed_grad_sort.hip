@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads) run_partials(EmbedGeom g, const T *_
     if (a + kRun > g.n) return;
     const uint32_t k = key[a];
     if (k != key[a + kRun - 1] || k >= uint32_t(g.V)) return;
-    const int nvec = (g.D + N - 1) / N;
+    const int nvec = vectors_of<N>(g.D);
     for (int i = lane; i < nvec; i += team) {
         const int c = min(i * N, g.D - N);
         float s[N] = {};
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kThreads) next_partials(int V, int D, const ui
     if (q >= rows) return;
     const uint32_t k = key[q * span];
     if (k != key[q * span + span - 1] || k >= uint32_t(V)) return;
-    const int nvec = (D + N - 1) / N;
+    const int nvec = vectors_of<N>(D);
     for (int i = threadIdx.x % team; i < nvec; i += team) {
         const int c = min(i * N, D - N);
         float s[N] = {};
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads) table_rows(EmbedGeom g, const T *__r
         end[r] = b;
     }
     __syncthreads();
-    const int nvec = (g.D + N - 1) / N;
+    const int nvec = vectors_of<N>(g.D);
     const int lane = threadIdx.x % team, teams = kThreads / team;
     for (int r = threadIdx.x / team; r < rows_wg; r += teams) {
         const int64_t v = blockIdx.x + int64_t(r) * gridDim.x;
@@ -477,7 +477,7 @@ template <typename T, int N>
 hipError_t sums(const EmbedGeom &g, const SortPlan &p, const void *dout, const uint32_t *key, const uint32_t *idx,
                 char *ws, void *dtable, float scale, hipStream_t s)
 {
-    const int nvec = (g.D + N - 1) / N;
+    const int nvec = vectors_of<N>(g.D);
     int team = 1;
     while (team < nvec && team < kThreads) team <<= 1;
     const int teams = kThreads / team;
@@ -504,7 +504,7 @@ hipError_t sums(const EmbedGeom &g, const SortPlan &p, const void *dout, const u
     }
     const int rows_wg = std::min(kRowsMax, teams * 8);
     const bool past = (size_t(g.n) + g.V) * g.D * sizeof(T) >= kStreamBytes;
-    hipLaunchKernelGGL((past ? table_rows<T, N, true> : table_rows<T, N, false>), dim3((g.V + rows_wg - 1) / rows_wg),
+    hipLaunchKernelGGL((past ? table_rows<T, N, true> : table_rows<T, N, false>), dim3((uint32_t(g.V) + rows_wg - 1) / rows_wg),
                        dim3(kThreads), 0, s, g, (const T *)dout, key, idx, q, first, last, (T *)dtable, scale, team,
                        rows_wg);
     return hipGetLastError();

@@ -6,6 +6,10 @@
 
 namespace gc {
 
+// Vectors of N elements that a row of D >= 1 takes; D may be the largest int.
+template <int N>
+__host__ __device__ __forceinline__ int vectors_of(int D) { return (D - 1) / N + 1; }
+
 struct EmbedGeom {
     uint32_t n;        // tokens: rows * tokens of a row, below 2^31
     int V, D;

@@ -61,7 +61,7 @@ int check_embed(const gc_embed_desc *d, EmbedGeom *g)
 bool embed_onehot(const EmbedGeom &g, int dtype)
 {
     if (g.D < 2 || g.n == 0 || g.V > 4096) return false;
-    const int64_t cells = int64_t(embed_grad_onehot_rows(g.V)) * ((g.D + 31) / 32);
+    const int64_t cells = int64_t(embed_grad_onehot_rows(g.V)) * ((int64_t(g.D) + 31) / 32);
     return dtype == GC_BF16 ? cells <= 4096 && cells * g.n <= 800000000
                             : cells <= 2048 && cells * g.n <= 150000000;
 }
