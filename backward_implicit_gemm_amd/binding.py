@@ -6,6 +6,7 @@ all computation happens in the HIP kernels behind it.  There is no fallback:
 if ``libgc.so`` is missing or a call fails, an exception is raised.
 """
 import ctypes
+import math
 import os
 
 import torch
@@ -530,6 +531,8 @@ class Embedding:
         if int(vocab) < 1 or int(dim) < 1 or int(rows) < 0 or int(tokens) < 0 or \
                 int(rows) >= 2 ** 60 or max(int(vocab), int(tokens), int(dim)) > _INT_MAX:
             raise ValueError(f"invalid embedding: rows {rows}, tokens {tokens}, vocab {vocab}, dim {dim}")
+        if not math.isfinite(ctypes.c_float(self.scale).value):
+            raise ValueError(f"the scale has to be finite in fp32, not {scale}")
         self.desc = gc_embed_desc(int(rows), int(tokens), int(vocab), int(dim), GC_I32,
                                   int(tokens) * int(dim), int(tokens))
         self._ref = ctypes.byref(self.desc)

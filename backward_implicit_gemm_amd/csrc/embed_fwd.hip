@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) embed_rows(EmbedGeom g, const void *
             float f[N];
 #pragma unroll
             for (int j = 0; j < N; ++j) f[j] = scale * v[u].get(j);
-            if (!(id[u] >= 0 && id[u] < g.V)) {   // an infinite scale makes no NaN of an empty token
+            if (!(id[u] >= 0 && id[u] < g.V)) {   // zeros whatever the scale's sign
 #pragma unroll
                 for (int j = 0; j < N; ++j) f[j] = 0.f;
             }

@@ -192,7 +192,7 @@ int gc_embed_fwd(const void *tokens, const void *table, void *out, const gc_embe
     EmbedGeom g;
     const int st = check_embed(d, &g);
     if (st != GC_OK) return st;
-    if (!valid_dtype(dtype) || !table || !aligned_to(table, dtype)) return GC_ERR_INVALID_ARG;
+    if (!valid_dtype(dtype) || !table || !aligned_to(table, dtype) || !isfinite(scale)) return GC_ERR_INVALID_ARG;
     if (g.n == 0) return GC_OK;
     if (!tokens || !out || !aligned(tokens, token_size(d->itype)) || !aligned_to(out, dtype))
         return GC_ERR_INVALID_ARG;
@@ -214,7 +214,7 @@ int gc_embed_bwd(const void *tokens, const void *dout, void *dtable, void *works
     EmbedGeom g;
     int st = check_embed(d, &g);
     if (st != GC_OK) return st;
-    if (!valid_dtype(dtype) || !dtable || !aligned_to(dtable, dtype)) return GC_ERR_INVALID_ARG;
+    if (!valid_dtype(dtype) || !dtable || !aligned_to(dtable, dtype) || !isfinite(scale)) return GC_ERR_INVALID_ARG;
     if (g.n && (!tokens || !dout || !aligned(tokens, token_size(d->itype)) || !aligned_to(dout, dtype)))
         return GC_ERR_INVALID_ARG;
     st = check_workspace(workspace, ws_bytes, embed_grad_ws_bytes(g, dtype));

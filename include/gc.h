@@ -201,7 +201,7 @@ int gc_conv_plan_name(int op, const gc_conv_desc *d, int dtype, char *buf, size_
  * elements apart; out and dout rows of tokens*D elements, ld >= tokens*D
  * elements apart (so the embedding can be part of a wider feature row; the
  * elements between are not touched).  table and dtable are dense [V][D].
- * rows and tokens may be 0; rows*tokens and tokens*D are below 2^31. */
+ * scale is finite.  rows and tokens may be 0; rows*tokens and tokens*D are below 2^31. */
 typedef enum { GC_I32 = 0, GC_I64 = 1, GC_U8 = 2 } gc_index_type;
 typedef struct {
     int64_t rows;
