@@ -13,7 +13,7 @@
 #include <algorithm>
 
 #include "gc_embed.h"
-#include "gc_kernels.h"
+#include "gc_train.h"
 #include "gc_vec.h"
 
 namespace gc {

@@ -5,8 +5,8 @@
 
 #include <type_traits>
 
-#include "gc_kernels.h"
 #include "gc_norm.h"
+#include "gc_train.h"
 
 namespace gc {
 

@@ -7,8 +7,8 @@
 #include <stdio.h>
 
 #include "gc_embed.h"
-#include "gc_kernels.h"
 #include "gc_norm.h"
+#include "gc_train.h"
 
 using namespace gc;
 

@@ -18,7 +18,7 @@
 // first, as the last ones read are still in cache.  Both passes are bound by memory:
 // the gradients are read twice and written once (238 MB in 37 us, then 75 us; a copy
 // of one 160 MB tensor takes 60 us, its norm and clipping 81).
-#include "gc_kernels.h"
+#include "gc_train.h"
 #include "gc_vec.h"
 
 namespace gc {

@@ -7,8 +7,8 @@
 // their turn.
 #include <algorithm>
 
-#include "gc_kernels.h"
 #include "gc_norm_res.h"
+#include "gc_train.h"
 #include "ig_common.h"
 
 namespace gc {

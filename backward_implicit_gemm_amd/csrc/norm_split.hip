@@ -20,8 +20,8 @@
 // groups, channels last, 26 us forward and 43 backward.
 #include <algorithm>
 
-#include "gc_kernels.h"
 #include "gc_norm.h"
+#include "gc_train.h"
 
 namespace gc {
 namespace {

@@ -43,6 +43,7 @@ import hashlib
 import glob
 import json
 import os
+import re
 import statistics
 import sys
 import time
@@ -110,18 +111,38 @@ def layer_bytes(L, esize):
     return {"fwd": fwd, "dgrad": dgrad, "wgrad": wgrad, "bwd": bwd}
 
 
+def conv_sources():
+    """The files the convolutions are built from: the units of csrc that do not
+    include the other operators' launchers (gc_train.h), and the headers they include."""
+    csrc = os.path.join(ROOT, "backward_implicit_gemm_amd", "csrc")
+    names = {os.path.basename(p): open(p).read() for p in glob.glob(os.path.join(csrc, "*"))}
+    includes = {n: set(re.findall(r'^#include "([^/"]+)"', t, re.M)) for n, t in names.items()}
+
+    def reach(name):
+        seen, todo = set(), [name]
+        while todo:
+            n = todo.pop()
+            if n not in seen:
+                seen.add(n)
+                todo += includes[n]
+        return seen
+
+    units = [reach(n) for n in names if n.endswith(".hip")]
+    return {n: names[n] for u in units if "gc_train.h" not in u for n in u}
+
+
 def source_digest():
     h = hashlib.sha256()
-    for p in sorted(glob.glob(os.path.join(ROOT, "backward_implicit_gemm_amd", "csrc", "*"))):
-        h.update(os.path.basename(p).encode())
-        h.update(open(p, "rb").read())
+    for name, text in sorted(conv_sources().items()):
+        h.update(name.encode())
+        h.update(text.encode())
     return h.hexdigest()[:16]
 
 
 def measured_traffic(workload, op):
     """HBM bytes per call from the committed rocprofv3 counter summary (the
     first ```json block of profiles/traffic.md), if it was taken on the
-    current kernel sources; else None."""
+    current sources of the convolutions; else None."""
     try:
         text = open(PROFILE_TRAFFIC).read()
         block = text.split("```json", 1)[1].split("```", 1)[0]
