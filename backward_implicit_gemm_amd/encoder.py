@@ -31,13 +31,16 @@ class Encoder:
         def weight(*shape, bound):
             return ((2 * torch.rand(shape, generator=gen) - 1) * bound).to(device=device, dtype=dtype)
 
-        # norm parameters and the update stay in fp32 whatever the storage type
+        # norm parameters are fp32 whatever the storage type
         self.params = {"w1": weight(*l1.w_shape, bound=l1.w_bound), "w2": weight(*l2.w_shape, bound=l2.w_bound),
                        "table": weight(VOCAB, DIM, bound=1.0)}
         for i, layer in ((1, l1), (2, l2)):
             self.params[f"gamma{i}"] = torch.ones(layer.OC, device=device)
             self.params[f"beta{i}"] = torch.zeros(layer.OC, device=device)
         self.grads = {k: torch.empty_like(v) for k, v in self.params.items()}
+        # what the update moves: fp32 copies of the bf16 parameters, in which a step below half of
+        # a parameter's last place would be lost
+        self.masters = {k: v if v.dtype == torch.float32 else v.float() for k, v in self.params.items()}
 
         self.conv1 = gb.Conv(l1.x_shape, l1.w_shape, l1.stride, 0, dtype, device)
         self.conv2 = gb.Conv(l2.x_shape, l2.w_shape, l2.stride, 0, dtype, device)
@@ -87,8 +90,10 @@ class Encoder:
         self.dfeatures.copy_(off / self.batch)
         self.backward(maps, tokens, self.dfeatures)
         norm = self.clip.clip(max_norm)
-        for k, v in self.params.items():
+        for k, v in self.masters.items():
             v.sub_(self.grads[k], alpha=rate)
+            if v is not self.params[k]:
+                self.params[k].copy_(v)
         return 0.5 * off.square().sum(1).mean(), norm
 
 
