@@ -287,20 +287,21 @@ int gc_group_norm_plan_name(int op, const gc_norm_desc *d, int dtype, char *buf,
     const bool bwd = op == GC_OP_BWD;
     const NormSel s = select_norm(g, dtype, bwd);
     const char *dir = bwd ? "bwd" : "fwd";
+    // past: the output goes past the cache
     if (s.k == NormKind::Split)
-        snprintf(buf, buf_bytes, "norm_split_%s<N=%d,NHWC=%d> chunks=%d grid=%lld", dir, s.q.N, g.nhwc, s.q.chunks,
-                 (long long)s.q.grid);
+        snprintf(buf, buf_bytes, "norm_split_%s<N=%d,NHWC=%d> chunks=%d grid=%lld past=%d", dir, s.q.N, g.nhwc,
+                 s.q.chunks, (long long)s.q.grid, bwd ? s.q.past_bwd : s.q.past_fwd);
     else if (s.k == NormKind::None)
         snprintf(buf, buf_bytes, "none");
     else if (s.r.small)
-        snprintf(buf, buf_bytes, "res_small_%s<N=%d,NV=%d,LAST=%d> threads=%d teams=%d grid=%lld", dir, s.r.N, s.r.NV,
-                 g.nhwc, s.r.L, s.r.teams, (long long)s.r.grid);
+        snprintf(buf, buf_bytes, "res_small_%s<N=%d,NV=%d,LAST=%d> threads=%d teams=%d grid=%lld past=%d", dir, s.r.N,
+                 s.r.NV, g.nhwc, s.r.L, s.r.teams, (long long)s.r.grid, s.r.past);
     else if (g.nhwc)
-        snprintf(buf, buf_bytes, "res_nhwc_%s<N=%d,NV=%d,MIX=%d> threads=%d teams=%d slab=%d grid=%lld", dir, s.r.N,
-                 s.r.NV, s.r.mix, s.r.L, s.r.teams, s.r.CW, (long long)s.r.grid);
+        snprintf(buf, buf_bytes, "res_nhwc_%s<N=%d,NV=%d,MIX=%d> threads=%d teams=%d slab=%d grid=%lld past=%d", dir,
+                 s.r.N, s.r.NV, s.r.mix, s.r.L, s.r.teams, s.r.CW, (long long)s.r.grid, s.r.past);
     else
-        snprintf(buf, buf_bytes, "res_nchw_%s<N=%d,NV=%d,TWO=%d> threads=%d teams=%d grid=%lld", dir, s.r.N, s.r.NV,
-                 s.r.two, s.r.L, s.r.teams, (long long)s.r.grid);
+        snprintf(buf, buf_bytes, "res_nchw_%s<N=%d,NV=%d,TWO=%d> threads=%d teams=%d grid=%lld past=%d", dir, s.r.N,
+                 s.r.NV, s.r.two, s.r.L, s.r.teams, (long long)s.r.grid, s.r.past);
     return GC_OK;
 }
 
