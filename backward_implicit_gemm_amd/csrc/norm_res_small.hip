@@ -58,22 +58,34 @@ __device__ __forceinline__ int64_t group_at(const NormGeom &g, int64_t b, int gg
     return b * g.img + int64_t(gg) * g.Cg * (LAST ? 1 : g.HW);
 }
 
+// constants of a vector that holds whole channels, planes of S, 2S, ... positions: S divides
+// N, so every vector starts with a channel.  Wide loads, see near_params (planes of 4, 20,000
+// x 128 x 2 x 2 bf16 forward: 13.6 us, a load an element 16.7).
+template <typename T, int N, int S>
+__device__ __forceinline__ bool whole_channels(const NormGeom &g, int c0, const void *gamma, const void *beta,
+                                               float (&a)[N], float (&b)[N])
+{
+    if (g.HW == S) {
+        near_params<N / S, T>(g, gamma, c0, 1.f, a);
+        near_params<N / S, T>(g, beta, c0, 0.f, b);
+        return true;
+    }
+    if constexpr (2 * S < N) return whole_channels<T, N, 2 * S>(g, c0, gamma, beta, a, b);
+    return false;
+}
+
 // constants of a vector's elements
 template <typename T, int N, bool LAST>
 __device__ __forceinline__ void element_params(const NormGeom &g, const Lane<N, LAST> &w, int gg, int at,
                                                const void *gamma, const void *beta, float (&a)[N], float (&b)[N])
 {
     const int c0 = gg * g.Cg + (LAST ? w.col * N : int(fdiv(uint32_t(at), g.fd_HW)));
-    if (LAST || g.HW == 1) {
+    if (LAST) {
         near_params<N, T>(g, gamma, c0, 1.f, a);
         near_params<N, T>(g, beta, c0, 0.f, b);
         return;
     }
-    if (g.HW == 2) {   // N is a multiple, so a vector starts with a channel
-        near_params<N / 2, T>(g, gamma, c0, 1.f, a);
-        near_params<N / 2, T>(g, beta, c0, 0.f, b);
-        return;
-    }
+    if (whole_channels<T, N, 1>(g, c0, gamma, beta, a, b)) return;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
         const int c = gg * g.Cg + int(fdiv(uint32_t(at + j), g.fd_HW));
