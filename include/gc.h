@@ -214,8 +214,10 @@ int gc_embed_fwd(const void *tokens, const void *table, void *out, const gc_embe
                  void *stream);
 
 /* Every row of dtable is written, rows without a token as zeros.  Sums run in
- * fp32 over the tokens sorted by value, in an order the tokens alone fix, and
- * are rounded once: the result is bit-identical from run to run. */
+ * fp32, over the tokens sorted by value or, for small tables, as a product with
+ * the tokens' one-hot matrix, in an order that the call's sizes and tokens alone
+ * fix (and, in a small table's columns beside a non-finite value, that value's
+ * place), and are rounded once: the result is bit-identical from run to run. */
 size_t gc_embed_workspace_bytes(const gc_embed_desc *d, int dtype);
 int gc_embed_bwd(const void *tokens, const void *dout, void *dtable, void *workspace, size_t ws_bytes,
                  const gc_embed_desc *d, float scale, int dtype, void *stream);
