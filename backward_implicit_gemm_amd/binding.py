@@ -675,9 +675,11 @@ class GradClip:
     """The global norm of a list of gradients and their clipping (gc_grad_norm
     and gc_grad_clip), in place or into `out`.
 
-    Made once for a program's gradient tensors, which it keeps; each call reads
-    the tensors' present addresses, and refuses them (ValueError) where one has
-    another size, type, device or layout than it was made for.  The norm comes back as
+    Made once for a program's gradient tensors, which it keeps: gradients that a
+    program makes anew each step (torch's zero_grad() does, zero_grad(set_to_none=False)
+    keeps them) are other tensors, which it does not see.  Each call reads the tensors'
+    present addresses, and refuses them (ValueError) where one has another size, type,
+    device or layout than it was made for.  The norm comes back as
     a float32 device tensor with one value, in memory of the call's stream; nothing is
     copied to the host.  prescale multiplies the gradients first (the mean over accumulated steps, or
     an undone loss scale)."""

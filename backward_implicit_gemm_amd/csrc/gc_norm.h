@@ -38,7 +38,7 @@ __device__ __forceinline__ void set_param(const NormGeom &g, void *p, int c, flo
 
 // gamma (or beta) of K neighbouring channels, each for N/K elements of v in a row.  One
 // wide load: lanes whose channels lie a vector apart would make a memory line of every
-// few lanes of each element load (50,000 x 128 x 1 x 2 bf16 forward 30 us that way, 13 this).
+// few lanes of each element load (50,000 x 128 x 1 x 2 bf16 forward 29 us that way, 16 this).
 template <int K, typename T, int N>
 __device__ __forceinline__ void near_params(const NormGeom &g, const void *p, int c, float none, float (&v)[N])
 {

@@ -14,8 +14,10 @@
 // team walks images slot, slot + images, ..., keeping the channels' running sums of g
 // and g*hat in registers; the teams of a workgroup join them at the end into one
 // row of partials.  Bound by memory: 32,768 x 128 x 3 x 4 bf16 backward 57 us (5.4 TB/s), 1000 x 64
-// x 11 x 15 fp32 forward 15 us (5.6 TB/s); with few large images by the 64-byte rows of their
-// slabs (16 x 256 x 64 x 64 bf16 forward 22 us, 3.1 TB/s).
+// x 11 x 15 fp32 forward 15 us (5.8 TB/s); with few large images by the 64-byte rows of their
+// slabs (16 x 256 x 64 x 64 bf16 forward 22 us, 3.1 TB/s); where vectors mix groups or end inside
+// them by the sums of single channels in LDS (1000 x 59 x 11 x 15 in one group, bf16 backward 29 us
+// for 59 MB).
 #include <type_traits>
 
 #include "gc_norm_res.h"
