@@ -357,8 +357,9 @@ def gc_conv_bwd(x, w, dy, y_mask, dx, dw, relu, stride, workspace, stream=None):
 
 
 class Conv:
-    """One convolution layer's three passes with their workspaces allocated
-    once (torch allocates; the library only receives pointers)."""
+    """One convolution layer's three passes with their workspaces (torch
+    allocates; the library only receives pointers), one each for the stream the helper
+    was made on, see _Workspace."""
 
     def __init__(self, x_shape, w_shape, stride, relu, dtype, device="cuda"):
         self.stride, self.relu = int(stride), int(relu)
@@ -368,35 +369,39 @@ class Conv:
         self.x_shape, self.w_shape = tuple(x_shape), tuple(w_shape)
         OH, OW = gc_conv_out_dims(self.desc)
         self.y_shape = (x_shape[0], w_shape[0], OH, OW)
-        self.ws = {op: workspace_for(op, self.desc, self.dt, device)
+        self.device = _device(device)
+        self.ws = {op: _Workspace(gc_conv_workspace_bytes(op, self.desc, self.dt), self.device)
                    for op in (GC_OP_FWD, GC_OP_BWD_DATA, GC_OP_BWD_WEIGHT, GC_OP_BWD_BIAS,
                               GC_OP_BWD, GC_OP_BWD_WEIGHT_BIAS)}
 
+    def _scratch(self, op, stream):
+        return self.ws[op].on(_raw_stream(stream, self.device))[2]
+
     def fwd(self, x, w, y, stream=None):
-        return gc_conv_fwd(x, w, y, self.relu, self.stride, self.ws[GC_OP_FWD], stream)
+        return gc_conv_fwd(x, w, y, self.relu, self.stride, self._scratch(GC_OP_FWD, stream), stream)
 
     def bwd_data(self, dy, w, y, dx, stream=None):
         return gc_conv_bwd_data(dy, w, y if self.relu else None, dx, self.relu, self.stride,
-                                self.ws[GC_OP_BWD_DATA], stream)
+                                self._scratch(GC_OP_BWD_DATA, stream), stream)
 
     def bwd_weight(self, x, dy, y, dw, stream=None):
         return gc_conv_bwd_weight(x, dy, y if self.relu else None, dw, self.relu, self.stride,
-                                  self.ws[GC_OP_BWD_WEIGHT], stream)
+                                  self._scratch(GC_OP_BWD_WEIGHT, stream), stream)
 
     def bwd(self, x, w, dy, y, dx, dw, stream=None):
         return gc_conv_bwd(x, w, dy, y if self.relu else None, dx, dw, self.relu, self.stride,
-                           self.ws[GC_OP_BWD], stream)
+                           self._scratch(GC_OP_BWD, stream), stream)
 
     def fwd_bias(self, x, w, bias, y, stream=None):
-        return gc_conv_fwd_bias(x, w, bias, y, self.relu, self.stride, self.ws[GC_OP_FWD], stream)
+        return gc_conv_fwd_bias(x, w, bias, y, self.relu, self.stride, self._scratch(GC_OP_FWD, stream), stream)
 
     def bwd_weight_bias(self, x, dy, y, dw, db, stream=None):
         return gc_conv_bwd_weight_bias(x, dy, y if self.relu else None, dw, db, self.relu,
-                                       self.stride, self.ws[GC_OP_BWD_WEIGHT_BIAS], stream)
+                                       self.stride, self._scratch(GC_OP_BWD_WEIGHT_BIAS, stream), stream)
 
     def bwd_bias(self, dy, y, db, stream=None):
         return gc_conv_bwd_bias(dy, y if self.relu else None, db, self.relu, self.x_shape,
-                                self.w_shape, self.stride, self.ws[GC_OP_BWD_BIAS], stream)
+                                self.w_shape, self.stride, self._scratch(GC_OP_BWD_BIAS, stream), stream)
 
 
 # ---------------------------------------------------------------------------
