@@ -39,6 +39,7 @@ the call's: what one launch of that size reaches here, beside the call.
 --workload NAME (or --all) prints the full line of other workloads.
 """
 import argparse
+import gc
 import hashlib
 import glob
 import json
@@ -280,15 +281,20 @@ def run_gpu(wl, steps, warmup, x_scale=1.0, extras=True, copies=True):
     floor["us_per_kernel"] = round(floor["us_per_step"] / nk, 3)
     del g
 
-    # The same steps issued eagerly through the C ABI, host work included.
+    # The same steps issued eagerly through the C ABI, host work included.  A full
+    # collection of Python's garbage takes 40 ms in this process: it is had before, not
+    # by chance within, the timed steps.
     ms_eager = None
     if extras:
+        gc.collect()
+        gc.disable()
         start.record(stream)
         for _ in range(steps):
             step()
         end.record(stream)
         torch.cuda.synchronize()
         ms_eager = start.elapsed_time(end) / steps
+        gc.enable()
 
     # Per call: a graph of REPS back-to-back copies of the call, replayed and
     # timed with HIP events on the launch stream, so each figure is the
