@@ -19,6 +19,8 @@ GC_OK, GC_ERR_INVALID_ARG, GC_ERR_UNSUPPORTED, GC_ERR_WORKSPACE, GC_ERR_HIP = ra
 GC_F32, GC_BF16 = 0, 1
 GC_OP_FWD, GC_OP_BWD_DATA, GC_OP_BWD_WEIGHT, GC_OP_BWD_BIAS, GC_OP_BWD = 0, 1, 2, 3, 4
 GC_OP_BWD_WEIGHT_BIAS = 5
+GC_OP_STEP = 6
+GC_RECURRENCE_BLOCK = 16
 
 EXPORTED = (
     "gc_conv_out_dims", "gc_conv_workspace_bytes", "gc_conv_fwd", "gc_conv_bwd_data",
@@ -28,6 +30,9 @@ EXPORTED = (
     "gc_embed_fwd", "gc_embed_bwd", "gc_embed_workspace_bytes", "gc_group_norm_fwd",
     "gc_group_norm_bwd", "gc_group_norm_workspace_bytes", "gc_grad_norm", "gc_grad_clip",
     "gc_grad_clip_workspace_bytes", "gc_group_norm_plan_name", "gc_embed_plan_name",
+    "gc_layer_norm_fwd", "gc_layer_norm_bwd", "gc_layer_norm_workspace_bytes", "gc_layer_norm_plan_name",
+    "gc_recurrence_fwd", "gc_recurrence_bwd", "gc_recurrence_workspace_bytes", "gc_recurrence_plan_name",
+    "gc_distill_fwd", "gc_distill_bwd", "gc_distill_step", "gc_distill_plan_name",
 )
 GC_I32, GC_I64, GC_U8 = 0, 1, 2
 GC_NCHW, GC_NHWC = 0, 1
@@ -59,6 +64,25 @@ class gc_norm_desc(ctypes.Structure):
 class gc_tensor(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64),
                 ("dtype", ctypes.c_int)]
+
+
+class gc_layer_norm_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int), ("eps", ctypes.c_float)] + \
+               [(n, ctypes.c_int64) for n in ("ld_x", "ld_residual", "ld_total", "ld_y")]
+
+
+class gc_strides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("step", ctypes.c_int64)]
+
+
+class gc_recurrence_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "D", "coupled")] + \
+               [(n, gc_strides) for n in ("gate", "value", "out", "dgate", "dvalue", "reset")]
+
+
+class gc_distill_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64)] + [(n, ctypes.c_int) for n in ("V", "K", "itype", "teacher_dtype")] + \
+               [("temperature", ctypes.c_float)] + [(n, ctypes.c_int64) for n in ("ld", "ld_grad", "ld_index", "ld_teacher")]
 
 
 _lib = None
@@ -128,6 +152,28 @@ def lib():
     L.gc_grad_norm.restype = i
     L.gc_grad_clip.argtypes = [tp, i, f, f, f, vp, vp, sz, vp]
     L.gc_grad_clip.restype = i
+    lp, rp, sp = (ctypes.POINTER(t) for t in (gc_layer_norm_desc, gc_recurrence_desc, gc_distill_desc))
+    L.gc_layer_norm_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, lp, i, i, vp]
+    L.gc_layer_norm_fwd.restype = i
+    L.gc_layer_norm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, lp, i, i, vp]
+    L.gc_layer_norm_bwd.restype = i
+    L.gc_layer_norm_workspace_bytes.argtypes = [lp, i]
+    L.gc_layer_norm_workspace_bytes.restype = sz
+    L.gc_recurrence_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, rp, i, vp]
+    L.gc_recurrence_fwd.restype = i
+    L.gc_recurrence_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, rp, i, vp]
+    L.gc_recurrence_bwd.restype = i
+    L.gc_recurrence_workspace_bytes.argtypes = [i, rp, i]
+    L.gc_recurrence_workspace_bytes.restype = sz
+    L.gc_distill_fwd.argtypes = [vp, vp, vp, vp, vp, vp, sp, i, vp]
+    L.gc_distill_fwd.restype = i
+    L.gc_distill_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, sp, i, vp]
+    L.gc_distill_bwd.restype = i
+    L.gc_distill_step.argtypes = [vp, vp, vp, vp, vp, vp, sp, i, vp]
+    L.gc_distill_step.restype = i
+    for name, ptr in (("layer_norm", lp), ("recurrence", rp), ("distill", sp)):
+        plan = getattr(L, f"gc_{name}_plan_name")
+        plan.argtypes, plan.restype = [i, ptr, i, ctypes.c_char_p, sz], i
     _lib = L
     return L
 
@@ -737,3 +783,304 @@ class GradClip:
                                 norm.data_ptr(), ws, n, raw)
         _check("gc_grad_clip", st)
         return norm
+
+
+# ---------------------------------------------------------------------------
+# The recurrent core and its head's loss
+#
+# A helper's calls take tensors of any row (or batch and step) distances; a descriptor is
+# made once for each set of them that a call brings and is not changed afterwards.
+# ---------------------------------------------------------------------------
+def _plan_name(name, op, desc, dtype):
+    buf = ctypes.create_string_buffer(256)
+    _check(name, getattr(lib(), name)(int(op), ctypes.byref(desc), int(dtype), buf, len(buf)))
+    return buf.value.decode()
+
+
+def gc_layer_norm_plan_name(op, desc, dtype):
+    """The kernels a layer norm would run (host only, enqueues nothing)."""
+    return _plan_name("gc_layer_norm_plan_name", op, desc, dtype)
+
+
+def gc_recurrence_plan_name(op, desc, dtype):
+    """The kernels a recurrence would run (host only, enqueues nothing)."""
+    return _plan_name("gc_recurrence_plan_name", op, desc, dtype)
+
+
+def gc_distill_plan_name(op, desc, dtype):
+    """The kernels a distillation would run (host only, enqueues nothing)."""
+    return _plan_name("gc_distill_plan_name", op, desc, dtype)
+
+
+class _Descs:
+    """A helper's descriptors by the distances they were made for."""
+
+    def __init__(self, make):
+        self.make, self.made = make, {}
+
+    def __call__(self, key):
+        ref = self.made.get(key)
+        if ref is None:
+            ref = ctypes.byref(self.make(*key))
+            if len(self.made) >= 64:     # a program whose layouts change without end
+                self.made = {}
+            self.made[key] = ref
+        return ref
+
+
+def _dense_rows(t, name, dtype, shape, device):
+    """Address of t, rows of dense values, and the distance of two rows."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    rows, n = shape
+    ld, inner = t.stride()
+    if inner != 1 and n > 1:
+        raise ValueError(f"{name} must be dense within a row")
+    if rows < 2:
+        ld = n
+    elif ld < n:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return _on(t, name, device), ld
+
+
+def _extent(value, name, least, most):
+    """A whole number within what the descriptor's field takes."""
+    value = int(value)
+    if not least <= value <= most:
+        raise ValueError(f"{name} has to be from {least} to {most}, not {value}")
+    return value
+
+
+class LayerNorm:
+    """Layer norm of rows with the residual stream's addition (gc_layer_norm_fwd and
+    gc_layer_norm_bwd): tensors of shape (rows, dim), whose rows may be parts of wider ones.
+
+    The forward norms x + residual (x alone without one) and writes that sum to ``total``
+    where it is given; ``total`` may be ``residual`` or ``x`` itself.  gamma and beta (dim)
+    have param_dtype, float32 or the storage type, or are None; mean and rstd are float32
+    (rows), in the forward None where they are not wanted.
+
+    The backward takes the normed rows (the forward's ``total`` where it had a residual), and
+    ``dtotal``, the gradient that reaches the stream past the norm, or None; dx is the
+    gradient of x and of the residual, and may be ``dtotal`` or ``dy`` itself."""
+
+    def __init__(self, rows, dim, dtype, eps=1e-5, param_dtype=torch.float32, device="cuda"):
+        self.dtype, self.dt = dtype, _code(dtype)
+        self.param_dtype, self.pt = param_dtype, _code(param_dtype)
+        if self.pt not in (GC_F32, self.dt):
+            raise TypeError(f"param_dtype {param_dtype} is neither float32 nor the storage type {dtype}")
+        rows, dim = _extent(rows, "rows", 0, _INT_MAX), _extent(dim, "dim", 1, 2 ** 23)
+        eps = ctypes.c_float(float(eps)).value
+        if not 0 <= eps < math.inf:
+            raise ValueError(f"eps has to be finite and not negative in fp32, not {eps}")
+        self.device = _device(device)
+        self.shape, self.param_shape = torch.Size((rows, dim)), torch.Size((dim,))
+        self.stat_shape = torch.Size((rows,))
+        self._desc = _Descs(lambda *ld: gc_layer_norm_desc(rows, dim, eps, *ld))
+        need = int(lib().gc_layer_norm_workspace_bytes(self._desc((dim,) * 4), self.dt))
+        self._ws = _Workspace(need, self.device)
+
+    def _rows(self, t, name):
+        return _dense_rows(t, name, self.dtype, self.shape, self.device)
+
+    def _param(self, t, name):
+        return None if t is None else _arg(t, name, self.param_dtype, self.param_shape, self.device)
+
+    def _stat(self, t, name):
+        return None if t is None else _arg(t, name, torch.float32, self.stat_shape, self.device)
+
+    @staticmethod
+    def _in_place(out, name, *inputs):
+        for address, ld in inputs:
+            if address == out[0] and ld != out[1] and address:
+                raise ValueError(f"{name} in place has to have the row distance of its input")
+
+    def fwd(self, x, gamma, beta, y, mean=None, rstd=None, residual=None, total=None, stream=None):
+        xp, yp = self._rows(x, "x"), self._rows(y, "y")
+        none = None, self.shape[1]
+        rp = none if residual is None else self._rows(residual, "residual")
+        tp = none if total is None else self._rows(total, "total")
+        if total is not None:
+            self._in_place(tp, "total", xp, rp)
+        gp, bp = self._param(gamma, "gamma"), self._param(beta, "beta")
+        mp, sp = self._stat(mean, "mean"), self._stat(rstd, "rstd")
+        st = lib().gc_layer_norm_fwd(xp[0], rp[0], gp, bp, yp[0], tp[0], mp, sp,
+                                     self._desc((xp[1], rp[1], tp[1], yp[1])), self.dt, self.pt,
+                                     _raw_stream(stream, self.device))
+        _check("gc_layer_norm_fwd", st)
+        return y, mean, rstd, total
+
+    def bwd(self, x, gamma, dy, mean, rstd, dx, dgamma=None, dbeta=None, dtotal=None, stream=None):
+        xp, yp, op = self._rows(x, "x"), self._rows(dy, "dy"), self._rows(dx, "dx")
+        tp = (None, self.shape[1]) if dtotal is None else self._rows(dtotal, "dtotal")
+        self._in_place(op, "dx", xp, yp, tp)
+        gp = self._param(gamma, "gamma")
+        mp, sp = self._stat(mean, "mean"), self._stat(rstd, "rstd")
+        dg, db = self._param(dgamma, "dgamma"), self._param(dbeta, "dbeta")
+        raw = _raw_stream(stream, self.device)
+        ws, n, _owner = self._ws.on(raw)
+        st = lib().gc_layer_norm_bwd(xp[0], gp, yp[0], tp[0], mp, sp, op[0], dg, db, ws, n,
+                                     self._desc((xp[1], op[1], tp[1], yp[1])), self.dt, self.pt, raw)
+        _check("gc_layer_norm_bwd", st)
+        return dx, dgamma, dbeta
+
+
+class Recurrence:
+    """The gated linear recurrence (gc_recurrence_fwd and gc_recurrence_bwd) over tensors of
+    shape (batch, length, dim): h = a * h + (1 - a) * value with a = sigmoid(gate), or, not
+    coupled, h = a * h + value.
+
+    gate, value, out and their gradients may lie in any order of batch and time, and be parts
+    of wider rows; only the channels have to be dense.  h0, last, dlast and dh0 are float32
+    (batch, dim); reset is bool or uint8 (batch, length), true where a step starts anew; lengths is
+    int32 (batch), steps behind them are not read and get zeros.  states, float32 of
+    ``states_shape``, is what the forward keeps for the backward.  A policy that acts makes a
+    helper with length 1 and passes its state as h0 and as last."""
+
+    def __init__(self, batch, length, dim, dtype, coupled=True, device="cuda"):
+        self.dtype, self.dt, self.coupled = dtype, _code(dtype), bool(coupled)
+        batch, length = _extent(batch, "batch", 0, _INT_MAX), _extent(length, "length", 0, 2 ** 30)
+        dim = _extent(dim, "dim", 1, _INT_MAX)
+        self.device = _device(device)
+        self.shape, self.end_shape = torch.Size((batch, length, dim)), torch.Size((batch, dim))
+        self.states_shape = torch.Size((batch, -(-length // GC_RECURRENCE_BLOCK), dim))
+        self._step_shape, self._length_shape = torch.Size((batch, length)), torch.Size((batch,))
+        own = int(self.coupled)
+        self._desc = _Descs(lambda *s: gc_recurrence_desc(batch, length, dim, own, *(gc_strides(*v) for v in s)))
+        self._dense = length * dim, dim
+        need = lib().gc_recurrence_workspace_bytes
+        every = self._desc((self._dense,) * 5 + ((length, 1),))
+        self._ws = {op: _Workspace(int(need(op, every, self.dt)), self.device) for op in (GC_OP_FWD, GC_OP_BWD)}
+
+    def _seq(self, t, name, output=False):
+        """Address of t and its distances of sequences and of steps."""
+        if t.shape != self.shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(self.shape)}")
+        if t.dtype != self.dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {self.dtype}")
+        batch, step, inner = t.stride()
+        if inner != 1 and self.shape[2] > 1:
+            raise ValueError(f"the channels of {name} must be dense")
+        if output and not self._apart(batch, step):
+            raise ValueError(f"the steps of {name} must not overlap")
+        return _on(t, name, self.device), (batch, step)
+
+    def _apart(self, batch, step):
+        B, T, D = self.shape
+        if B < 1 or T < 1:
+            return True
+        near, far = sorted([(step, T)] * (T > 1) + [(batch, B)] * (B > 1) + [(D, 1)] * ((T == 1) + (B == 1)))
+        return near[0] >= D and (far[1] == 1 or near[0] * (near[1] - 1) + D <= far[0])
+
+    def _end(self, t, name):
+        return None if t is None else _arg(t, name, torch.float32, self.end_shape, self.device)
+
+    def _states(self, t):
+        return None if t is None else _arg(t, "states", torch.float32, self.states_shape, self.device)
+
+    def _steps(self, reset, lengths):
+        rp, rs, lp = None, (0, 0), None
+        if reset is not None:
+            if reset.shape != self._step_shape:
+                raise ValueError(f"reset has shape {tuple(reset.shape)}, expected {tuple(self._step_shape)}")
+            if reset.dtype not in (torch.bool, torch.uint8):
+                raise TypeError(f"reset has dtype {reset.dtype}, expected bool or uint8")
+            rp, rs = _on(reset, "reset", self.device), reset.stride()
+        if lengths is not None:
+            lp = _arg(lengths, "lengths", torch.int32, self._length_shape, self.device)
+        return rp, rs, lp
+
+    def fwd(self, gate, value, out, h0=None, last=None, states=None, reset=None, lengths=None, stream=None):
+        gp, gs = self._seq(gate, "gate")
+        vp, vs = self._seq(value, "value")
+        op, os_ = self._seq(out, "out", True)
+        hp, ep, kp = self._end(h0, "h0"), self._end(last, "last"), self._states(states)
+        rp, rs, lp = self._steps(reset, lengths)
+        raw = _raw_stream(stream, self.device)
+        ws, n, _owner = self._ws[GC_OP_FWD].on(raw)
+        st = lib().gc_recurrence_fwd(gp, vp, hp, rp, lp, op, ep, kp, ws, n,
+                                     self._desc((gs, vs, os_, self._dense, self._dense, rs)), self.dt, raw)
+        _check("gc_recurrence_fwd", st)
+        return out, last
+
+    def bwd(self, gate, value, states, dout, dgate, dvalue, dlast=None, dh0=None, reset=None, lengths=None, stream=None):
+        gp, gs = self._seq(gate, "gate")
+        vp, vs = self._seq(value, "value")
+        op, os_ = self._seq(dout, "dout")
+        dgp, dgs = self._seq(dgate, "dgate", True)
+        dvp, dvs = self._seq(dvalue, "dvalue", True)
+        kp, ep, hp = self._states(states), self._end(dlast, "dlast"), self._end(dh0, "dh0")
+        rp, rs, lp = self._steps(reset, lengths)
+        raw = _raw_stream(stream, self.device)
+        ws, n, _owner = self._ws[GC_OP_BWD].on(raw)
+        st = lib().gc_recurrence_bwd(gp, vp, kp, rp, lp, op, ep, dgp, dvp, hp, ws, n,
+                                     self._desc((gs, vs, os_, dgs, dvs, rs)), self.dt, raw)
+        _check("gc_recurrence_bwd", st)
+        return dgate, dvalue, dh0
+
+
+class Distill:
+    """Distillation of a head from a teacher's top logits (gc_distill_fwd, gc_distill_bwd and
+    gc_distill_step): logits of shape (rows, vocab), the teacher's entries as index (int32 or
+    int64) and teacher (teacher_dtype) of shape (rows, top).
+
+    An entry whose index is outside [0, vocab) is empty; a row without entries has no loss and no
+    gradient.  The loss is the divergence of the softmaxes at the temperature, times its
+    square, one float32 value a row; dloss is its gradient a row.  The forward also writes peak and
+    mass (float32, rows), which the backward reads; ``step`` gives loss and gradient in one
+    pass where dloss is known before.  dlogits may be logits itself."""
+
+    def __init__(self, rows, vocab, top, dtype, temperature=1.0, teacher_dtype=torch.float32, device="cuda"):
+        self.dtype, self.dt = dtype, _code(dtype)
+        self.teacher_dtype, tt = teacher_dtype, _code(teacher_dtype)
+        rows, vocab = _extent(rows, "rows", 0, _INT_MAX), _extent(vocab, "vocab", 1, _INT_MAX)
+        top = _extent(top, "top", 1, 1024)
+        t = ctypes.c_float(float(temperature)).value
+        if not 0 < t < math.inf:
+            raise ValueError(f"the temperature has to be positive and finite in fp32, not {temperature}")
+        self.temperature, self.device = t, _device(device)
+        self.shape, self.entry_shape = torch.Size((rows, vocab)), torch.Size((rows, top))
+        self.row_shape = torch.Size((rows,))
+        self._desc = _Descs(lambda itype, *ld: gc_distill_desc(rows, vocab, top, itype, tt, t, *ld))
+
+    def _row(self, t, name):
+        return None if t is None else _arg(t, name, torch.float32, self.row_shape, self.device)
+
+    def _inputs(self, logits, index, teacher, dlogits=None):
+        """Addresses of logits, index, teacher and dlogits, and the call's descriptor."""
+        if index.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"index has dtype {index.dtype}, expected int32 or int64")
+        lp, ld = _dense_rows(logits, "logits", self.dtype, self.shape, self.device)
+        ip, li = _dense_rows(index, "index", index.dtype, self.entry_shape, self.device)
+        tp, lt = _dense_rows(teacher, "teacher", self.teacher_dtype, self.entry_shape, self.device)
+        gp, lg = None, self.shape[1]
+        if dlogits is not None:
+            gp, lg = _dense_rows(dlogits, "dlogits", self.dtype, self.shape, self.device)
+            if gp == lp and lg != ld:
+                raise ValueError("dlogits in place has to have the row distance of logits")
+        return lp, ip, tp, gp, self._desc((_INDEX_TYPES[index.dtype], ld, lg, li, lt))
+
+    def fwd(self, logits, index, teacher, loss, peak=None, mass=None, stream=None):
+        lp, ip, tp, _, desc = self._inputs(logits, index, teacher)
+        if loss is None:
+            raise ValueError("loss is not optional")
+        st = lib().gc_distill_fwd(lp, ip, tp, self._row(loss, "loss"), self._row(peak, "peak"), self._row(mass, "mass"),
+                                  desc, self.dt, _raw_stream(stream, self.device))
+        _check("gc_distill_fwd", st)
+        return loss, peak, mass
+
+    def bwd(self, logits, index, teacher, peak, mass, dloss, dlogits, stream=None):
+        lp, ip, tp, gp, desc = self._inputs(logits, index, teacher, dlogits)
+        st = lib().gc_distill_bwd(lp, ip, tp, self._row(peak, "peak"), self._row(mass, "mass"), self._row(dloss, "dloss"), gp,
+                                  desc, self.dt, _raw_stream(stream, self.device))
+        _check("gc_distill_bwd", st)
+        return dlogits
+
+    def step(self, logits, index, teacher, dloss, loss, dlogits, stream=None):
+        lp, ip, tp, gp, desc = self._inputs(logits, index, teacher, dlogits)
+        st = lib().gc_distill_step(lp, ip, tp, self._row(dloss, "dloss"), self._row(loss, "loss"), gp, desc, self.dt,
+                                   _raw_stream(stream, self.device))
+        _check("gc_distill_step", st)
+        return loss, dlogits

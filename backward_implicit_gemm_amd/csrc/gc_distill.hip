@@ -1,0 +1,344 @@
+// gc_distill.hip -- distillation of a head from a teacher's top logits: the loss, its gradient,
+// and both at once.
+//
+//   p = softmax(teacher / t) over a row's entries,  q = softmax(logits / t)
+//   loss = t^2 * sum p * (log p - log q[index]),  dlogits = dloss * t * (q - p at the entries)
+//
+// Memory bound: the logits are read once (the step holds a row in the registers of its
+// team between the row's sum and its gradient), the gradient is written once.  A team of
+// threads takes a row: lanes of a wave for short rows, a workgroup for long ones.  The teacher's shares
+// are worked out by every wave for itself, which needs no barrier; entries are few.  The
+// gradient is written as if there were no entries, then the entries' places are written again
+// with all that belongs to them, by the first entry of each place.
+#include <algorithm>
+#include <math.h>
+#include <type_traits>
+
+#include "gc_core.h"
+#include "gc_norm_res.h"
+
+namespace gc {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896f;
+
+// An entry in LDS: its place (-1: empty), its share and its logit.
+struct Entry {
+    int at;
+    float p, z;
+};
+
+template <typename V, typename F>
+__device__ __forceinline__ V lanes_fold(V v, int width, F f)
+{
+    for (int m = width >> 1; m > 0; m >>= 1) v = f(v, __shfl_xor(v, m, 64));
+    return v;
+}
+
+// Folds a value of each of the team's L threads; a team of more than 64 is the workgroup.
+template <typename F>
+__device__ __forceinline__ float team_fold(float v, int L, float *red, F f)
+{
+    v = lanes_fold(v, L < 64 ? L : 64, f);
+    if (L <= 64) return v;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float s = red[0];
+    for (int i = 1; i < L >> 6; ++i) s = f(s, red[i]);
+    return s;
+}
+
+template <int N>
+struct Place {
+    int at, skip;
+    bool live;
+    __device__ __forceinline__ Place(int64_t i, int V)
+    {
+        const int64_t first = i * N;
+        live = first < V;
+        at = live ? min(int(first), V - N) : 0;
+        skip = live ? int(first) - at : N;
+    }
+};
+
+template <bool PAST, typename T, int N>
+__device__ __forceinline__ void put_own(T *p, const Vec<T, N> &v, int skip)
+{
+    if (N == 1 || skip == 0) {
+        put_vec<PAST, T, N>(p, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j >= skip) p[j] = from_f32<T>(v.get(j));
+    }
+}
+
+// exp((z - peak) / t), NaN where both are infinite alike
+__device__ __forceinline__ float share(float z, float peak, float c) { return __builtin_amdgcn_exp2f((z - peak) * c); }
+
+// OP: GC_OP_FWD writes loss, peak and mass, GC_OP_BWD reads the last two and writes dlogits,
+// GC_OP_STEP writes loss and dlogits.  NV vectors of a row stay in registers, 0: the row is walked.
+template <typename T, int N, int NV, int OP, bool PAST>
+__global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, const T *logits, const void *__restrict__ index,
+                                                const void *__restrict__ teacher, float *__restrict__ peak,
+                                                float *__restrict__ mass, const float *__restrict__ dloss,
+                                                float *__restrict__ loss, T *dlogits)
+{
+    __shared__ float red[16];
+    extern __shared__ Entry all[];
+    const int tt = threadIdx.x & (L - 1), team = threadIdx.x / L, teams = blockDim.x / L;
+    const int64_t row = int64_t(blockIdx.x) * teams + team;
+    if (row >= g.rows) return;   // a whole team; a team of several waves is alone in its workgroup
+    Entry *entry = all + team * g.K;
+    const T *z = logits + row * g.ld;
+    const float t = g.temperature, c = kLog2e / t;
+    const int nv = vectors(g.V, N);
+    const auto most = [](float a, float b) { return fmaxf(a, b); };
+    const auto plus = [](float a, float b) { return a + b; };
+
+    Vec<T, N> held[NV ? NV : 1];
+    if (OP == GC_OP_STEP) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) held[i] = load_vec<T, N>(z + Place<N>(int64_t(i) * L + tt, g.V).at);
+    }
+
+    // the teacher's shares, by every wave for itself
+    const int width = L < 64 ? L : 64, lane = tt & (width - 1);
+    auto entry_at = [&](int k, int &at, float &v) {
+        const int64_t i = g.i64 ? static_cast<const int64_t *>(index)[row * g.ld_index + k]
+                                : static_cast<const int32_t *>(index)[row * g.ld_index + k];
+        at = i >= 0 && i < g.V ? int(i) : -1;
+        v = g.t32 ? static_cast<const float *>(teacher)[row * g.ld_teacher + k]
+                  : to_f32(static_cast<const bf16_t *>(teacher)[row * g.ld_teacher + k]);
+        if (at < 0) v = -INFINITY;
+    };
+    float top = -INFINITY, total = 0.f;
+    for (int k = lane; k < g.K; k += width) {
+        int at;
+        float v;
+        entry_at(k, at, v);
+        top = fmaxf(top, v != v ? INFINITY : v);
+    }
+    top = lanes_fold(top, width, most);
+    const bool some = top > -INFINITY;
+    for (int k = lane; k < g.K; k += width) {
+        int at;
+        float v;
+        entry_at(k, at, v);
+        total += v == -INFINITY ? 0.f : share(v, top, c);
+    }
+    total = lanes_fold(total, width, plus);
+    const float inv_total = 1.f / total;
+    for (int k = tt; k < g.K; k += L) {
+        Entry e;
+        float v;
+        entry_at(k, e.at, v);
+        e.p = v == -INFINITY ? 0.f : share(v, top, c) * inv_total;
+        e.z = e.at >= 0 ? to_f32(z[e.at]) : 0.f;
+        entry[k] = e;
+    }
+
+    // the student's largest logit, and the sum of the exponentials
+    float m, s;
+    if (OP == GC_OP_BWD) {
+        m = peak[row];
+        s = mass[row];
+    } else if (NV) {
+        m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Place<N> at(int64_t(i) * L + tt, g.V);
+#pragma unroll
+            for (int j = 0; j < N; ++j) m = fmaxf(m, j >= at.skip ? held[i].get(j) : -INFINITY);
+        }
+        m = team_fold(m, L, red, most);
+        const float base = m == -INFINITY ? 0.f : m;
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Place<N> at(int64_t(i) * L + tt, g.V);
+#pragma unroll
+            for (int j = 0; j < N; ++j) s += j >= at.skip ? share(held[i].get(j), base, c) : 0.f;
+        }
+        s = team_fold(s, L, red, plus);
+    } else {
+        // running maximum and sum
+        constexpr int U = 4;
+        float mine = -INFINITY;
+        s = 0.f;
+        for (int64_t i = tt; i < nv; i += int64_t(U) * L) {
+            Vec<T, N> v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = load_vec<T, N>(z + Place<N>(i + int64_t(u) * L, g.V).at);
+            float high = mine;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const Place<N> at(i + int64_t(u) * L, g.V);
+#pragma unroll
+                for (int j = 0; j < N; ++j) high = fmaxf(high, j >= at.skip ? v[u].get(j) : -INFINITY);
+            }
+            const float base = high == -INFINITY ? 0.f : high;   // nothing yet but masked logits
+            s *= share(mine, base, c);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const Place<N> at(i + int64_t(u) * L, g.V);
+#pragma unroll
+                for (int j = 0; j < N; ++j) s += j >= at.skip ? share(v[u].get(j), base, c) : 0.f;
+            }
+            mine = high;
+        }
+        m = team_fold(mine, L, red, most);
+        // a thread without a logit above -inf has s == 0; with none at all the sum is 0
+        s = team_fold(mine == -INFINITY ? s : s * share(mine, m, c), L, red, plus);
+    }
+    if (OP == GC_OP_FWD && tt == 0) {
+        if (peak) peak[row] = m;
+        if (mass) mass[row] = s;
+    }
+    team_sync(L <= 64);     // the entries are in LDS
+    if (OP != GC_OP_BWD && tt < width) {
+        // log q = (z - peak)/t - log(mass), log p = (teacher - top)/t - log(total)
+        const float log_s = logf(s), log_total = logf(total);
+        float sum = 0.f;
+        for (int k = lane; k < g.K; k += width) {
+            const Entry e = entry[k];
+            int at;
+            float v;
+            entry_at(k, at, v);
+            if (some && e.p != 0.f)
+                sum += e.z == -INFINITY ? INFINITY : e.p * (((v - top) - (e.z - m)) / t - log_total + log_s);
+        }
+        sum = lanes_fold(sum, width, plus);
+        if (tt == 0) loss[row] = t * t * sum;
+    }
+    if (OP == GC_OP_FWD) return;
+
+    const float by = some ? dloss[row] * t : 0.f, inv = by / s;
+    T *out = dlogits + row * g.ld_grad;
+    auto write = [&](const Vec<T, N> &v, int64_t i) {
+        const Place<N> at(i, g.V);
+        if (!at.live) return;
+        float y[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) y[j] = some ? share(v.get(j), m, c) * inv : 0.f;
+        Vec<T, N> o;
+        o.put(y);
+        put_own<PAST, T, N>(out + at.at, o, at.skip);
+    };
+    if (NV) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) write(held[i], int64_t(i) * L + tt);
+    } else {
+        constexpr int U = 4;
+        for (int64_t i = tt; i < nv; i += int64_t(U) * L) {
+            Vec<T, N> v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = load_vec<T, N>(z + Place<N>(i + int64_t(u) * L, g.V).at);
+#pragma unroll
+            for (int u = 0; u < U; ++u) write(v[u], i + int64_t(u) * L);
+        }
+    }
+    if (!some) return;
+    // the stores above have arrived before any of the entries' begins
+    __builtin_amdgcn_s_waitcnt(0);
+    team_sync(L <= 64);
+    for (int k = tt; k < g.K; k += L) {
+        const Entry e = entry[k];
+        if (e.at < 0) continue;
+        float p = 0.f;
+        bool first = true;
+        for (int o = 0; o < g.K; ++o) {
+            const bool same = entry[o].at == e.at;
+            if (same) p += entry[o].p;
+            first &= !(same && o < k);
+        }
+        if (first) out[e.at] = from_f32<T>(by * (share(e.z, m, c) / s - p));
+    }
+}
+
+// Calls f(NV) for the numbers of vectors a thread may hold.
+template <typename F>
+hipError_t with_held(int nv, F f)
+{
+    switch (nv) {
+    case 0: return f(std::integral_constant<int, 0>());
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 3: return f(std::integral_constant<int, 3>());
+    case 4: return f(std::integral_constant<int, 4>());
+    case 5: return f(std::integral_constant<int, 5>());
+    case 6: return f(std::integral_constant<int, 6>());
+    case 8: return f(std::integral_constant<int, 8>());
+    case 10: return f(std::integral_constant<int, 10>());
+    case 12: return f(std::integral_constant<int, 12>());
+    case 16: return f(std::integral_constant<int, 16>());
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+void plan_distill(const DistillGeom &g, int dtype, int op, DistillPlan &q)
+{
+    q = DistillPlan{};
+    const int vec = dtype == GC_F32 ? 4 : 8;
+    q.N = g.V < vec ? 1 : vec;
+    const int64_t nv = vectors(g.V, q.N);
+    q.L = 8;
+    while (q.L < 64 && q.L * 2 < nv) q.L *= 2;
+    while (q.L < 1024 && q.L * 4 < nv) q.L *= 2;
+    q.threads = std::max(256, q.L);
+    while (q.L <= 64 && size_t(q.threads / q.L) * g.K * 12 > 49152) {
+        if (q.threads > 64) q.threads /= 2;
+        else q.L *= 2;
+    }
+    if (q.L > 64) q.threads = q.L;
+    if (op == GC_OP_STEP) {
+        q.NV = int(std::min<int64_t>(17, (nv + q.L - 1) / q.L));
+        if (q.NV == 7 || q.NV == 9 || q.NV == 11) ++q.NV;
+        if (q.NV > 12) q.NV = q.NV <= 16 ? 16 : 0;
+    }
+    const int teams = q.threads / q.L;
+    q.grid = (g.rows + teams - 1) / teams;
+    q.lds_bytes = size_t(teams) * g.K * 12;
+    q.past = op != GC_OP_FWD && q.N > 1 && size_t(g.rows) * g.V * (dtype == GC_F32 ? 8 : 4) >= kStreamBytes;
+}
+
+template <typename T>
+hipError_t launch_distill(const DistillGeom &g, const DistillPlan &q, int op, const void *logits, const void *index,
+                          const void *teacher, float *peak, float *mass, const float *dloss, float *loss, void *dlogits,
+                          hipStream_t s)
+{
+    if (!g.rows) return hipSuccess;
+    auto go = [&](auto n, auto nv, auto o, auto past) {
+        hipLaunchKernelGGL((distill<T, decltype(n)::value, decltype(nv)::value, decltype(o)::value, decltype(past)::value>),
+                           dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s, g, q.L, static_cast<const T *>(logits),
+                           index, teacher, peak, mass, dloss, loss, static_cast<T *>(dlogits));
+        return hipGetLastError();
+    };
+    using Fwd = std::integral_constant<int, GC_OP_FWD>;
+    using Bwd = std::integral_constant<int, GC_OP_BWD>;
+    using Step = std::integral_constant<int, GC_OP_STEP>;
+    using None = std::integral_constant<int, 0>;
+    auto with_op = [&](auto n) {
+        constexpr bool WIDE = decltype(n)::value > 1;
+        if (op == GC_OP_FWD) return go(n, None(), Fwd(), std::false_type());
+        if (op == GC_OP_BWD) return with_past<WIDE>(q.past, [&](auto past) { return go(n, None(), Bwd(), past); });
+        if constexpr (!WIDE) return go(n, std::integral_constant<int, 1>(), Step(), std::false_type());
+        else
+            return with_held(q.NV, [&](auto nv) {
+                return with_past<WIDE>(q.past, [&](auto past) { return go(n, nv, Step(), past); });
+            });
+    };
+    if (q.N == 1) return with_op(std::integral_constant<int, 1>());
+    return with_op(std::integral_constant<int, kVec<T>>());
+}
+
+#define GC_DISTILL_INSTANCES(T)                                                                                     \
+    template hipError_t launch_distill<T>(const DistillGeom &, const DistillPlan &, int, const void *, const void *, \
+                                          const void *, float *, float *, const float *, float *, void *, hipStream_t);
+GC_DISTILL_INSTANCES(float)
+GC_DISTILL_INSTANCES(bf16_t)
+
+}  // namespace gc

@@ -1,0 +1,515 @@
+// norm_rows.hip -- layer norm of rows, the residual stream's addition with it, and the
+// backward pass with the gradients of its weights.
+//
+//   s = x + residual,  hat = (s - mean) * rstd,  y = gamma * hat + beta
+//   w = gamma * dy,  dx = dtotal + rstd * (w - mean(w) - hat * mean(w*hat))
+//   dgamma = sum over rows of dy*hat,  dbeta = sum over rows of dy
+//
+// Memory bound: a row is read once into the registers of a team of threads, which adds up
+// its sums by lane exchanges (a team of one wave) or through LDS, and writes its outputs.  Teams
+// walk rows, so gamma and beta are read once a team, and the backward's sums over rows
+// stay in registers until a team's last row.  Rows past a workgroup's registers are
+// walked in several passes.
+#include <algorithm>
+#include <type_traits>
+
+#include "gc_core.h"
+#include "gc_norm.h"
+#include "gc_norm_res.h"
+
+namespace gc {
+namespace {
+
+// Place of vector number i of a row of D >= N values.  The last vector of a row whose length is
+// no multiple of N is moved back to end with the row; its first `skip` elements belong
+// to the vector before it and are neither counted nor stored.
+template <int N>
+struct Place {
+    int at, skip;
+    bool live;
+    __device__ __forceinline__ Place(int i, int D)
+    {
+        const int first = i * N;
+        live = first < D;
+        at = live ? min(first, D - N) : 0;
+        skip = live ? first - at : N;
+    }
+};
+
+// Stores the elements that are this vector's own.
+template <bool PAST, typename T, int N>
+__device__ __forceinline__ void put_own(T *p, const Vec<T, N> &v, int skip)
+{
+    if (N == 1 || skip == 0) {
+        put_vec<PAST, T, N>(p, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j >= skip) p[j] = from_f32<T>(v.get(j));
+    }
+}
+
+// N neighbouring values of gamma or beta in fp32.
+template <typename T, int N>
+__device__ __forceinline__ void params_at(const RowsGeom &g, const void *p, int at, float none, float (&v)[N])
+{
+    if (!p) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = none;
+    } else if (g.pf32) {
+        const Vec<float, N> w = load_vec<float, N>(static_cast<const float *>(p) + at);
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = w.get(j);
+    } else {
+        const Vec<T, N> w = load_vec<T, N>(static_cast<const T *>(p) + at);
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = w.get(j);
+    }
+}
+
+// Sums over the L threads of a team, the same value for all: lanes of a wave, or whole
+// waves of a workgroup that may hold several such teams (`red` 16*K values).
+template <int K>
+__device__ __forceinline__ void rows_sum(float (&v)[K], int L, float *red)
+{
+    const int w = L < 64 ? L : 64;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = lanes_sum(v[k], w);
+    if (L <= 64) return;
+    const int wave = threadIdx.x >> 6, nw = L >> 6, first = wave & ~(nw - 1);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) red[k * 16 + wave] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        float s = red[k * 16 + first];
+        for (int i = 1; i < nw; ++i) s += red[k * 16 + first + i];
+        v[k] = s;
+    }
+}
+
+// ----------------------------------------------------------------- forward --
+// The values of a row stay in fp32, 32 a thread at most.  The mean first, then the squares around
+// it, so a mean far from zero costs no precision.
+template <typename T, int N, int NV, bool RES, bool PAST>
+__global__ void __launch_bounds__(512) rows_fwd(RowsGeom g, int L, const T *x, const T *res,
+                                                 const void *__restrict__ gamma, const void *__restrict__ beta,
+                                                 T *y, T *total, float *__restrict__ mean, float *__restrict__ rstd)
+{
+    __shared__ float red[16];
+    const int tt = threadIdx.x & (L - 1), teams = blockDim.x / L;
+    float gm[NV][N], bt[NV][N];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const Place<N> at(i * L + tt, g.D);
+        params_at<T, N>(g, gamma, at.at, 1.f, gm[i]);
+        params_at<T, N>(g, beta, at.at, 0.f, bt[i]);
+    }
+    const float inv = 1.f / float(g.D);
+    // every team of a workgroup takes as many turns, for the barriers; one without a row reads the last again
+    for (int64_t turn = int64_t(blockIdx.x) * teams; turn < g.rows; turn += int64_t(gridDim.x) * teams) {
+        const bool own = turn + threadIdx.x / L < g.rows;
+        const int64_t row = own ? turn + threadIdx.x / L : g.rows - 1;
+        const T *xr = x + row * g.ld_x;
+        Vec<T, N> xv[NV], rv[RES ? NV : 1];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Place<N> at(i * L + tt, g.D);
+            xv[i] = load_vec<T, N>(xr + at.at);
+            if (RES) rv[i] = load_vec<T, N>(res + row * g.ld_res + at.at);
+        }
+        float v[NV][N];
+        float sum[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Place<N> at(i * L + tt, g.D);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                v[i][j] = xv[i].get(j);
+                if (RES) v[i][j] += rv[i].get(j);
+                sum[0] += j >= at.skip ? v[i][j] : 0.f;
+            }
+        }
+        rows_sum<1>(sum, L, red);
+        const float m = sum[0] * inv;
+        float sq[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Place<N> at(i * L + tt, g.D);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float off = v[i][j] - m;
+                sq[0] += j >= at.skip ? off * off : 0.f;
+            }
+        }
+        rows_sum<1>(sq, L, red);
+        const float r = 1.f / sqrtf(sq[0] * inv + g.eps);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Place<N> at(i * L + tt, g.D);
+            if (!at.live || !own) continue;
+            Vec<T, N> out;
+            if (total) {
+                out.put(v[i]);
+                put_own<PAST, T, N>(total + row * g.ld_total + at.at, out, at.skip);
+            }
+            float z[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) z[j] = (v[i][j] - m) * r * gm[i][j] + bt[i][j];
+            out.put(z);
+            put_own<PAST, T, N>(y + row * g.ld_y + at.at, out, at.skip);
+        }
+        if (tt == 0 && own) {
+            if (mean) mean[row] = m;
+            if (rstd) rstd[row] = r;
+        }
+    }
+}
+
+// A row past the registers: three passes over it by one workgroup.
+template <typename T, int N>
+__global__ void __launch_bounds__(1024) rows_fwd_loop(RowsGeom g, const T *x, const T *res,
+                                                      const void *__restrict__ gamma, const void *__restrict__ beta,
+                                                      T *y, T *total, float *__restrict__ mean,
+                                                      float *__restrict__ rstd)
+{
+    __shared__ float red[16];
+    const int nv = vectors(g.D, N);
+    const float inv = 1.f / float(g.D);
+    for (int64_t row = blockIdx.x; row < g.rows; row += gridDim.x) {
+        const T *xr = x + row * g.ld_x, *rr = res ? res + row * g.ld_res : nullptr;
+        auto values = [&](int at, float (&v)[N]) {
+            const Vec<T, N> a = load_vec<T, N>(xr + at);
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = a.get(j);
+            if (!rr) return;
+            const Vec<T, N> b = load_vec<T, N>(rr + at);
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] += b.get(j);
+        };
+        float sum = 0.f, sq = 0.f, v[N];
+        for (int i = threadIdx.x; i < nv; i += blockDim.x) {
+            const Place<N> at(i, g.D);
+            values(at.at, v);
+#pragma unroll
+            for (int j = 0; j < N; ++j) sum += j >= at.skip ? v[j] : 0.f;
+        }
+        const float m = block_sum(sum, red) * inv;
+        for (int i = threadIdx.x; i < nv; i += blockDim.x) {
+            const Place<N> at(i, g.D);
+            values(at.at, v);
+#pragma unroll
+            for (int j = 0; j < N; ++j) sq += j >= at.skip ? (v[j] - m) * (v[j] - m) : 0.f;
+        }
+        const float r = 1.f / sqrtf(block_sum(sq, red) * inv + g.eps);
+        for (int i = threadIdx.x; i < nv; i += blockDim.x) {
+            const Place<N> at(i, g.D);
+            values(at.at, v);
+            float gm[N], bt[N];
+            params_at<T, N>(g, gamma, at.at, 1.f, gm);
+            params_at<T, N>(g, beta, at.at, 0.f, bt);
+            Vec<T, N> out;
+            if (total) {
+                out.put(v);
+                put_own<false, T, N>(total + row * g.ld_total + at.at, out, at.skip);
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = (v[j] - m) * r * gm[j] + bt[j];
+            out.put(v);
+            put_own<false, T, N>(y + row * g.ld_y + at.at, out, at.skip);
+        }
+        if (threadIdx.x == 0) {
+            if (mean) mean[row] = m;
+            if (rstd) rstd[row] = r;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- backward --
+// Adds up the running sums of a workgroup's teams and writes them as one row of D
+// pairs (dbeta's, dgamma's): teams within a wave by lane exchanges, the others
+// in order through one row in LDS.
+template <int N, int NV>
+__device__ __forceinline__ void write_part(int D, int L, float (&db)[NV][N], float (&dg)[NV][N], float *row, float *part)
+{
+    const int tt = threadIdx.x & (L - 1);
+    for (int m = 32; m >= L; m >>= 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                db[i][j] += __shfl_xor(db[i][j], m, 64);
+                dg[i][j] += __shfl_xor(dg[i][j], m, 64);
+            }
+    }
+    const int wide = L < 64 ? 64 : L, turns = blockDim.x / wide, turn = threadIdx.x / wide;
+    const bool writes = int(threadIdx.x) % wide < L;
+    for (int w = 0; w < turns; ++w) {
+        if (w == turn && writes) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const Place<N> at(i * L + tt, D);
+                if (!at.live) continue;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    if (j < at.skip) continue;
+                    float *dst = (turns > 1 && w < turns - 1 ? row : part) + 2 * int64_t(at.at + j);
+                    const float *src = row + 2 * int64_t(at.at + j);
+                    dst[0] = w ? src[0] + db[i][j] : db[i][j];
+                    dst[1] = w ? src[1] + dg[i][j] : dg[i][j];
+                }
+            }
+        }
+        if (turns > 1) __syncthreads();
+    }
+}
+
+template <typename T, int N, int NV, bool PAST>
+__global__ void __launch_bounds__(512) rows_bwd(RowsGeom g, int L, const T *x, const void *__restrict__ gamma,
+                                                const T *dy, const T *dtotal, const float *__restrict__ mean,
+                                                const float *__restrict__ rstd, T *dx, float *__restrict__ part)
+{
+    __shared__ float red[32];
+    extern __shared__ float joined[];
+    const int tt = threadIdx.x & (L - 1), teams = blockDim.x / L;
+    float gm[NV][N], dg[NV][N] = {}, db[NV][N] = {};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const Place<N> at(i * L + tt, g.D);
+        params_at<T, N>(g, gamma, at.at, 1.f, gm[i]);
+    }
+    const float inv = 1.f / float(g.D);
+    // every team of a workgroup takes as many turns, for the barriers; one without a row reads the last again
+    for (int64_t turn = int64_t(blockIdx.x) * teams; turn < g.rows; turn += int64_t(gridDim.x) * teams) {
+        const bool own = turn + threadIdx.x / L < g.rows;
+        const int64_t row = own ? turn + threadIdx.x / L : g.rows - 1;
+        Vec<T, N> xv[NV], dv[NV], tv[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Place<N> at(i * L + tt, g.D);
+            xv[i] = load_vec<T, N>(x + row * g.ld_x + at.at);
+            dv[i] = load_vec<T, N>(dy + row * g.ld_y + at.at);
+            if (dtotal) tv[i] = load_vec<T, N>(dtotal + row * g.ld_total + at.at);
+        }
+        const float m = mean[row], r = rstd[row];
+        float c[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Place<N> at(i * L + tt, g.D);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float hat = (xv[i].get(j) - m) * r;
+                const float d = own && j >= at.skip ? dv[i].get(j) : 0.f;
+                const float dh = own && j >= at.skip ? d * hat : 0.f;
+                db[i][j] += d;
+                dg[i][j] += dh;
+                c[0] += gm[i][j] * d;
+                c[1] += gm[i][j] * dh;
+            }
+        }
+        rows_sum<2>(c, L, red);
+        const float c1 = c[0] * inv, c2 = c[1] * inv;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Place<N> at(i * L + tt, g.D);
+            if (!at.live || !own) continue;
+            float z[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float hat = (xv[i].get(j) - m) * r;
+                z[j] = r * (gm[i][j] * dv[i].get(j) - c1 - hat * c2);
+                if (dtotal) z[j] += tv[i].get(j);
+            }
+            Vec<T, N> out;
+            out.put(z);
+            put_own<PAST, T, N>(dx + row * g.ld_res + at.at, out, at.skip);
+        }
+    }
+    if (part) write_part<N, NV>(g.D, L, db, dg, joined, part + int64_t(blockIdx.x) * 2 * g.D);
+}
+
+// Rows past the registers: the sums over rows first, by columns (dx may take dy's place),
+// then dx in two passes over a row.
+template <typename T>
+__global__ void __launch_bounds__(256) rows_bwd_columns(RowsGeom g, const T *__restrict__ x, const T *__restrict__ dy,
+                                                        const float *__restrict__ mean, const float *__restrict__ rstd,
+                                                        float *__restrict__ part)
+{
+    const int e = blockIdx.x * 256 + threadIdx.x;
+    if (e >= g.D) return;
+    float db = 0.f, dg = 0.f;
+    for (int64_t row = blockIdx.y; row < g.rows; row += gridDim.y) {
+        const float d = to_f32(dy[row * g.ld_y + e]);
+        db += d;
+        dg += d * ((to_f32(x[row * g.ld_x + e]) - mean[row]) * rstd[row]);
+    }
+    float *to = part + (int64_t(blockIdx.y) * g.D + e) * 2;
+    to[0] = db;
+    to[1] = dg;
+}
+
+template <typename T, int N>
+__global__ void __launch_bounds__(1024) rows_bwd_loop(RowsGeom g, const T *x, const void *__restrict__ gamma,
+                                                      const T *dy, const T *dtotal, const float *__restrict__ mean,
+                                                      const float *__restrict__ rstd, T *dx)
+{
+    __shared__ float red[32];
+    const int nv = vectors(g.D, N);
+    const float inv = 1.f / float(g.D);
+    for (int64_t row = blockIdx.x; row < g.rows; row += gridDim.x) {
+        const T *xr = x + row * g.ld_x, *dr = dy + row * g.ld_y;
+        const float m = mean[row], r = rstd[row];
+        float c[2] = {0.f, 0.f}, gm[N];
+        for (int i = threadIdx.x; i < nv; i += blockDim.x) {
+            const Place<N> at(i, g.D);
+            params_at<T, N>(g, gamma, at.at, 1.f, gm);
+            const Vec<T, N> xv = load_vec<T, N>(xr + at.at), dv = load_vec<T, N>(dr + at.at);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float w = j >= at.skip ? gm[j] * dv.get(j) : 0.f;
+                c[0] += w;
+                c[1] += j >= at.skip ? w * ((xv.get(j) - m) * r) : 0.f;
+            }
+        }
+        rows_sum<2>(c, 1024, red);
+        const float c1 = c[0] * inv, c2 = c[1] * inv;
+        for (int i = threadIdx.x; i < nv; i += blockDim.x) {
+            const Place<N> at(i, g.D);
+            params_at<T, N>(g, gamma, at.at, 1.f, gm);
+            const Vec<T, N> xv = load_vec<T, N>(xr + at.at), dv = load_vec<T, N>(dr + at.at);
+            float z[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) z[j] = r * (gm[j] * dv.get(j) - c1 - (xv.get(j) - m) * r * c2);
+            if (dtotal) {
+                const Vec<T, N> tv = load_vec<T, N>(dtotal + row * g.ld_total + at.at);
+#pragma unroll
+                for (int j = 0; j < N; ++j) z[j] += tv.get(j);
+            }
+            Vec<T, N> out;
+            out.put(z);
+            put_own<false, T, N>(dx + row * g.ld_res + at.at, out, at.skip);
+        }
+    }
+}
+
+constexpr int kFwdHeld = 32, kBwdHeld = 16;   // values of a row that a thread holds, at most
+
+// Calls f(N, NV) with the plan's vector as compile-time constants.
+template <typename T, int MOST, typename F>
+hipError_t with_vectors(const RowsPlan &q, F f)
+{
+    if (q.N == 1) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
+    return with_nv<MOST / kVec<T>>(q.NV, [&](auto nv) { return f(std::integral_constant<int, kVec<T>>(), nv); });
+}
+
+}  // namespace
+
+void plan_rows(const RowsGeom &g, int dtype, bool bwd, bool more, RowsPlan &q)
+{
+    q = RowsPlan{};
+    const int vec = dtype == GC_F32 ? 4 : 8, held = bwd ? kBwdHeld : kFwdHeld;
+    const int threads = 512;
+    q.N = g.D < vec ? 1 : vec;
+    const int64_t nv = vectors(g.D, q.N);
+    const int most = q.N == 1 ? 1 : held / vec;
+    q.loop = nv > int64_t(threads) * most;
+    const int64_t rows = std::max<int64_t>(1, g.rows);
+    if (q.loop) {
+        q.N = vec;
+        q.NV = 1;
+        q.L = q.threads = 1024;
+        q.grid = std::min<int64_t>(rows, 4 * kCUs);
+        q.parts = std::min<int64_t>(rows, 64);
+    } else {
+        // the smallest team that holds a row; while there are fewer teams than the chip takes, twice the threads
+        q.L = 1;
+        while (int64_t(q.L) * most < nv) q.L *= 2;
+        while (q.L < threads && q.L < nv && rows * q.L < 1024 * kCUs / 4) q.L *= 2;
+        q.NV = int((nv + q.L - 1) / q.L);
+        while (!(q.NV <= 4 || q.NV == 8)) ++q.NV;   // the instances there are
+        q.threads = bwd ? 512 : std::max(256, q.L);
+        const int teams = q.threads / q.L;
+        q.grid = std::min<int64_t>((rows + teams - 1) / teams, bwd ? kCUs * 512 / q.threads : kCUs * 2048 / q.threads);
+        q.parts = q.grid;
+        q.lds_bytes = bwd && q.threads > std::max(64, q.L) ? size_t(g.D) * 8 : 0;
+    }
+    const size_t bytes = size_t(rows) * g.D * (dtype == GC_F32 ? 4 : 2) * ((bwd ? 3 : 2) + (more ? (bwd ? 1 : 2) : 0));
+    q.past = !q.loop && q.N > 1 && bytes >= kStreamBytes;
+    q.ws_bytes = bwd ? (size_t(q.parts) * g.D * 8 + 255) & ~size_t(255) : 0;
+}
+
+template <typename T>
+hipError_t launch_rows_fwd(const RowsGeom &g, const RowsPlan &q, const void *x, const void *res, const void *gamma,
+                           const void *beta, void *y, void *total, float *mean, float *rstd, hipStream_t s)
+{
+    const T *xt = static_cast<const T *>(x), *rt = static_cast<const T *>(res);
+    T *yt = static_cast<T *>(y), *tt = static_cast<T *>(total);
+    if (q.loop) {
+        hipLaunchKernelGGL((rows_fwd_loop<T, kVec<T>>), dim3(unsigned(q.grid)), dim3(q.threads), 0, s, g, xt, rt, gamma,
+                           beta, yt, tt, mean, rstd);
+        return hipGetLastError();
+    }
+    return with_vectors<T, kFwdHeld>(q, [&](auto n, auto nv) {
+        constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
+        auto go = [&](auto r) {
+            return with_past<(N > 1)>(q.past, [&](auto past) {
+                hipLaunchKernelGGL((rows_fwd<T, N, NV, decltype(r)::value, decltype(past)::value>), dim3(unsigned(q.grid)),
+                                   dim3(q.threads), 0, s, g, q.L, xt, rt, gamma, beta, yt, tt, mean, rstd);
+                return hipGetLastError();
+            });
+        };
+        return rt ? go(std::true_type()) : go(std::false_type());
+    });
+}
+
+template <typename T>
+hipError_t launch_rows_bwd(const RowsGeom &g, const RowsPlan &q, const void *x, const void *gamma, const void *dy,
+                           const void *dtotal, const float *mean, const float *rstd, void *dx, void *dgamma,
+                           void *dbeta, float *part, hipStream_t s)
+{
+    const T *xt = static_cast<const T *>(x), *dt = static_cast<const T *>(dy), *tt = static_cast<const T *>(dtotal);
+    T *out = static_cast<T *>(dx);
+    const bool sums = dgamma || dbeta;
+    if (g.rows) {
+        hipError_t e;
+        if (q.loop) {
+            if (sums) {
+                hipLaunchKernelGGL((rows_bwd_columns<T>), dim3(unsigned((g.D + 255) / 256), unsigned(q.parts)), dim3(256), 0,
+                                   s, g, xt, dt, mean, rstd, part);
+                if (e = hipGetLastError(); e != hipSuccess) return e;
+            }
+            hipLaunchKernelGGL((rows_bwd_loop<T, kVec<T>>), dim3(unsigned(q.grid)), dim3(q.threads), 0, s, g, xt, gamma, dt,
+                               tt, mean, rstd, out);
+            e = hipGetLastError();
+        } else {
+            e = with_vectors<T, kBwdHeld>(q, [&](auto n, auto nv) {
+                constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
+                return with_past<(N > 1)>(q.past, [&](auto past) {
+                    hipLaunchKernelGGL((rows_bwd<T, N, NV, decltype(past)::value>), dim3(unsigned(q.grid)),
+                                       dim3(q.threads), q.lds_bytes, s, g, q.L, xt, gamma, dt, tt, mean, rstd, out,
+                                       sums ? part : nullptr);
+                    return hipGetLastError();
+                });
+            });
+        }
+        if (e != hipSuccess) return e;
+    }
+    NormGeom n{};
+    n.C = g.D;
+    n.pf32 = g.pf32;
+    return launch_norm_params<T>(n, g.rows ? q.parts : 0, part, dgamma, dbeta, s);
+}
+
+#define GC_ROWS_INSTANCES(T)                                                                                          \
+    template hipError_t launch_rows_fwd<T>(const RowsGeom &, const RowsPlan &, const void *, const void *, const void *, \
+                                           const void *, void *, void *, float *, float *, hipStream_t);               \
+    template hipError_t launch_rows_bwd<T>(const RowsGeom &, const RowsPlan &, const void *, const void *, const void *, \
+                                           const void *, const float *, const float *, void *, void *, void *, float *, \
+                                           hipStream_t);
+GC_ROWS_INSTANCES(float)
+GC_ROWS_INSTANCES(bf16_t)
+
+}  // namespace gc

@@ -294,6 +294,139 @@ int gc_grad_norm(const gc_tensor *list, int count, float prescale, float *norm, 
 int gc_grad_clip(const gc_tensor *list, int count, float max_norm, float prescale, float eps, float *norm,
                  void *workspace, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The recurrent core that a policy has behind its encoder, and the loss of its
+ * head.  The conventions of the operators above hold.
+ * ------------------------------------------------------------------------ */
+
+/* Layer norm of rows, with the residual stream's addition in the same pass:
+ *
+ *   s     = x + residual                 (x alone where residual is NULL)
+ *   y     = gamma * (s - mean) * rstd + beta,  rstd = 1 / sqrt(var + eps)  (var biased, over the row)
+ *   total = s                            (where total is not NULL)
+ *
+ * s is added in fp32 and normed as it is; total and y are each rounded once.
+ * Rows have D values and lie ld elements apart (ld >= D: parts of wider rows;
+ * the elements between are not touched).  gamma, beta, dgamma and dbeta [D]
+ * have param_dtype, GC_F32 or dtype; gamma == NULL stands for ones, beta ==
+ * NULL for zeros.  mean and rstd [rows] are fp32; the forward writes them where
+ * they are not NULL.  total may be residual or x, with the same row distance.
+ * rows may be 0 and is at most 2^31 - 1; D is at most 2^23. */
+typedef struct {
+    int64_t rows;
+    int D;
+    float eps;                                   /* >= 0 */
+    int64_t ld_x, ld_residual, ld_total, ld_y;   /* elements between rows */
+} gc_layer_norm_desc;
+
+int gc_layer_norm_fwd(const void *x, const void *residual, const void *gamma, const void *beta, void *y, void *total,
+                      float *mean, float *rstd, const gc_layer_norm_desc *d, int dtype, int param_dtype, void *stream);
+
+/* With x the normed rows (the forward's total where it had a residual), hat =
+ * (x - mean) * rstd and w = gamma * dy:
+ *
+ *   dx     = dtotal + rstd * (w - mean of w - hat * mean of w*hat)   (means over the row)
+ *   dgamma = sum over rows of dy*hat,  dbeta = sum over rows of dy
+ *
+ * dtotal, the gradient that reaches the residual stream past the norm, may be
+ * NULL; dx is the gradient of x and of the residual alike, and may be dtotal or
+ * dy, with the same row distance.  Row distances: x ld_x, dy ld_y, dtotal ld_total, dx
+ * ld_residual.  dgamma and dbeta may be NULL; with rows == 0 they are zeros.
+ * Sums have a fixed order: bit-identical from run to run. */
+size_t gc_layer_norm_workspace_bytes(const gc_layer_norm_desc *d, int dtype);
+int gc_layer_norm_bwd(const void *x, const void *gamma, const void *dy, const void *dtotal, const float *mean,
+                      const float *rstd, void *dx, void *dgamma, void *dbeta, void *workspace, size_t ws_bytes,
+                      const gc_layer_norm_desc *d, int dtype, int param_dtype, void *stream);
+
+/* The gated linear recurrence over B sequences of up to T steps of D channels:
+ *
+ *   a = sigmoid(gate),  i = coupled ? 1 - a : 1
+ *   h[b,t,:] = a[b,t,:] * (reset[b,t] ? 0 : h[b,t-1,:]) + i[b,t,:] * value[b,t,:],   out = h
+ *
+ * h before the first step is h0 [B][D] (fp32; NULL for zeros), after the last
+ * one it is written to last [B][D] (fp32, may be NULL, may be h0).  reset, one
+ * byte a step (not 0: the step starts anew, as after an episode's end or at the
+ * start of a sequence in a packed row; whatever the state held, also if it was
+ * not finite), and lengths [B] (int32; values are taken into [0, T]) may be NULL.
+ * Steps at and behind a sequence's length are not read; its out there is zeros,
+ * its last the state at its length.  T == 1 is the step of a policy that acts.
+ *
+ * gate, value, out and their gradients have the storage type, D dense channels,
+ * and two distances each (elements; reset: bytes): any order of batch and time,
+ * and parts of wider rows.  Distances of inputs may be 0; elements of outputs
+ * must not overlap.  States are fp32.  states, where it is not NULL, is what the
+ * backward needs: [B][ceil(T/16)][D] fp32, h before every sixteenth step.
+ * B and T may be 0; T is at most 2^30, GC_ERR_UNSUPPORTED where B*D is 2^31
+ * or more. */
+enum { GC_RECURRENCE_BLOCK = 16 };      /* steps between two kept states */
+typedef struct {
+    int64_t batch, step;                /* distance of two sequences, of two steps */
+} gc_strides;
+typedef struct {
+    int B, T, D;
+    int coupled;                        /* 0 or 1 */
+    gc_strides gate, value, out, dgate, dvalue, reset;
+} gc_recurrence_desc;
+
+size_t gc_recurrence_workspace_bytes(int op, const gc_recurrence_desc *d, int dtype);
+int gc_recurrence_fwd(const void *gate, const void *value, const float *h0, const uint8_t *reset, const int32_t *lengths,
+                      void *out, float *last, float *states, void *workspace, size_t ws_bytes,
+                      const gc_recurrence_desc *d, int dtype, void *stream);
+
+/* With g the gradient of h[b,t,:], which is dout and what comes back from the
+ * step after it (dlast [B][D], NULL for zeros, behind the last step), and h' the state
+ * a step starts from (0 at a reset):
+ *
+ *   dvalue = i * g,   dgate = a * (1 - a) * (h' - (coupled ? value : 0)) * g,   dh0 = h0's share
+ *
+ * h' is computed anew from states, so out is not read.  dout has the distances
+ * of out.  dgate and dvalue are zeros behind a sequence's length.  dh0 [B][D]
+ * fp32 may be NULL, and may be dlast.  Every sum has a fixed order. */
+int gc_recurrence_bwd(const void *gate, const void *value, const float *states, const uint8_t *reset,
+                      const int32_t *lengths, const void *dout, const float *dlast, void *dgate, void *dvalue, float *dh0,
+                      void *workspace, size_t ws_bytes, const gc_recurrence_desc *d, int dtype, void *stream);
+
+/* Distillation of a head from a teacher's K top logits a row, at a temperature t:
+ *
+ *   p = softmax(teacher / t) over the row's entries,  q = softmax(logits / t) over its V logits
+ *   loss     = t^2 * sum over entries of p * (log p - log q[index])
+ *   dlogits  = dloss * t * (q - sum of the p of the entries at that place)
+ *
+ * An entry whose index is outside [0, V) is empty, and an entry of p == 0 adds
+ * nothing; several entries may have one index.  A row without any entry of a
+ * teacher's logit above -inf has loss 0 and gradient 0, whatever its logits
+ * hold.  A logit of -inf has q == 0 (its loss is infinite where p is not 0).
+ * The forward also writes peak, the largest logit, and mass, the sum of
+ * exp((logits - peak) / t) (either may be NULL); the backward reads them.  dloss,
+ * loss, peak and mass are fp32 [rows].  logits and dlogits have the storage
+ * type, rows ld and ld_grad elements apart (>= V), index and teacher rows
+ * ld_index and ld_teacher elements apart (>= K).  dlogits may be logits, with the
+ * same row distance.  rows may be 0; rows and V are below 2^31, K is from 1 to 1024. */
+typedef struct {
+    int64_t rows;
+    int V, K;
+    int itype;              /* GC_I32 or GC_I64 */
+    int teacher_dtype;      /* gc_dtype of teacher */
+    float temperature;      /* > 0, finite */
+    int64_t ld, ld_grad, ld_index, ld_teacher;
+} gc_distill_desc;
+
+int gc_distill_fwd(const void *logits, const void *index, const void *teacher, float *loss, float *peak, float *mass,
+                   const gc_distill_desc *d, int dtype, void *stream);
+int gc_distill_bwd(const void *logits, const void *index, const void *teacher, const float *peak, const float *mass,
+                   const float *dloss, void *dlogits, const gc_distill_desc *d, int dtype, void *stream);
+/* Both at once, where dloss is known before the loss (a mean over rows, say):
+ * one read of the logits where a row fits a workgroup's registers. */
+int gc_distill_step(const void *logits, const void *index, const void *teacher, const float *dloss, float *loss,
+                    void *dlogits, const gc_distill_desc *d, int dtype, void *stream);
+
+/* Which kernels these would run (pure host, as gc_conv_plan_name): op is GC_OP_FWD
+ * or GC_OP_BWD, for the distillation also GC_OP_STEP, both at once. */
+enum { GC_OP_STEP = 6 };
+int gc_layer_norm_plan_name(int op, const gc_layer_norm_desc *d, int dtype, char *buf, size_t buf_bytes);
+int gc_recurrence_plan_name(int op, const gc_recurrence_desc *d, int dtype, char *buf, size_t buf_bytes);
+int gc_distill_plan_name(int op, const gc_distill_desc *d, int dtype, char *buf, size_t buf_bytes);
+
 /* Human-readable name of a status code. */
 const char *gc_status_string(int status);
 
