@@ -23,19 +23,22 @@ namespace gc {
 namespace {
 
 constexpr int kBlock = GC_RECURRENCE_BLOCK;
+constexpr int kHalf = kBlock / 2;
 
 // Where a thread works: sequence b, channels d .. d+N-1, of which the first `skip` belong to
 // the thread before it (the last vector of an odd row is moved back), steps [t0, t1) of chunk c.
+// b0 is the first thread's sequence, for addresses of a scalar and a 32-bit lane part.
 template <int N>
 struct Lane {
-    int b, d, skip, c, t0, t1, valid;
+    int b, b0, d, skip, c, t0, t1, valid;
     __device__ __forceinline__ bool find(const ScanGeom &g, const ScanPlan &q, const int32_t *lengths)
     {
-        const int64_t lane = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+        const int64_t lane = int64_t(blockIdx.x) * 64 + threadIdx.x;
         if (lane >= q.lanes) return false;
         uint32_t bb, v;
         fdivmod(uint32_t(lane), q.fd_nv, bb, v);
         b = int(bb);
+        b0 = __builtin_amdgcn_readfirstlane(b);
         d = min(int(v) * N, g.D - N);
         skip = int(v) * N - d;
         c = blockIdx.y;
@@ -44,10 +47,13 @@ struct Lane {
         valid = lengths ? min(max(lengths[b], 0), g.T) : g.T;
         return true;
     }
-    __device__ __forceinline__ int64_t at(const gc_strides &s, int t) const { return int64_t(b) * s.batch + int64_t(t) * s.step + d; }
-    // place among [B][D] fp32, and among [chunks][B][D]
+    // place among [B][D] fp32, among [chunks][B][D], and of the state before step t among [B][blocks][D]
     __device__ __forceinline__ int64_t end(const ScanGeom &g) const { return int64_t(b) * g.D + d; }
     __device__ __forceinline__ int64_t end(const ScanGeom &g, int chunk) const { return (int64_t(chunk) * g.B + b) * g.D + d; }
+    __device__ __forceinline__ int64_t state(const ScanGeom &g, int t) const
+    {
+        return (int64_t(b) * ((g.T - 1) / kBlock + 1) + t / kBlock) * g.D + d;
+    }
 };
 
 template <typename T, int N>
@@ -72,6 +78,58 @@ __device__ __forceinline__ void get_f32(const float *p, float (&v)[N])
     for (int j = 0; j < N; ++j) v[j] = w.get(j);
 }
 
+// A tensor along a thread's steps: a scalar base and distance, and the lane's offset from it
+// (Off: 32 bits where a wave's sequences lie within 4 GiB of each other).
+template <typename T, int N, typename Off>
+struct Line {
+    T *base;
+    int64_t step;
+    Off off;       // bytes
+    __device__ __forceinline__ Line(T *p, const gc_strides &s, const Lane<N> &w)
+        : base(p + int64_t(w.b0) * s.batch), step(s.step), off(Off((int64_t(w.b - w.b0) * s.batch + w.d) * int64_t(sizeof(T))))
+    {
+    }
+    __device__ __forceinline__ T *at(int t) const
+    {
+        typedef std::conditional_t<std::is_const_v<T>, const char, char> byte;
+        return reinterpret_cast<T *>(reinterpret_cast<byte *>(base + int64_t(t) * step) + off);
+    }
+    // `COUNT` steps from t; those from n on are not read
+    template <int COUNT, bool FULL>
+    __device__ __forceinline__ void load(Vec<std::remove_const_t<T>, N> (&v)[COUNT], int t, int n) const
+    {
+#pragma unroll
+        for (int u = 0; u < COUNT; ++u)
+            if (FULL || u < n) v[u] = load_vec<std::remove_const_t<T>, N>(at(t + u));
+    }
+};
+
+// The resets of a thread's steps, as bits.
+template <bool SOME>
+struct Resets {
+    const uint8_t *p;
+    int64_t step;
+    __device__ __forceinline__ Resets(const uint8_t *reset, const ScanGeom &g, int b)
+        : p(SOME ? reset + int64_t(b) * g.reset.batch : nullptr), step(g.reset.step)
+    {
+    }
+    template <int COUNT, bool FULL>
+    __device__ __forceinline__ uint32_t load(int t, int n) const
+    {
+        if (!SOME) return 0;
+        uint8_t v[COUNT];
+#pragma unroll
+        for (int u = 0; u < COUNT; ++u) {
+            v[u] = 0;
+            if (FULL || u < n) v[u] = p[(int64_t(t) + u) * step];
+        }
+        uint32_t bits = 0;
+#pragma unroll
+        for (int u = 0; u < COUNT; ++u) bits |= (v[u] ? 1u : 0u) << u;
+        return bits;
+    }
+};
+
 // a = sigmoid(f) and i = 1 - a, each to fp32 accuracy: e = exp(-f), a = 1/(1+e), i = e*a.  Below -80
 // e would overflow; a is then below 2e-35 instead of smaller, NaN stays NaN.
 __device__ __forceinline__ void gates(float f, float &a, float &i)
@@ -81,27 +139,6 @@ __device__ __forceinline__ void gates(float f, float &a, float &i)
     i = e * a;
 }
 
-// The elements of kBlock steps of a tensor, and the steps' resets as bits.  Steps from
-// `n` on are not read.
-template <typename T, int N>
-struct Steps {
-    Vec<T, N> v[kBlock];
-    __device__ __forceinline__ void load(const T *p, int64_t step, int n)
-    {
-#pragma unroll
-        for (int u = 0; u < kBlock; ++u)
-            if (u < n) v[u] = load_vec<T, N>(p + u * step);
-    }
-};
-__device__ __forceinline__ uint32_t load_resets(const uint8_t *p, int64_t step, int n)
-{
-    uint32_t bits = 0;
-#pragma unroll
-    for (int u = 0; u < kBlock; ++u)
-        if (u < n) bits |= (p[u * step] ? 1u : 0u) << u;
-    return bits;
-}
-
 // One step of the state; i is 1 - a.
 __device__ __forceinline__ float advance(float before, float i, float v, bool coupled)
 {
@@ -109,7 +146,58 @@ __device__ __forceinline__ float advance(float before, float i, float v, bool co
 }
 
 // ----------------------------------------------------------------- forward --
-template <typename T, int N>
+// Runs step(u, bit u of resets) for COUNT steps; without a reset in the wave, the steps' code
+// has none.
+template <int COUNT, bool SOME, typename F>
+__device__ __forceinline__ void each_step(uint32_t resets, F step)
+{
+    if (SOME && __any(resets != 0)) {
+#pragma unroll
+        for (int u = 0; u < COUNT; ++u) step(u, (resets >> u & 1) != 0);
+    } else {
+#pragma unroll
+        for (int u = 0; u < COUNT; ++u) step(u, false);
+    }
+}
+
+// Walks a thread's valid steps: body(t, count, FULL, gates, values, resets) for eight steps at a time while
+// every thread of the wave has sixteen more, their loads one half ahead, then for what is left.
+template <typename T, int N, bool SOME, typename Off, typename Body>
+__device__ __forceinline__ int walk(const Line<const T, N, Off> &x, const Line<const T, N, Off> &y, const Resets<SOME> &r,
+                                    int t, int t1, Body body)
+{
+    Vec<T, N> xa[kHalf], ya[kHalf], xb[kHalf], yb[kHalf];
+    if (__all(t + kBlock <= t1)) {
+        x.template load<kHalf, true>(xa, t, 0);
+        y.template load<kHalf, true>(ya, t, 0);
+        uint32_t ra = r.template load<kHalf, true>(t, 0);
+        for (;;) {
+            x.template load<kHalf, true>(xb, t + kHalf, 0);
+            y.template load<kHalf, true>(yb, t + kHalf, 0);
+            const uint32_t rb = r.template load<kHalf, true>(t + kHalf, 0);
+            body(t, kHalf, std::true_type(), xa, ya, ra);
+            const bool more = __all(t + 2 * kBlock <= t1);
+            if (more) {
+                x.template load<kHalf, true>(xa, t + kBlock, 0);
+                y.template load<kHalf, true>(ya, t + kBlock, 0);
+                ra = r.template load<kHalf, true>(t + kBlock, 0);
+            }
+            body(t + kHalf, kHalf, std::true_type(), xb, yb, rb);
+            t += kBlock;
+            if (!more) break;
+        }
+    }
+    for (; __any(t < t1); t += kHalf) {
+        const int n = min(kHalf, t1 - t);
+        x.template load<kHalf, false>(xa, t, n);
+        y.template load<kHalf, false>(ya, t, n);
+        const uint32_t ra = r.template load<kHalf, false>(t, n);
+        body(t, n, std::false_type(), xa, ya, ra);
+    }
+    return t;
+}
+
+template <typename T, int N, bool SOME, typename Off>
 __global__ void __launch_bounds__(64) scan_fwd(ScanGeom g, ScanPlan q, const T *__restrict__ gate,
                                                const T *__restrict__ value, const float *start,
                                                const uint8_t *__restrict__ reset, const int32_t *__restrict__ lengths,
@@ -120,36 +208,39 @@ __global__ void __launch_bounds__(64) scan_fwd(ScanGeom g, ScanPlan q, const T *
     float h[N] = {};
     if (start) get_f32<N>(start + w.end(g, w.c), h);
     const bool coupled = g.coupled;
-    for (int t = w.t0; t < w.t1; t += kBlock) {
-        const int n = min(kBlock, w.t1 - t), live = min(n, w.valid - t);
-        Steps<T, N> f, v;
-        f.load(gate + w.at(g.gate, t), g.gate.step, live);
-        v.load(value + w.at(g.value, t), g.value.step, live);
-        const uint32_t resets = reset ? load_resets(reset + w.b * g.reset.batch + t * g.reset.step, g.reset.step, live) : 0;
-        if (states) put_own<float, N>(states + (int64_t(w.b) * ((g.T - 1) / kBlock + 1) + t / kBlock) * g.D + w.d, h, w.skip);
-        T *o = out + w.at(g.out, t);
+    const Line<T, N, Off> o(out, g.out, w);
+    // what lies behind the end of a sequence is a state that stands still and zeros
+    int t = walk<T, N, SOME, Off>(
+        Line<const T, N, Off>(gate, g.gate, w), Line<const T, N, Off>(value, g.value, w), Resets<SOME>(reset, g, w.b), w.t0,
+        min(w.t1, w.valid), [&](int t, int n, auto full, const auto &f, const auto &v, uint32_t resets) {
+            constexpr bool FULL = decltype(full)::value;
+            if (states && t % kBlock == 0 && t < w.t1) put_own<float, N>(states + w.state(g, t), h, w.skip);
+            each_step<kHalf, SOME>(resets, [&](int u, bool cut) {
+                if (!FULL && t + u >= w.t1) return;
+                float y[N] = {};
+                if (FULL || u < n) {
 #pragma unroll
-        for (int u = 0; u < kBlock; ++u) {
-            if (u >= n) break;
-            float y[N] = {};
-            if (u < live) {
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    float a, i;
-                    gates(f.v[u].get(j), a, i);
-                    h[j] = advance(resets >> u & 1 ? 0.f : h[j], i, v.v[u].get(j), coupled);
-                    y[j] = h[j];
+                    for (int j = 0; j < N; ++j) {
+                        float a, i;
+                        gates(f[u].get(j), a, i);
+                        h[j] = advance(cut ? 0.f : h[j], i, v[u].get(j), coupled);
+                        y[j] = h[j];
+                    }
                 }
-            }
-            put_own<T, N>(o + u * g.out.step, y, w.skip);
-        }
+                put_own<T, N>(o.at(t + u), y, w.skip);
+            });
+        });
+    const float none[N] = {};
+    for (; t < w.t1; ++t) {
+        if (states && t % kBlock == 0) put_own<float, N>(states + w.state(g, t), h, w.skip);
+        put_own<T, N>(o.at(t), none, w.skip);
     }
     if (last && w.c == q.chunks - 1) put_own<float, N>(last + w.end(g), h, w.skip);
 }
 
 // A chunk as a step of its own: the product of its a (-1 where a reset cuts the state off), and its
 // state from zero.
-template <typename T, int N>
+template <typename T, int N, bool SOME, typename Off>
 __global__ void __launch_bounds__(64) scan_fold_fwd(ScanGeom g, ScanPlan q, const T *__restrict__ gate,
                                                     const T *__restrict__ value, const uint8_t *__restrict__ reset,
                                                     const int32_t *__restrict__ lengths, float *__restrict__ keep,
@@ -162,25 +253,22 @@ __global__ void __launch_bounds__(64) scan_fold_fwd(ScanGeom g, ScanPlan q, cons
 #pragma unroll
     for (int j = 0; j < N; ++j) p[j] = 1.f;
     const bool coupled = g.coupled;
-    for (int t = w.t0; t < min(w.t1, w.valid); t += kBlock) {
-        const int live = min(kBlock, min(w.t1, w.valid) - t);
-        Steps<T, N> f, v;
-        f.load(gate + w.at(g.gate, t), g.gate.step, live);
-        v.load(value + w.at(g.value, t), g.value.step, live);
-        const uint32_t resets = reset ? load_resets(reset + w.b * g.reset.batch + t * g.reset.step, g.reset.step, live) : 0;
-        cut |= resets != 0;
+    walk<T, N, SOME, Off>(Line<const T, N, Off>(gate, g.gate, w), Line<const T, N, Off>(value, g.value, w),
+                          Resets<SOME>(reset, g, w.b), w.t0, min(w.t1, w.valid),
+                          [&](int, int n, auto full, const auto &f, const auto &v, uint32_t resets) {
+                              constexpr bool FULL = decltype(full)::value;
+                              cut |= resets != 0;
+                              each_step<kHalf, SOME>(resets, [&](int u, bool zero) {
+                                  if (!FULL && u >= n) return;
 #pragma unroll
-        for (int u = 0; u < kBlock; ++u) {
-            if (u >= live) break;
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                float a, i;
-                gates(f.v[u].get(j), a, i);
-                h[j] = advance(resets >> u & 1 ? 0.f : h[j], i, v.v[u].get(j), coupled);
-                p[j] = fmaf(-i, p[j], p[j]);
-            }
-        }
-    }
+                                  for (int j = 0; j < N; ++j) {
+                                      float a, i;
+                                      gates(f[u].get(j), a, i);
+                                      h[j] = advance(zero ? 0.f : h[j], i, v[u].get(j), coupled);
+                                      p[j] = fmaf(-i, p[j], p[j]);
+                                  }
+                              });
+                          });
 #pragma unroll
     for (int j = 0; j < N; ++j) p[j] = cut ? -1.f : p[j];
     put_own<float, N>(keep + w.end(g, w.c), p, w.skip);
@@ -224,7 +312,10 @@ __global__ void __launch_bounds__(1024) scan_carry(int64_t ends, int chunks, con
 }
 
 // ---------------------------------------------------------------- backward --
-template <typename T, int N>
+// A block's states are worked out forward from the kept one, leaving two numbers a step: i, and what
+// dgate is of g.  The gates' and values' registers are then free for the next block's loads, which fly
+// while the block's gradient is walked back; dout's follow behind it.
+template <typename T, int N, bool SOME, typename Off>
 __global__ void __launch_bounds__(64) scan_bwd(ScanGeom g, ScanPlan q, const T *__restrict__ gate,
                                                const T *__restrict__ value, const float *__restrict__ states,
                                                const uint8_t *__restrict__ reset, const int32_t *__restrict__ lengths,
@@ -236,52 +327,85 @@ __global__ void __launch_bounds__(64) scan_bwd(ScanGeom g, ScanPlan q, const T *
     float back[N] = {};
     if (start) get_f32<N>(start + w.end(g, w.c), back);
     const bool coupled = g.coupled;
-    for (int t = (w.t1 - 1) / kBlock * kBlock; t >= w.t0 && w.t1 > w.t0; t -= kBlock) {
-        const int n = min(kBlock, w.t1 - t), live = min(n, w.valid - t);
-        T *df = dgate + w.at(g.dgate, t), *dv = dvalue + w.at(g.dvalue, t);
-        Steps<T, N> f, v, d;
-        f.load(gate + w.at(g.gate, t), g.gate.step, live);
-        v.load(value + w.at(g.value, t), g.value.step, live);
-        d.load(dout + w.at(g.out, t), g.out.step, live);
-        const uint32_t resets = reset ? load_resets(reset + w.b * g.reset.batch + t * g.reset.step, g.reset.step, live) : 0;
-        float h[N] = {}, share[kBlock][N], slope[kBlock][N];
-        if (live > 0) get_f32<N>(states + (int64_t(w.b) * ((g.T - 1) / kBlock + 1) + t / kBlock) * g.D + w.d, h);
-#pragma unroll
-        for (int u = 0; u < kBlock; ++u) {
+    const Line<const T, N, Off> fl(gate, g.gate, w), vl(value, g.value, w), dl(dout, g.out, w);
+    const Line<T, N, Off> dfl(dgate, g.dgate, w), dvl(dvalue, g.dvalue, w);
+    const Resets<SOME> rl(reset, g, w.b);
+    Vec<T, N> f[kBlock], v[kBlock], d[kBlock];
+    float h[N] = {};
+    uint32_t resets = 0;
+    float share[kBlock][N], slope[kBlock][N];
+    auto inputs = [&](auto full, int t, int live) {
+        constexpr bool FULL = decltype(full)::value;
+        fl.template load<kBlock, FULL>(f, t, live);
+        vl.template load<kBlock, FULL>(v, t, live);
+        if (FULL || live > 0) get_f32<N>(states + w.state(g, t), h);
+    };
+    auto gradients = [&](auto full, int t, int live) {
+        constexpr bool FULL = decltype(full)::value;
+        dl.template load<kBlock, FULL>(d, t, live);
+        resets = rl.template load<kBlock, FULL>(t, live);
+    };
+    auto forward = [&](auto full, int live) {
+        constexpr bool FULL = decltype(full)::value;
+        each_step<kBlock, SOME>(resets, [&](int u, bool cut) {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                share[u][j] = slope[u][j] = 0.f;
-                if (u < live) {
-                    float a, i;
-                    gates(f.v[u].get(j), a, i);
-                    const float before = resets >> u & 1 ? 0.f : h[j], x = v.v[u].get(j);
-                    share[u][j] = i;
-                    slope[u][j] = a * i * (coupled ? before - x : before);
-                    h[j] = advance(before, i, x, coupled);
-                }
+                if (!FULL) share[u][j] = slope[u][j] = 0.f;
+                if (!FULL && u >= live) continue;
+                float a, i;
+                gates(f[u].get(j), a, i);
+                const float before = cut ? 0.f : h[j], x = v[u].get(j);
+                share[u][j] = i;
+                slope[u][j] = a * i * (coupled ? before - x : before);
+                h[j] = advance(before, i, x, coupled);
             }
-        }
-#pragma unroll
-        for (int u = kBlock - 1; u >= 0; --u) {
-            if (u >= n) continue;
+        });
+    };
+    auto backward = [&](auto full, int t, int n, int live) {
+        constexpr bool FULL = decltype(full)::value;
+        each_step<kBlock, SOME>(SOME ? __brev(resets) >> (32 - kBlock) : 0, [&](int k, bool cut) {
+            const int u = kBlock - 1 - k;
+            if (!FULL && u >= n) return;
             float yf[N] = {}, yv[N] = {};
-            if (u < live) {
+            if (FULL || u < live) {
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    const float gr = back[j] + d.v[u].get(j);
+                    const float gr = back[j] + d[u].get(j);
                     yf[j] = slope[u][j] * gr;
                     yv[j] = coupled ? share[u][j] * gr : gr;
-                    back[j] = resets >> u & 1 ? 0.f : fmaf(-share[u][j], gr, gr);
+                    back[j] = cut ? 0.f : fmaf(-share[u][j], gr, gr);
                 }
             }
-            put_own<T, N>(df + u * g.dgate.step, yf, w.skip);
-            put_own<T, N>(dv + u * g.dvalue.step, yv, w.skip);
+            put_own<T, N>(dfl.at(t + u), yf, w.skip);
+            put_own<T, N>(dvl.at(t + u), yv, w.skip);
+        });
+    };
+    // blocks from the last one back: with checks until every step is valid in every thread of the wave
+    const int t1 = min(w.t1, w.valid);
+    int t = w.t0 + (w.t1 - w.t0 + kBlock - 1) / kBlock * kBlock - kBlock;
+    for (; t >= w.t0 && !__all(t + kBlock <= t1); t -= kBlock) {
+        const int n = min(kBlock, w.t1 - t), live = min(kBlock, t1 - t);
+        inputs(std::false_type(), t, live);
+        gradients(std::false_type(), t, live);
+        forward(std::false_type(), live);
+        backward(std::false_type(), t, n, live);
+    }
+    if (t >= w.t0) {
+        inputs(std::true_type(), t, 0);
+        gradients(std::true_type(), t, 0);
+        for (;; t -= kBlock) {
+            const bool more = t > w.t0;
+            forward(std::true_type(), 0);
+            if (more) inputs(std::true_type(), t - kBlock, 0);
+            backward(std::true_type(), t, 0, 0);
+            if (!more) break;
+            gradients(std::true_type(), t - kBlock, 0);
         }
     }
     if (dh0 && w.c == 0) put_own<float, N>(dh0 + w.end(g), back, w.skip);
 }
 
-template <typename T, int N>
+template <typename T, int N, bool SOME, typename Off>
 __global__ void __launch_bounds__(64) scan_fold_bwd(ScanGeom g, ScanPlan q, const T *__restrict__ gate,
                                                     const T *__restrict__ dout, const uint8_t *__restrict__ reset,
                                                     const int32_t *__restrict__ lengths, float *__restrict__ keep,
@@ -293,25 +417,54 @@ __global__ void __launch_bounds__(64) scan_fold_bwd(ScanGeom g, ScanPlan q, cons
     bool cut = false;
 #pragma unroll
     for (int j = 0; j < N; ++j) p[j] = 1.f;
+    const Line<const T, N, Off> fl(gate, g.gate, w), dl(dout, g.out, w);
+    const Resets<SOME> rl(reset, g, w.b);
+    Vec<T, N> fa[kHalf], da[kHalf], fb[kHalf], db[kHalf];
     const int t1 = min(w.t1, w.valid);
-    for (int t = (w.t1 - 1) / kBlock * kBlock; t >= w.t0 && w.t1 > w.t0; t -= kBlock) {
-        const int live = min(kBlock, t1 - t);
-        Steps<T, N> f, d;
-        f.load(gate + w.at(g.gate, t), g.gate.step, live);
-        d.load(dout + w.at(g.out, t), g.out.step, live);
-        const uint32_t resets = reset ? load_resets(reset + w.b * g.reset.batch + t * g.reset.step, g.reset.step, live) : 0;
+    auto body = [&](int n, auto full, const Vec<T, N>(&f)[kHalf], const Vec<T, N>(&d)[kHalf], uint32_t resets) {
+        constexpr bool FULL = decltype(full)::value;
         cut |= resets != 0;
-#pragma unroll
-        for (int u = kBlock - 1; u >= 0; --u) {
-            if (u >= live) continue;
+        each_step<kHalf, SOME>(SOME ? __brev(resets) >> (32 - kHalf) : 0, [&](int k, bool zero) {
+            const int u = kHalf - 1 - k;
+            if (!FULL && u >= n) return;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 float a, i;
-                gates(f.v[u].get(j), a, i);
-                const float gr = back[j] + d.v[u].get(j);
-                back[j] = resets >> u & 1 ? 0.f : fmaf(-i, gr, gr);
+                gates(f[u].get(j), a, i);
+                const float gr = back[j] + d[u].get(j);
+                back[j] = zero ? 0.f : fmaf(-i, gr, gr);
                 p[j] = fmaf(-i, p[j], p[j]);
             }
+        });
+    };
+    // halves from the last one back; t is the first step of the half behind the next
+    int t = w.t0 + (w.t1 - w.t0 + kHalf - 1) / kHalf * kHalf;
+    while (t > w.t0 && !__all(t <= t1 && t - w.t0 >= kBlock)) {
+        t -= kHalf;
+        const int n = min(kHalf, t1 - t);
+        fl.template load<kHalf, false>(fa, t, n);
+        dl.template load<kHalf, false>(da, t, n);
+        body(n, std::false_type(), fa, da, rl.template load<kHalf, false>(t, n));
+    }
+    if (t > w.t0) {
+        // whole halves only; an odd one first, so that pairs are left
+        auto fetch = [&](Vec<T, N>(&f)[kHalf], Vec<T, N>(&d)[kHalf], int at) {
+            fl.template load<kHalf, true>(f, at, 0);
+            dl.template load<kHalf, true>(d, at, 0);
+            return rl.template load<kHalf, true>(at, 0);
+        };
+        if ((t - w.t0) / kHalf % 2) {
+            t -= kHalf;
+            const uint32_t r = fetch(fa, da, t);
+            body(kHalf, std::true_type(), fa, da, r);
+        }
+        uint32_t ra = fetch(fa, da, t - kHalf);
+        while (t > w.t0) {
+            const uint32_t rb = fetch(fb, db, t - kBlock);
+            body(kHalf, std::true_type(), fa, da, ra);
+            t -= kBlock;
+            if (t > w.t0) ra = fetch(fa, da, t - kHalf);
+            body(kHalf, std::true_type(), fb, db, rb);
         }
     }
 #pragma unroll
@@ -329,10 +482,23 @@ hipError_t carry(const ScanGeom &g, const ScanPlan &q, const float *first, float
     return hipGetLastError();
 }
 
-template <typename F>
-hipError_t with_channels(int n, F f)
+// Calls f(N, SOME, Off) with the plan's channels a thread, whether there are resets, and the type of a
+// lane's offset.
+template <bool TWO, typename F>
+hipError_t with_lanes(const ScanPlan &q, bool some, F f)
 {
-    return n == 2 ? f(std::integral_constant<int, 2>()) : f(std::integral_constant<int, 1>());
+    auto with_off = [&](auto n, auto r) { return q.far ? f(n, r, int64_t()) : f(n, r, uint32_t()); };
+    auto with_resets = [&](auto n) { return some ? with_off(n, std::true_type()) : with_off(n, std::false_type()); };
+    if constexpr (TWO)
+        if (q.N == 2) return with_resets(std::integral_constant<int, 2>());
+    return with_resets(std::integral_constant<int, 1>());
+}
+
+// The sequences of a wave lie within 4 GiB of each other, in bytes of the storage type.
+bool near(const gc_strides &s, const ScanGeom &g, const ScanPlan &q, int size)
+{
+    const int64_t others = std::min<int64_t>(g.B - 1, 63 / q.nv + 1);
+    return (__int128)others * s.batch + g.D < (int64_t(1) << 32) / size;
 }
 
 }  // namespace
@@ -354,6 +520,9 @@ bool plan_scan(const ScanGeom &g, int dtype, bool bwd, ScanPlan &q)
     q.part_bytes = q.chunks > 1 ? (size_t(q.chunks) * g.B * g.D * 4 + 255) & ~size_t(255) : 0;
     q.ws_bytes = 2 * q.part_bytes;
     q.fd_nv = make_fastdiv(uint32_t(q.nv));
+    const int size = dtype == GC_F32 ? 4 : 2;
+    q.far = !near(g.gate, g, q, size) || !near(g.value, g, q, size) || !near(g.out, g, q, size);
+    if (bwd) q.far |= !near(g.dgate, g, q, size) || !near(g.dvalue, g, q, size);
     return launchable(waves * q.chunks, 64);
 }
 
@@ -366,14 +535,16 @@ hipError_t launch_scan_fwd(const ScanGeom &g, const ScanPlan &q, const void *gat
     const T *f = static_cast<const T *>(gate), *v = static_cast<const T *>(value);
     float *keep = static_cast<float *>(ws), *add = keep + q.part_bytes / 4;
     const dim3 grid(unsigned((q.lanes + 63) / 64), unsigned(q.chunks));
-    return with_channels(q.N, [&](auto nn) {
+    return with_lanes<sizeof(T) == 2>(q, reset, [&](auto nn, auto some, auto off) {
         constexpr int N = decltype(nn)::value;
+        constexpr bool SOME = decltype(some)::value;
+        using Off = decltype(off);
         if (q.chunks > 1) {
-            hipLaunchKernelGGL((scan_fold_fwd<T, N>), grid, dim3(64), 0, s, g, q, f, v, reset, lengths, keep, add);
+            hipLaunchKernelGGL((scan_fold_fwd<T, N, SOME, Off>), grid, dim3(64), 0, s, g, q, f, v, reset, lengths, keep, add);
             if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
             if (const hipError_t e = carry<false>(g, q, h0, keep, add, s); e != hipSuccess) return e;
         }
-        hipLaunchKernelGGL((scan_fwd<T, N>), grid, dim3(64), 0, s, g, q, f, v, q.chunks > 1 ? keep : h0, reset, lengths,
+        hipLaunchKernelGGL((scan_fwd<T, N, SOME, Off>), grid, dim3(64), 0, s, g, q, f, v, q.chunks > 1 ? keep : h0, reset, lengths,
                            static_cast<T *>(out), last, states);
         return hipGetLastError();
     });
@@ -388,14 +559,16 @@ hipError_t launch_scan_bwd(const ScanGeom &g, const ScanPlan &q, const void *gat
     const T *f = static_cast<const T *>(gate), *v = static_cast<const T *>(value), *d = static_cast<const T *>(dout);
     float *keep = static_cast<float *>(ws), *add = keep + q.part_bytes / 4;
     const dim3 grid(unsigned((q.lanes + 63) / 64), unsigned(q.chunks));
-    return with_channels(q.N, [&](auto nn) {
+    return with_lanes<sizeof(T) == 2>(q, reset, [&](auto nn, auto some, auto off) {
         constexpr int N = decltype(nn)::value;
+        constexpr bool SOME = decltype(some)::value;
+        using Off = decltype(off);
         if (q.chunks > 1) {
-            hipLaunchKernelGGL((scan_fold_bwd<T, N>), grid, dim3(64), 0, s, g, q, f, d, reset, lengths, keep, add);
+            hipLaunchKernelGGL((scan_fold_bwd<T, N, SOME, Off>), grid, dim3(64), 0, s, g, q, f, d, reset, lengths, keep, add);
             if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
             if (const hipError_t e = carry<true>(g, q, dlast, keep, add, s); e != hipSuccess) return e;
         }
-        hipLaunchKernelGGL((scan_bwd<T, N>), grid, dim3(64), 0, s, g, q, f, v, states, reset, lengths, d,
+        hipLaunchKernelGGL((scan_bwd<T, N, SOME, Off>), grid, dim3(64), 0, s, g, q, f, v, states, reset, lengths, d,
                            q.chunks > 1 ? keep : dlast, static_cast<T *>(dgate), static_cast<T *>(dvalue), dh0);
         return hipGetLastError();
     });
