@@ -51,10 +51,11 @@ struct ScanPlan {
     int N;              // channels of a thread
     int nv;             // threads of a step's channels
     int64_t lanes;      // B * nv
+    int past;           // the outputs go past the cache
     int far;            // lanes of a wave may be 4 GiB apart and more
     int chunks, len;    // pieces the steps are cut into, and their length (a multiple of the block)
     size_t part_bytes, ws_bytes;
-    FastDiv fd_nv;
+    FastDiv fd_nv, fd_blocks;
 };
 bool plan_scan(const ScanGeom &g, int dtype, bool bwd, ScanPlan &q);
 template <typename T>

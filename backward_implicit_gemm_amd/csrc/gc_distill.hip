@@ -11,6 +11,7 @@
 // gradient is written as if there were no entries, then the entries' places are written again
 // with all that belongs to them, by the first entry of each place.
 #include <algorithm>
+#include <iterator>
 #include <math.h>
 #include <type_traits>
 
@@ -33,20 +34,6 @@ __device__ __forceinline__ V lanes_fold(V v, int width, F f)
 {
     for (int m = width >> 1; m > 0; m >>= 1) v = f(v, __shfl_xor(v, m, 64));
     return v;
-}
-
-// Folds a value of each of the team's L threads; a team of more than 64 is the workgroup.
-template <typename F>
-__device__ __forceinline__ float team_fold(float v, int L, float *red, F f)
-{
-    v = lanes_fold(v, L < 64 ? L : 64, f);
-    if (L <= 64) return v;
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float s = red[0];
-    for (int i = 1; i < L >> 6; ++i) s = f(s, red[i]);
-    return s;
 }
 
 template <int N>
@@ -74,6 +61,15 @@ __device__ __forceinline__ void put_own(T *p, const Vec<T, N> &v, int skip)
     }
 }
 
+// Makes the compiler work out anew what depends on this number: the places of a row's vectors would
+// take more registers than the vectors do.
+__device__ __forceinline__ int64_t anew(int64_t i)
+{
+    int v = int(i);
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // exp((z - peak) / t), NaN where both are infinite alike
 __device__ __forceinline__ float share(float z, float peak, float c) { return __builtin_amdgcn_exp2f((z - peak) * c); }
 
@@ -85,7 +81,7 @@ __global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, const T *l
                                                 float *__restrict__ mass, const float *__restrict__ dloss,
                                                 float *__restrict__ loss, T *dlogits)
 {
-    __shared__ float red[16];
+    __shared__ float red[2][16];
     extern __shared__ Entry all[];
     const int tt = threadIdx.x & (L - 1), team = threadIdx.x / L, teams = blockDim.x / L;
     const int64_t row = int64_t(blockIdx.x) * teams + team;
@@ -96,14 +92,25 @@ __global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, const T *l
     const int nv = vectors(g.V, N);
     const auto most = [](float a, float b) { return fmaxf(a, b); };
     const auto plus = [](float a, float b) { return a + b; };
+    constexpr int U = NV ? NV : 4;      // vectors whose loads fly together
+    // the step keeps the exponentials of short rows instead of working them out again
+    constexpr bool KEEP = OP == GC_OP_STEP && NV > 0 && NV * N <= 48;
 
-    Vec<T, N> held[NV ? NV : 1];
-    if (OP == GC_OP_STEP) {
+    Vec<T, N> held[U];
+    float shares[KEEP ? U : 1][N];
+    auto fetch = [&](int64_t i) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) held[i] = load_vec<T, N>(z + Place<N>(int64_t(i) * L + tt, g.V).at);
+        for (int u = 0; u < U; ++u) held[u] = load_vec<T, N>(z + Place<N>(i + int64_t(u) * L, g.V).at);
+    };
+    fetch(tt);
+    float m = 0.f, s = 0.f, scale = 0.f;
+    if (OP == GC_OP_BWD) {
+        m = peak[row];
+        s = mass[row];
     }
+    if (OP != GC_OP_FWD) scale = dloss[row];
 
-    // the teacher's shares, by every wave for itself
+    // the teacher's shares, by every wave for itself; a lane's first entry stays in registers
     const int width = L < 64 ? L : 64, lane = tt & (width - 1);
     auto entry_at = [&](int k, int &at, float &v) {
         const int64_t i = g.i64 ? static_cast<const int64_t *>(index)[row * g.ld_index + k]
@@ -113,130 +120,133 @@ __global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, const T *l
                   : to_f32(static_cast<const bf16_t *>(teacher)[row * g.ld_teacher + k]);
         if (at < 0) v = -INFINITY;
     };
-    float top = -INFINITY, total = 0.f;
-    for (int k = lane; k < g.K; k += width) {
-        int at;
-        float v;
-        entry_at(k, at, v);
-        top = fmaxf(top, v != v ? INFINITY : v);
-    }
+    int at0 = -1;
+    float v0 = -INFINITY, top = -INFINITY, total = 0.f;
+    if (lane < g.K) entry_at(lane, at0, v0);
+    auto each_entry = [&](auto f) {
+        if (lane < g.K) f(lane, at0, v0);
+        for (int k = lane + width; k < g.K; k += width) {
+            int at;
+            float v;
+            entry_at(k, at, v);
+            f(k, at, v);
+        }
+    };
+    each_entry([&](int, int, float v) { top = fmaxf(top, v != v ? INFINITY : v); });
     top = lanes_fold(top, width, most);
     const bool some = top > -INFINITY;
-    for (int k = lane; k < g.K; k += width) {
-        int at;
-        float v;
-        entry_at(k, at, v);
-        total += v == -INFINITY ? 0.f : share(v, top, c);
-    }
+    each_entry([&](int, int, float v) { total += v == -INFINITY ? 0.f : share(v, top, c); });
     total = lanes_fold(total, width, plus);
     const float inv_total = 1.f / total;
-    for (int k = tt; k < g.K; k += L) {
-        Entry e;
-        float v;
-        entry_at(k, e.at, v);
-        e.p = v == -INFINITY ? 0.f : share(v, top, c) * inv_total;
-        e.z = e.at >= 0 ? to_f32(z[e.at]) : 0.f;
-        entry[k] = e;
-    }
+    if (tt < width)
+        each_entry([&](int k, int at, float v) {
+            entry[k] = Entry{at, v == -INFINITY ? 0.f : share(v, top, c) * inv_total, at >= 0 ? to_f32(z[at]) : 0.f};
+        });
 
-    // the student's largest logit, and the sum of the exponentials
-    float m, s;
-    if (OP == GC_OP_BWD) {
-        m = peak[row];
-        s = mass[row];
-    } else if (NV) {
-        m = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const Place<N> at(int64_t(i) * L + tt, g.V);
-#pragma unroll
-            for (int j = 0; j < N; ++j) m = fmaxf(m, j >= at.skip ? held[i].get(j) : -INFINITY);
-        }
-        m = team_fold(m, L, red, most);
-        const float base = m == -INFINITY ? 0.f : m;
-        s = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const Place<N> at(int64_t(i) * L + tt, g.V);
-#pragma unroll
-            for (int j = 0; j < N; ++j) s += j >= at.skip ? share(held[i].get(j), base, c) : 0.f;
-        }
-        s = team_fold(s, L, red, plus);
-    } else {
-        // running maximum and sum
-        constexpr int U = 4;
-        float mine = -INFINITY;
-        s = 0.f;
-        for (int64_t i = tt; i < nv; i += int64_t(U) * L) {
-            Vec<T, N> v[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = load_vec<T, N>(z + Place<N>(i + int64_t(u) * L, g.V).at);
+    // The student's largest logit and the sum of the exponentials: each thread around its own largest,
+    // so that one exchange joins both.
+    float mine = -INFINITY, base = 0.f;
+    if (OP != GC_OP_BWD) {
+        auto add = [&](int64_t i) {
+            i = anew(i);
             float high = mine;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const Place<N> at(i + int64_t(u) * L, g.V);
 #pragma unroll
-                for (int j = 0; j < N; ++j) high = fmaxf(high, j >= at.skip ? v[u].get(j) : -INFINITY);
+                for (int j = 0; j < N; ++j) high = fmaxf(high, j >= at.skip ? held[u].get(j) : -INFINITY);
             }
-            const float base = high == -INFINITY ? 0.f : high;   // nothing yet but masked logits
-            s *= share(mine, base, c);
+            keep_packed(held);
+            i = anew(i);
+            base = high == -INFINITY ? 0.f : high;   // nothing yet but masked logits
+            if (!NV) s *= share(mine, base, c);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const Place<N> at(i + int64_t(u) * L, g.V);
 #pragma unroll
-                for (int j = 0; j < N; ++j) s += j >= at.skip ? share(v[u].get(j), base, c) : 0.f;
+                for (int j = 0; j < N; ++j) {
+                    const float e = j >= at.skip ? share(held[u].get(j), base, c) : 0.f;
+                    if (KEEP) shares[u][j] = e;
+                    s += e;
+                }
             }
             mine = high;
+        };
+        if (NV) add(tt);
+        else
+            for (int64_t i = tt; i < nv; i += int64_t(U) * L) {
+                if (i != tt) fetch(i);
+                add(i);
+            }
+        // joins two pairs; a thread without a logit above -inf has s == 0
+        m = mine;
+        auto join = [&](float m2, float s2) {
+            const float high = fmaxf(m, m2);
+            s = (m == high ? s : s * share(m, high, c)) + (m2 == high ? s2 : s2 * share(m2, high, c));
+            m = high;
+        };
+        for (int w = width >> 1; w > 0; w >>= 1) {
+            const float m2 = __shfl_xor(m, w, 64), s2 = __shfl_xor(s, w, 64);
+            join(m2, s2);
         }
-        m = team_fold(mine, L, red, most);
-        // a thread without a logit above -inf has s == 0; with none at all the sum is 0
-        s = team_fold(mine == -INFINITY ? s : s * share(mine, m, c), L, red, plus);
+        if (L > 64) {
+            if ((threadIdx.x & 63) == 0) {
+                red[0][threadIdx.x >> 6] = m;
+                red[1][threadIdx.x >> 6] = s;
+            }
+            __syncthreads();
+            m = red[0][0];
+            s = red[1][0];
+            for (int w = 1; w < L >> 6; ++w) join(red[0][w], red[1][w]);
+        }
     }
     if (OP == GC_OP_FWD && tt == 0) {
         if (peak) peak[row] = m;
         if (mass) mass[row] = s;
     }
-    team_sync(L <= 64);     // the entries are in LDS
     if (OP != GC_OP_BWD && tt < width) {
         // log q = (z - peak)/t - log(mass), log p = (teacher - top)/t - log(total)
         const float log_s = logf(s), log_total = logf(total);
         float sum = 0.f;
-        for (int k = lane; k < g.K; k += width) {
-            const Entry e = entry[k];
-            int at;
-            float v;
-            entry_at(k, at, v);
+        each_entry([&](int k, int, float v) {
+            const Entry e = entry[k];      // this thread's own
             if (some && e.p != 0.f)
                 sum += e.z == -INFINITY ? INFINITY : e.p * (((v - top) - (e.z - m)) / t - log_total + log_s);
-        }
+        });
         sum = lanes_fold(sum, width, plus);
         if (tt == 0) loss[row] = t * t * sum;
     }
     if (OP == GC_OP_FWD) return;
 
-    const float by = some ? dloss[row] * t : 0.f, inv = by / s;
+    // the entries' logits have been read, should the gradient take their place
+    if (OP == GC_OP_BWD && dlogits == logits) team_sync(L <= 64);
+    const float by = some ? scale * t : 0.f, inv = by / s;
+    const float own = mine == -INFINITY ? 0.f : share(base, m, c) * inv;     // of this thread's exponentials
     T *out = dlogits + row * g.ld_grad;
-    auto write = [&](const Vec<T, N> &v, int64_t i) {
-        const Place<N> at(i, g.V);
-        if (!at.live) return;
-        float y[N];
+    auto write = [&](int64_t i) {
+        if (!KEEP) keep_packed(held);
+        i = anew(i);
 #pragma unroll
-        for (int j = 0; j < N; ++j) y[j] = some ? share(v.get(j), m, c) * inv : 0.f;
-        Vec<T, N> o;
-        o.put(y);
-        put_own<PAST, T, N>(out + at.at, o, at.skip);
+        for (int u = 0; u < U; ++u) {
+            const Place<N> at(i + int64_t(u) * L, g.V);
+            if (!at.live) continue;
+            float y[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                y[j] = KEEP ? shares[u][j] * own : share(held[u].get(j), m, c) * inv;
+                if (!some) y[j] = 0.f;
+            }
+            Vec<T, N> o;
+            o.put(y);
+            put_own<PAST, T, N>(out + at.at, o, at.skip);
+        }
     };
     if (NV) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) write(held[i], int64_t(i) * L + tt);
+        write(tt);
     } else {
-        constexpr int U = 4;
         for (int64_t i = tt; i < nv; i += int64_t(U) * L) {
-            Vec<T, N> v[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = load_vec<T, N>(z + Place<N>(i + int64_t(u) * L, g.V).at);
-#pragma unroll
-            for (int u = 0; u < U; ++u) write(v[u], i + int64_t(u) * L);
+            if (OP == GC_OP_STEP || i != tt) fetch(i);
+            write(i);
         }
     }
     if (!some) return;
@@ -273,6 +283,7 @@ hipError_t with_held(int nv, F f)
     case 10: return f(std::integral_constant<int, 10>());
     case 12: return f(std::integral_constant<int, 12>());
     case 16: return f(std::integral_constant<int, 16>());
+    case 20: return f(std::integral_constant<int, 20>());
     default: return hipErrorInvalidValue;
     }
 }
@@ -285,19 +296,22 @@ void plan_distill(const DistillGeom &g, int dtype, int op, DistillPlan &q)
     const int vec = dtype == GC_F32 ? 4 : 8;
     q.N = g.V < vec ? 1 : vec;
     const int64_t nv = vectors(g.V, q.N);
+    // two vectors a thread within a wave, then as many as keep two workgroups on a CU
+    const int many = dtype == GC_F32 ? 8 : 5;
     q.L = 8;
     while (q.L < 64 && q.L * 2 < nv) q.L *= 2;
-    while (q.L < 1024 && q.L * 4 < nv) q.L *= 2;
+    while (q.L < 1024 && int64_t(q.L) * many < nv) q.L *= 2;
     q.threads = std::max(256, q.L);
-    while (q.L <= 64 && size_t(q.threads / q.L) * g.K * 12 > 49152) {
+    while (q.L <= 64 && size_t(q.threads / q.L) * g.K * sizeof(float) * 3 > 49152) {
         if (q.threads > 64) q.threads /= 2;
         else q.L *= 2;
     }
     if (q.L > 64) q.threads = q.L;
-    if (op == GC_OP_STEP) {
-        q.NV = int(std::min<int64_t>(17, (nv + q.L - 1) / q.L));
-        if (q.NV == 7 || q.NV == 9 || q.NV == 11) ++q.NV;
-        if (q.NV > 12) q.NV = q.NV <= 16 ? 16 : 0;
+    if (op != GC_OP_FWD) {
+        q.NV = int(std::min<int64_t>(21, (nv + q.L - 1) / q.L));
+        const int sizes[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20};
+        const int *next = std::lower_bound(std::begin(sizes), std::end(sizes), q.NV);
+        q.NV = next == std::end(sizes) ? 0 : *next;
     }
     const int teams = q.threads / q.L;
     q.grid = (g.rows + teams - 1) / teams;
@@ -324,12 +338,16 @@ hipError_t launch_distill(const DistillGeom &g, const DistillPlan &q, int op, co
     auto with_op = [&](auto n) {
         constexpr bool WIDE = decltype(n)::value > 1;
         if (op == GC_OP_FWD) return go(n, None(), Fwd(), std::false_type());
-        if (op == GC_OP_BWD) return with_past<WIDE>(q.past, [&](auto past) { return go(n, None(), Bwd(), past); });
-        if constexpr (!WIDE) return go(n, std::integral_constant<int, 1>(), Step(), std::false_type());
-        else
+        if constexpr (!WIDE) {
+            const std::integral_constant<int, 1> one;
+            return op == GC_OP_BWD ? go(n, one, Bwd(), std::false_type()) : go(n, one, Step(), std::false_type());
+        } else {
             return with_held(q.NV, [&](auto nv) {
-                return with_past<WIDE>(q.past, [&](auto past) { return go(n, nv, Step(), past); });
+                return with_past<true>(q.past, [&](auto past) {
+                    return op == GC_OP_BWD ? go(n, nv, Bwd(), past) : go(n, nv, Step(), past);
+                });
             });
+        }
     };
     if (q.N == 1) return with_op(std::integral_constant<int, 1>());
     return with_op(std::integral_constant<int, kVec<T>>());

@@ -18,6 +18,7 @@
 #include <type_traits>
 
 #include "gc_core.h"
+#include "gc_norm_res.h"
 
 namespace gc {
 namespace {
@@ -33,7 +34,9 @@ struct Lane {
     int b, b0, d, skip, c, t0, t1, valid;
     __device__ __forceinline__ bool find(const ScanGeom &g, const ScanPlan &q, const int32_t *lengths)
     {
-        const int64_t lane = int64_t(blockIdx.x) * 64 + threadIdx.x;
+        uint32_t chunk, block;
+        fdivmod(die_order(blockIdx.x, gridDim.x), q.fd_blocks, chunk, block);
+        const int64_t lane = int64_t(block) * 64 + threadIdx.x;
         if (lane >= q.lanes) return false;
         uint32_t bb, v;
         fdivmod(uint32_t(lane), q.fd_nv, bb, v);
@@ -41,7 +44,7 @@ struct Lane {
         b0 = __builtin_amdgcn_readfirstlane(b);
         d = min(int(v) * N, g.D - N);
         skip = int(v) * N - d;
-        c = blockIdx.y;
+        c = int(chunk);
         t0 = min(c * q.len, g.T);
         t1 = min(g.T - t0, q.len) + t0;
         valid = lengths ? min(max(lengths[b], 0), g.T) : g.T;
@@ -56,13 +59,25 @@ struct Lane {
     }
 };
 
-template <typename T, int N>
+// A vector of at most 4 bytes as a word.
+struct Words {
+    uint32_t w;
+};
+
+// Stores the channels that are this thread's own; PAST: past the cache.
+template <typename T, int N, bool PAST = false>
 __device__ __forceinline__ void put_own(T *p, const float (&v)[N], int skip)
 {
     if (N == 1 || skip == 0) {
         Vec<T, N> w;
         w.put(v);
-        store_vec<T, N>(p, w);
+        if constexpr (PAST) {
+            typedef std::conditional_t<sizeof(T) * N == 4, uint32_t, uint16_t> bits;
+            typedef bits loose __attribute__((aligned(sizeof(T))));
+            __builtin_nontemporal_store(bits(__builtin_bit_cast(Words, w).w), reinterpret_cast<loose *>(p));
+        } else {
+            store_vec<T, N>(p, w);
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < N; ++j)
@@ -82,25 +97,26 @@ __device__ __forceinline__ void get_f32(const float *p, float (&v)[N])
 // (Off: 32 bits where a wave's sequences lie within 4 GiB of each other).
 template <typename T, int N, typename Off>
 struct Line {
-    T *base;
-    int64_t step;
+    typedef std::conditional_t<std::is_const_v<T>, const char, char> byte;
+    byte *base;
+    int64_t step;  // bytes
     Off off;       // bytes
     __device__ __forceinline__ Line(T *p, const gc_strides &s, const Lane<N> &w)
-        : base(p + int64_t(w.b0) * s.batch), step(s.step), off(Off((int64_t(w.b - w.b0) * s.batch + w.d) * int64_t(sizeof(T))))
+        : base(reinterpret_cast<byte *>(p + int64_t(w.b0) * s.batch)), step(s.step * int64_t(sizeof(T))),
+          off(Off((int64_t(w.b - w.b0) * s.batch + w.d) * int64_t(sizeof(T))))
     {
     }
-    __device__ __forceinline__ T *at(int t) const
-    {
-        typedef std::conditional_t<std::is_const_v<T>, const char, char> byte;
-        return reinterpret_cast<T *>(reinterpret_cast<byte *>(base + int64_t(t) * step) + off);
-    }
+    // the scalar part of step t's address, which a walk moves on by `step`; and the lane's address
+    __device__ __forceinline__ byte *row(int t) const { return base + int64_t(t) * step; }
+    __device__ __forceinline__ T *lane(byte *row) const { return reinterpret_cast<T *>(row + off); }
     // `COUNT` steps from t; those from n on are not read
     template <int COUNT, bool FULL>
     __device__ __forceinline__ void load(Vec<std::remove_const_t<T>, N> (&v)[COUNT], int t, int n) const
     {
+        byte *p = row(t);
 #pragma unroll
-        for (int u = 0; u < COUNT; ++u)
-            if (FULL || u < n) v[u] = load_vec<std::remove_const_t<T>, N>(at(t + u));
+        for (int u = 0; u < COUNT; ++u, p += step)
+            if (FULL || u < n) v[u] = load_vec<std::remove_const_t<T>, N>(lane(p));
     }
 };
 
@@ -118,10 +134,11 @@ struct Resets {
     {
         if (!SOME) return 0;
         uint8_t v[COUNT];
+        const uint8_t *at = p + int64_t(t) * step;
 #pragma unroll
-        for (int u = 0; u < COUNT; ++u) {
+        for (int u = 0; u < COUNT; ++u, at += step) {
             v[u] = 0;
-            if (FULL || u < n) v[u] = p[(int64_t(t) + u) * step];
+            if (FULL || u < n) v[u] = *at;
         }
         uint32_t bits = 0;
 #pragma unroll
@@ -140,9 +157,10 @@ __device__ __forceinline__ void gates(float f, float &a, float &i)
 }
 
 // One step of the state; i is 1 - a.
-__device__ __forceinline__ float advance(float before, float i, float v, bool coupled)
+template <bool COUPLED>
+__device__ __forceinline__ float advance(float before, float i, float v)
 {
-    return coupled ? fmaf(i, v - before, before) : fmaf(-i, before, before) + v;
+    return COUPLED ? fmaf(i, v - before, before) : fmaf(-i, before, before) + v;
 }
 
 // ----------------------------------------------------------------- forward --
@@ -197,7 +215,7 @@ __device__ __forceinline__ int walk(const Line<const T, N, Off> &x, const Line<c
     return t;
 }
 
-template <typename T, int N, bool SOME, typename Off>
+template <typename T, int N, bool COUPLED, bool SOME, bool PAST, typename Off>
 __global__ void __launch_bounds__(64) scan_fwd(ScanGeom g, ScanPlan q, const T *__restrict__ gate,
                                                const T *__restrict__ value, const float *start,
                                                const uint8_t *__restrict__ reset, const int32_t *__restrict__ lengths,
@@ -207,7 +225,6 @@ __global__ void __launch_bounds__(64) scan_fwd(ScanGeom g, ScanPlan q, const T *
     if (!w.find(g, q, lengths)) return;
     float h[N] = {};
     if (start) get_f32<N>(start + w.end(g, w.c), h);
-    const bool coupled = g.coupled;
     const Line<T, N, Off> o(out, g.out, w);
     // what lies behind the end of a sequence is a state that stands still and zeros
     int t = walk<T, N, SOME, Off>(
@@ -215,6 +232,7 @@ __global__ void __launch_bounds__(64) scan_fwd(ScanGeom g, ScanPlan q, const T *
         min(w.t1, w.valid), [&](int t, int n, auto full, const auto &f, const auto &v, uint32_t resets) {
             constexpr bool FULL = decltype(full)::value;
             if (states && t % kBlock == 0 && t < w.t1) put_own<float, N>(states + w.state(g, t), h, w.skip);
+            char *to = o.row(t);
             each_step<kHalf, SOME>(resets, [&](int u, bool cut) {
                 if (!FULL && t + u >= w.t1) return;
                 float y[N] = {};
@@ -223,24 +241,25 @@ __global__ void __launch_bounds__(64) scan_fwd(ScanGeom g, ScanPlan q, const T *
                     for (int j = 0; j < N; ++j) {
                         float a, i;
                         gates(f[u].get(j), a, i);
-                        h[j] = advance(cut ? 0.f : h[j], i, v[u].get(j), coupled);
+                        h[j] = advance<COUPLED>(cut ? 0.f : h[j], i, v[u].get(j));
                         y[j] = h[j];
                     }
                 }
-                put_own<T, N>(o.at(t + u), y, w.skip);
+                put_own<T, N, PAST>(o.lane(to), y, w.skip);
+                to += o.step;
             });
         });
     const float none[N] = {};
     for (; t < w.t1; ++t) {
         if (states && t % kBlock == 0) put_own<float, N>(states + w.state(g, t), h, w.skip);
-        put_own<T, N>(o.at(t), none, w.skip);
+        put_own<T, N, PAST>(o.lane(o.row(t)), none, w.skip);
     }
     if (last && w.c == q.chunks - 1) put_own<float, N>(last + w.end(g), h, w.skip);
 }
 
 // A chunk as a step of its own: the product of its a (-1 where a reset cuts the state off), and its
 // state from zero.
-template <typename T, int N, bool SOME, typename Off>
+template <typename T, int N, bool COUPLED, bool SOME, typename Off>
 __global__ void __launch_bounds__(64) scan_fold_fwd(ScanGeom g, ScanPlan q, const T *__restrict__ gate,
                                                     const T *__restrict__ value, const uint8_t *__restrict__ reset,
                                                     const int32_t *__restrict__ lengths, float *__restrict__ keep,
@@ -252,7 +271,6 @@ __global__ void __launch_bounds__(64) scan_fold_fwd(ScanGeom g, ScanPlan q, cons
     bool cut = false;
 #pragma unroll
     for (int j = 0; j < N; ++j) p[j] = 1.f;
-    const bool coupled = g.coupled;
     walk<T, N, SOME, Off>(Line<const T, N, Off>(gate, g.gate, w), Line<const T, N, Off>(value, g.value, w),
                           Resets<SOME>(reset, g, w.b), w.t0, min(w.t1, w.valid),
                           [&](int, int n, auto full, const auto &f, const auto &v, uint32_t resets) {
@@ -264,7 +282,7 @@ __global__ void __launch_bounds__(64) scan_fold_fwd(ScanGeom g, ScanPlan q, cons
                                   for (int j = 0; j < N; ++j) {
                                       float a, i;
                                       gates(f[u].get(j), a, i);
-                                      h[j] = advance(zero ? 0.f : h[j], i, v[u].get(j), coupled);
+                                      h[j] = advance<COUPLED>(zero ? 0.f : h[j], i, v[u].get(j));
                                       p[j] = fmaf(-i, p[j], p[j]);
                                   }
                               });
@@ -291,12 +309,26 @@ __global__ void __launch_bounds__(1024) scan_carry(int64_t ends, int chunks, con
     auto place = [&](int c) { return int64_t(BACK ? chunks - 1 - c : c) * ends + e; };
     float p = 1.f, h = 0.f;
     bool cut = false;
+    constexpr int U = 16;     // chunks whose loads fly together
+    float k[U], a[U];
+    auto fetch = [&](int c) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c + u < c1) {
+                k[u] = keep[place(c + u)];
+                a[u] = add[place(c + u)];
+            }
+    };
     if (live)
-        for (int c = c0; c < c1; ++c) {
-            const float k = keep[place(c)], a = add[place(c)];
-            h = carry_over(k, a, h);
-            cut |= k < 0.f;
-            p *= k;
+        for (int c = c0; c < c1; c += U) {
+            fetch(c);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (c + u >= c1) break;
+                h = carry_over(k[u], a[u], h);
+                cut |= k[u] < 0.f;
+                p *= k[u];
+            }
         }
     part[0][wave][lane] = cut ? -1.f : p;
     part[1][wave][lane] = h;
@@ -304,10 +336,14 @@ __global__ void __launch_bounds__(1024) scan_carry(int64_t ends, int chunks, con
     if (!live) return;
     h = first ? first[e] : 0.f;
     for (int w = 0; w < wave; ++w) h = carry_over(part[0][w][lane], part[1][w][lane], h);
-    for (int c = c0; c < c1; ++c) {
-        const float k = keep[place(c)], a = add[place(c)];
-        keep[place(c)] = h;
-        h = carry_over(k, a, h);
+    for (int c = c0; c < c1; c += U) {
+        if (per > U) fetch(c);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (c + u >= c1) break;
+            keep[place(c + u)] = h;
+            h = carry_over(k[u], a[u], h);
+        }
     }
 }
 
@@ -315,7 +351,7 @@ __global__ void __launch_bounds__(1024) scan_carry(int64_t ends, int chunks, con
 // A block's states are worked out forward from the kept one, leaving two numbers a step: i, and what
 // dgate is of g.  The gates' and values' registers are then free for the next block's loads, which fly
 // while the block's gradient is walked back; dout's follow behind it.
-template <typename T, int N, bool SOME, typename Off>
+template <typename T, int N, bool COUPLED, bool SOME, bool PAST, typename Off>
 __global__ void __launch_bounds__(64) scan_bwd(ScanGeom g, ScanPlan q, const T *__restrict__ gate,
                                                const T *__restrict__ value, const float *__restrict__ states,
                                                const uint8_t *__restrict__ reset, const int32_t *__restrict__ lengths,
@@ -326,7 +362,6 @@ __global__ void __launch_bounds__(64) scan_bwd(ScanGeom g, ScanPlan q, const T *
     if (!w.find(g, q, lengths)) return;
     float back[N] = {};
     if (start) get_f32<N>(start + w.end(g, w.c), back);
-    const bool coupled = g.coupled;
     const Line<const T, N, Off> fl(gate, g.gate, w), vl(value, g.value, w), dl(dout, g.out, w);
     const Line<T, N, Off> dfl(dgate, g.dgate, w), dvl(dvalue, g.dvalue, w);
     const Resets<SOME> rl(reset, g, w.b);
@@ -356,15 +391,18 @@ __global__ void __launch_bounds__(64) scan_bwd(ScanGeom g, ScanPlan q, const T *
                 gates(f[u].get(j), a, i);
                 const float before = cut ? 0.f : h[j], x = v[u].get(j);
                 share[u][j] = i;
-                slope[u][j] = a * i * (coupled ? before - x : before);
-                h[j] = advance(before, i, x, coupled);
+                slope[u][j] = a * i * (COUPLED ? before - x : before);
+                h[j] = advance<COUPLED>(before, i, x);
             }
         });
     };
     auto backward = [&](auto full, int t, int n, int live) {
         constexpr bool FULL = decltype(full)::value;
+        char *to_gate = dfl.row(t + kBlock), *to_value = dvl.row(t + kBlock);
         each_step<kBlock, SOME>(SOME ? __brev(resets) >> (32 - kBlock) : 0, [&](int k, bool cut) {
             const int u = kBlock - 1 - k;
+            to_gate -= dfl.step;
+            to_value -= dvl.step;
             if (!FULL && u >= n) return;
             float yf[N] = {}, yv[N] = {};
             if (FULL || u < live) {
@@ -372,12 +410,12 @@ __global__ void __launch_bounds__(64) scan_bwd(ScanGeom g, ScanPlan q, const T *
                 for (int j = 0; j < N; ++j) {
                     const float gr = back[j] + d[u].get(j);
                     yf[j] = slope[u][j] * gr;
-                    yv[j] = coupled ? share[u][j] * gr : gr;
+                    yv[j] = COUPLED ? share[u][j] * gr : gr;
                     back[j] = cut ? 0.f : fmaf(-share[u][j], gr, gr);
                 }
             }
-            put_own<T, N>(dfl.at(t + u), yf, w.skip);
-            put_own<T, N>(dvl.at(t + u), yv, w.skip);
+            put_own<T, N, PAST>(dfl.lane(to_gate), yf, w.skip);
+            put_own<T, N, PAST>(dvl.lane(to_value), yv, w.skip);
         });
     };
     // blocks from the last one back: with checks until every step is valid in every thread of the wave
@@ -482,22 +520,27 @@ hipError_t carry(const ScanGeom &g, const ScanPlan &q, const float *first, float
     return hipGetLastError();
 }
 
-// Calls f(N, SOME, Off) with the plan's channels a thread, whether there are resets, and the type of a
-// lane's offset.
+// Calls f(N, COUPLED, SOME, Off) with the plan's channels a thread, the form, whether there are resets,
+// and the type of a lane's offset.
 template <bool TWO, typename F>
-hipError_t with_lanes(const ScanPlan &q, bool some, F f)
+hipError_t with_lanes(const ScanGeom &g, const ScanPlan &q, bool some, F f)
 {
-    auto with_off = [&](auto n, auto r) { return q.far ? f(n, r, int64_t()) : f(n, r, uint32_t()); };
-    auto with_resets = [&](auto n) { return some ? with_off(n, std::true_type()) : with_off(n, std::false_type()); };
+    auto with_resets = [&](auto n, auto c, auto off) {
+        return some ? f(n, c, std::true_type(), off) : f(n, c, std::false_type(), off);
+    };
+    auto with_form = [&](auto n, auto off) {
+        return g.coupled ? with_resets(n, std::true_type(), off) : with_resets(n, std::false_type(), off);
+    };
     if constexpr (TWO)
-        if (q.N == 2) return with_resets(std::integral_constant<int, 2>());
-    return with_resets(std::integral_constant<int, 1>());
+        if (q.N == 2) return with_form(std::integral_constant<int, 2>(), uint32_t());
+    return q.far ? with_form(std::integral_constant<int, 1>(), int64_t())
+                 : with_form(std::integral_constant<int, 1>(), uint32_t());
 }
 
 // The sequences of a wave lie within 4 GiB of each other, in bytes of the storage type.
-bool near(const gc_strides &s, const ScanGeom &g, const ScanPlan &q, int size)
+bool near(const gc_strides &s, const ScanGeom &g, int nv, int size)
 {
-    const int64_t others = std::min<int64_t>(g.B - 1, 63 / q.nv + 1);
+    const int64_t others = std::min<int64_t>(g.B - 1, 63 / nv + 1);
     return (__int128)others * s.batch + g.D < (int64_t(1) << 32) / size;
 }
 
@@ -506,23 +549,35 @@ bool near(const gc_strides &s, const ScanGeom &g, const ScanPlan &q, int size)
 bool plan_scan(const ScanGeom &g, int dtype, bool bwd, ScanPlan &q)
 {
     q = ScanPlan{};
-    q.N = g.D >= 2 && dtype == GC_BF16 ? 2 : 1;
+    if (int64_t(g.B) * g.D >= int64_t(1) << 31) return false;
+    const int blocks = g.T ? (g.T - 1) / kBlock + 1 : 1, size = dtype == GC_F32 ? 4 : 2;
+    q.far = !near(g.gate, g, g.D, size) || !near(g.value, g, g.D, size) || !near(g.out, g, g.D, size);
+    if (bwd) q.far |= !near(g.dgate, g, g.D, size) || !near(g.dvalue, g, g.D, size);
+    auto waves_of = [&](int n) { return (int64_t(g.B) * vectors(g.D, n) + 63) / 64; };
+    auto chunks_of = [&](int64_t waves) -> int64_t {
+        if (!waves || waves >= 512 || blocks < (bwd ? 10 : 15)) return 1;
+        return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(2048 / waves, 256), blocks / 2));
+    };
+    q.N = 1;
+    if (bwd && dtype == GC_BF16 && g.D >= 2 && !q.far) {
+        const int64_t waves = waves_of(2), chunks = chunks_of(waves);
+        if (waves * chunks >= (chunks > 1 ? 1536 : 2048)) q.N = 2;
+    }
+    const int64_t waves = waves_of(q.N);
     q.nv = vectors(g.D, q.N);
     q.lanes = int64_t(g.B) * q.nv;
-    if (int64_t(g.B) * g.D >= int64_t(1) << 31) return false;
-    const int64_t waves = (q.lanes + 63) / 64;
-    const int blocks = g.T ? (g.T - 1) / kBlock + 1 : 1;
-    int64_t chunks = 1;
-    if (waves && waves < 512) chunks = std::max<int64_t>(1, std::min<int64_t>(2048 / waves, blocks / 4));
+    const int64_t chunks = chunks_of(waves);
     const int per = int((blocks + chunks - 1) / chunks);
-    q.len = g.T ? std::min<int64_t>(int64_t(per) * kBlock, 0x7FFFFFF0) : kBlock;
+    q.len = int(std::min<int64_t>(int64_t(per) * kBlock, 1 << 30));
     q.chunks = (blocks + per - 1) / per;
     q.part_bytes = q.chunks > 1 ? (size_t(q.chunks) * g.B * g.D * 4 + 255) & ~size_t(255) : 0;
     q.ws_bytes = 2 * q.part_bytes;
+    // words of memory that rows of odd length share would go past the cache in halves
+    auto words = [&](const gc_strides &s) { return s.step * size % 4 == 0 && (g.B == 1 || s.batch * size % 4 == 0); };
+    q.past = size_t(g.B) * g.T * g.D * size * (bwd ? 5 : 3) >= kStreamBytes &&
+             (bwd ? words(g.dgate) && words(g.dvalue) : words(g.out));
     q.fd_nv = make_fastdiv(uint32_t(q.nv));
-    const int size = dtype == GC_F32 ? 4 : 2;
-    q.far = !near(g.gate, g, q, size) || !near(g.value, g, q, size) || !near(g.out, g, q, size);
-    if (bwd) q.far |= !near(g.dgate, g, q, size) || !near(g.dvalue, g, q, size);
+    q.fd_blocks = make_fastdiv(uint32_t(std::max<int64_t>(1, waves)));
     return launchable(waves * q.chunks, 64);
 }
 
@@ -534,19 +589,21 @@ hipError_t launch_scan_fwd(const ScanGeom &g, const ScanPlan &q, const void *gat
     if (!q.lanes) return hipSuccess;
     const T *f = static_cast<const T *>(gate), *v = static_cast<const T *>(value);
     float *keep = static_cast<float *>(ws), *add = keep + q.part_bytes / 4;
-    const dim3 grid(unsigned((q.lanes + 63) / 64), unsigned(q.chunks));
-    return with_lanes<sizeof(T) == 2>(q, reset, [&](auto nn, auto some, auto off) {
+    const dim3 grid(unsigned((q.lanes + 63) / 64 * q.chunks));
+    return with_lanes<false>(g, q, reset, [&](auto nn, auto form, auto some, auto off) {
         constexpr int N = decltype(nn)::value;
-        constexpr bool SOME = decltype(some)::value;
+        constexpr bool COUPLED = decltype(form)::value, SOME = decltype(some)::value;
         using Off = decltype(off);
         if (q.chunks > 1) {
-            hipLaunchKernelGGL((scan_fold_fwd<T, N, SOME, Off>), grid, dim3(64), 0, s, g, q, f, v, reset, lengths, keep, add);
+            hipLaunchKernelGGL((scan_fold_fwd<T, N, COUPLED, SOME, Off>), grid, dim3(64), 0, s, g, q, f, v, reset, lengths, keep, add);
             if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
             if (const hipError_t e = carry<false>(g, q, h0, keep, add, s); e != hipSuccess) return e;
         }
-        hipLaunchKernelGGL((scan_fwd<T, N, SOME, Off>), grid, dim3(64), 0, s, g, q, f, v, q.chunks > 1 ? keep : h0, reset, lengths,
-                           static_cast<T *>(out), last, states);
-        return hipGetLastError();
+        return with_past<true>(q.past, [&](auto past) {
+            hipLaunchKernelGGL((scan_fwd<T, N, COUPLED, SOME, decltype(past)::value, Off>), grid, dim3(64), 0, s, g, q, f, v,
+                               q.chunks > 1 ? keep : h0, reset, lengths, static_cast<T *>(out), last, states);
+            return hipGetLastError();
+        });
     });
 }
 
@@ -558,19 +615,22 @@ hipError_t launch_scan_bwd(const ScanGeom &g, const ScanPlan &q, const void *gat
     if (!q.lanes) return hipSuccess;
     const T *f = static_cast<const T *>(gate), *v = static_cast<const T *>(value), *d = static_cast<const T *>(dout);
     float *keep = static_cast<float *>(ws), *add = keep + q.part_bytes / 4;
-    const dim3 grid(unsigned((q.lanes + 63) / 64), unsigned(q.chunks));
-    return with_lanes<sizeof(T) == 2>(q, reset, [&](auto nn, auto some, auto off) {
+    const dim3 grid(unsigned((q.lanes + 63) / 64 * q.chunks));
+    return with_lanes<sizeof(T) == 2>(g, q, reset, [&](auto nn, auto form, auto some, auto off) {
         constexpr int N = decltype(nn)::value;
-        constexpr bool SOME = decltype(some)::value;
+        constexpr bool COUPLED = decltype(form)::value, SOME = decltype(some)::value;
         using Off = decltype(off);
         if (q.chunks > 1) {
             hipLaunchKernelGGL((scan_fold_bwd<T, N, SOME, Off>), grid, dim3(64), 0, s, g, q, f, d, reset, lengths, keep, add);
             if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
             if (const hipError_t e = carry<true>(g, q, dlast, keep, add, s); e != hipSuccess) return e;
         }
-        hipLaunchKernelGGL((scan_bwd<T, N, SOME, Off>), grid, dim3(64), 0, s, g, q, f, v, states, reset, lengths, d,
-                           q.chunks > 1 ? keep : dlast, static_cast<T *>(dgate), static_cast<T *>(dvalue), dh0);
-        return hipGetLastError();
+        return with_past<true>(q.past, [&](auto past) {
+            hipLaunchKernelGGL((scan_bwd<T, N, COUPLED, SOME, decltype(past)::value, Off>), grid, dim3(64), 0, s, g, q, f, v,
+                               states, reset, lengths, d, q.chunks > 1 ? keep : dlast, static_cast<T *>(dgate),
+                               static_cast<T *>(dvalue), dh0);
+            return hipGetLastError();
+        });
     });
 }
 

@@ -14,7 +14,6 @@
 #include <type_traits>
 
 #include "gc_core.h"
-#include "gc_norm.h"
 #include "gc_norm_res.h"
 
 namespace gc {
@@ -229,11 +228,10 @@ __global__ void __launch_bounds__(1024) rows_fwd_loop(RowsGeom g, const T *x, co
 }
 
 // ---------------------------------------------------------------- backward --
-// Adds up the running sums of a workgroup's teams and writes them as one row of D
-// pairs (dbeta's, dgamma's): teams within a wave by lane exchanges, the others
-// in order through one row in LDS.
+// Adds up the running sums of a workgroup's teams and writes them as one row of partials, D of dbeta's and
+// D of dgamma's: teams within a wave by lane exchanges, the others in order from LDS.
 template <int N, int NV>
-__device__ __forceinline__ void write_part(int D, int L, float (&db)[NV][N], float (&dg)[NV][N], float *row, float *part)
+__device__ __forceinline__ void write_part(int D, int L, float (&db)[NV][N], float (&dg)[NV][N], float *all, float *part)
 {
     const int tt = threadIdx.x & (L - 1);
     for (int m = 32; m >= L; m >>= 1) {
@@ -245,27 +243,35 @@ __device__ __forceinline__ void write_part(int D, int L, float (&db)[NV][N], flo
                 dg[i][j] += __shfl_xor(dg[i][j], m, 64);
             }
     }
-    const int wide = L < 64 ? 64 : L, turns = blockDim.x / wide, turn = threadIdx.x / wide;
-    const bool writes = int(threadIdx.x) % wide < L;
-    for (int w = 0; w < turns; ++w) {
-        if (w == turn && writes) {
+    const int wide = L < 64 ? 64 : L, turns = blockDim.x / wide;
+    if (int(threadIdx.x) % wide < L) {
+        float *to = turns > 1 ? all + int(threadIdx.x) / wide * 2 * D : part;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const Place<N> at(i * L + tt, D);
-                if (!at.live) continue;
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    if (j < at.skip) continue;
-                    float *dst = (turns > 1 && w < turns - 1 ? row : part) + 2 * int64_t(at.at + j);
-                    const float *src = row + 2 * int64_t(at.at + j);
-                    dst[0] = w ? src[0] + db[i][j] : db[i][j];
-                    dst[1] = w ? src[1] + dg[i][j] : dg[i][j];
-                }
-            }
+        for (int i = 0; i < NV; ++i) {
+            const Place<N> at(i * L + tt, D);
+            if (!at.live) continue;
+            Vec<float, N> b, g;
+            b.put(db[i]);
+            g.put(dg[i]);
+            put_own<false, float, N>(to + at.at, b, at.skip);
+            put_own<false, float, N>(to + D + at.at, g, at.skip);
         }
-        if (turns > 1) __syncthreads();
+    }
+    if (turns == 1) return;
+    __syncthreads();
+    for (int e = threadIdx.x; e < 2 * D; e += blockDim.x) {
+        float s = all[e];
+        for (int w = 1; w < turns; ++w) s += all[w * 2 * D + e];
+        part[e] = s;
     }
 }
+
+// A row's inputs, as they lie in memory.
+template <typename T, int N, int NV>
+struct RowIn {
+    Vec<T, N> x[NV], d[NV], t[NV];
+    float mean, rstd;
+};
 
 template <typename T, int N, int NV, bool PAST>
 __global__ void __launch_bounds__(512) rows_bwd(RowsGeom g, int L, const T *x, const void *__restrict__ gamma,
@@ -274,7 +280,24 @@ __global__ void __launch_bounds__(512) rows_bwd(RowsGeom g, int L, const T *x, c
 {
     __shared__ float red[32];
     extern __shared__ float joined[];
-    const int tt = threadIdx.x & (L - 1), teams = blockDim.x / L;
+    const int tt = threadIdx.x & (L - 1), teams = blockDim.x / L, team = threadIdx.x / L;
+    // every team of a workgroup takes as many turns, for the barriers; one without a row reads the last again
+    auto row_of = [&](int64_t turn) { return min(turn + team, g.rows - 1); };
+    auto fetch = [&](int64_t row) {
+        RowIn<T, N, NV> in;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const Place<N> at(i * L + tt, g.D);
+            in.x[i] = load_vec<T, N>(x + row * g.ld_x + at.at);
+            in.d[i] = load_vec<T, N>(dy + row * g.ld_y + at.at);
+            if (dtotal) in.t[i] = load_vec<T, N>(dtotal + row * g.ld_total + at.at);
+        }
+        in.mean = mean[row];
+        in.rstd = rstd[row];
+        return in;
+    };
+    const int64_t stride = int64_t(gridDim.x) * teams, first = int64_t(blockIdx.x) * teams;
+    RowIn<T, N, NV> next = fetch(row_of(first));
     float gm[NV][N], dg[NV][N] = {}, db[NV][N] = {};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -282,27 +305,19 @@ __global__ void __launch_bounds__(512) rows_bwd(RowsGeom g, int L, const T *x, c
         params_at<T, N>(g, gamma, at.at, 1.f, gm[i]);
     }
     const float inv = 1.f / float(g.D);
-    // every team of a workgroup takes as many turns, for the barriers; one without a row reads the last again
-    for (int64_t turn = int64_t(blockIdx.x) * teams; turn < g.rows; turn += int64_t(gridDim.x) * teams) {
-        const bool own = turn + threadIdx.x / L < g.rows;
-        const int64_t row = own ? turn + threadIdx.x / L : g.rows - 1;
-        Vec<T, N> xv[NV], dv[NV], tv[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const Place<N> at(i * L + tt, g.D);
-            xv[i] = load_vec<T, N>(x + row * g.ld_x + at.at);
-            dv[i] = load_vec<T, N>(dy + row * g.ld_y + at.at);
-            if (dtotal) tv[i] = load_vec<T, N>(dtotal + row * g.ld_total + at.at);
-        }
-        const float m = mean[row], r = rstd[row];
+    for (int64_t turn = first; turn < g.rows; turn += stride) {
+        const bool own = turn + team < g.rows;
+        const int64_t row = row_of(turn);
+        const RowIn<T, N, NV> in = next;
+        if (turn + stride < g.rows) next = fetch(row_of(turn + stride));     // flies while this row is worked on
         float c[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const Place<N> at(i * L + tt, g.D);
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const float hat = (xv[i].get(j) - m) * r;
-                const float d = own && j >= at.skip ? dv[i].get(j) : 0.f;
+                const float hat = (in.x[i].get(j) - in.mean) * in.rstd;
+                const float d = own && j >= at.skip ? in.d[i].get(j) : 0.f;
                 const float dh = own && j >= at.skip ? d * hat : 0.f;
                 db[i][j] += d;
                 dg[i][j] += dh;
@@ -319,9 +334,9 @@ __global__ void __launch_bounds__(512) rows_bwd(RowsGeom g, int L, const T *x, c
             float z[N];
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const float hat = (xv[i].get(j) - m) * r;
-                z[j] = r * (gm[i][j] * dv[i].get(j) - c1 - hat * c2);
-                if (dtotal) z[j] += tv[i].get(j);
+                const float hat = (in.x[i].get(j) - in.mean) * in.rstd;
+                z[j] = in.rstd * (gm[i][j] * in.d[i].get(j) - c1 - hat * c2);
+                if (dtotal) z[j] += in.t[i].get(j);
             }
             Vec<T, N> out;
             out.put(z);
@@ -329,6 +344,46 @@ __global__ void __launch_bounds__(512) rows_bwd(RowsGeom g, int L, const T *x, c
         }
     }
     if (part) write_part<N, NV>(g.D, L, db, dg, joined, part + int64_t(blockIdx.x) * 2 * g.D);
+}
+
+// dbeta and dgamma from the rows of partials: a workgroup takes 64 columns, its threads every 32nd row
+// of two columns each.
+constexpr int kSumCols = 64, kSumSlots = 32;
+template <typename T>
+__global__ void __launch_bounds__(1024) rows_params(RowsGeom g, int parts, const float *__restrict__ part,
+                                                    void *__restrict__ dgamma, void *__restrict__ dbeta)
+{
+    __shared__ float red[kSumSlots][kSumCols];
+    constexpr int U = 8;      // rows whose loads fly together
+    const int col = threadIdx.x % (kSumCols / 2) * 2, slot = threadIdx.x / (kSumCols / 2);
+    const int e = blockIdx.x * kSumCols + col;
+    float s0 = 0.f, s1 = 0.f;
+    if (e < 2 * g.D)
+        for (int r = slot; r < parts; r += U * kSumSlots) {
+            Vec<float, 2> v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (r + u * kSumSlots < parts) v[u] = load_vec<float, 2>(part + int64_t(r + u * kSumSlots) * 2 * g.D + e);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (r + u * kSumSlots < parts) {
+                    s0 += v[u].get(0);
+                    s1 += v[u].get(1);
+                }
+        }
+    red[slot][col] = s0;
+    red[slot][col + 1] = s1;
+    __syncthreads();
+    const int k = blockIdx.x * kSumCols + threadIdx.x;
+    if (threadIdx.x >= kSumCols || k >= 2 * g.D) return;
+    float s = red[0][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < kSumSlots; ++i) s += red[i][threadIdx.x];
+    void *to = k < g.D ? dbeta : dgamma;
+    const int at = k < g.D ? k : k - g.D;
+    if (!to) return;
+    if (g.pf32) static_cast<float *>(to)[at] = s;
+    else static_cast<T *>(to)[at] = from_f32<T>(s);
 }
 
 // Rows past the registers: the sums over rows first, by columns (dx may take dy's place),
@@ -346,9 +401,9 @@ __global__ void __launch_bounds__(256) rows_bwd_columns(RowsGeom g, const T *__r
         db += d;
         dg += d * ((to_f32(x[row * g.ld_x + e]) - mean[row]) * rstd[row]);
     }
-    float *to = part + (int64_t(blockIdx.y) * g.D + e) * 2;
+    float *to = part + int64_t(blockIdx.y) * 2 * g.D + e;
     to[0] = db;
-    to[1] = dg;
+    to[g.D] = dg;
 }
 
 template <typename T, int N>
@@ -434,7 +489,8 @@ void plan_rows(const RowsGeom &g, int dtype, bool bwd, bool more, RowsPlan &q)
         const int teams = q.threads / q.L;
         q.grid = std::min<int64_t>((rows + teams - 1) / teams, bwd ? kCUs * 512 / q.threads : kCUs * 2048 / q.threads);
         q.parts = q.grid;
-        q.lds_bytes = bwd && q.threads > std::max(64, q.L) ? size_t(g.D) * 8 : 0;
+        const int turns = q.threads / std::max(64, q.L);
+        q.lds_bytes = bwd && turns > 1 ? size_t(turns) * g.D * 8 : 0;
     }
     const size_t bytes = size_t(rows) * g.D * (dtype == GC_F32 ? 4 : 2) * ((bwd ? 3 : 2) + (more ? (bwd ? 1 : 2) : 0));
     q.past = !q.loop && q.N > 1 && bytes >= kStreamBytes;
@@ -497,10 +553,10 @@ hipError_t launch_rows_bwd(const RowsGeom &g, const RowsPlan &q, const void *x, 
         }
         if (e != hipSuccess) return e;
     }
-    NormGeom n{};
-    n.C = g.D;
-    n.pf32 = g.pf32;
-    return launch_norm_params<T>(n, g.rows ? q.parts : 0, part, dgamma, dbeta, s);
+    if (!sums) return hipSuccess;
+    hipLaunchKernelGGL((rows_params<T>), dim3(unsigned((2 * g.D + kSumCols - 1) / kSumCols)), dim3(1024), 0, s, g,
+                       g.rows ? int(q.parts) : 0, part, dgamma, dbeta);
+    return hipGetLastError();
 }
 
 #define GC_ROWS_INSTANCES(T)                                                                                          \
