@@ -79,7 +79,8 @@ struct DistillPlan {
     int N, NV;      // elements of a vector; vectors a thread holds (0: the row is walked)
     int L;          // threads of a row's team, a power of two
     int threads;    // of a workgroup
-    int past;
+    int lists;      // of a row's many entries, a power of two
+    int past;       // the output goes past the cache
     int64_t grid;
     size_t lds_bytes;
 };

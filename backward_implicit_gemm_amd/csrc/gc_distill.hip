@@ -7,9 +7,11 @@
 // Memory bound: the logits are read once (the step holds a row in the registers of its
 // team between the row's sum and its gradient), the gradient is written once.  A team of
 // threads takes a row: lanes of a wave for short rows, a workgroup for long ones.  The teacher's shares
-// are worked out by every wave for itself, which needs no barrier; entries are few.  The
+// are worked out by the row's first wave while the others add up the logits; entries are few.  The
 // gradient is written as if there were no entries, then the entries' places are written again
-// with all that belongs to them, by the first entry of each place.
+// with all that belongs to them.  Many entries are rather looked up, vector by vector, while the
+// gradient is written, as each place written again costs a memory line: 4096 rows of 40,960 bf16
+// with 256 entries take took 202 us the one way and 181 the other.
 #include <algorithm>
 #include <iterator>
 #include <math.h>
@@ -23,17 +25,68 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896f;
 
-// An entry in LDS: its place (-1: empty), its share and its logit.
-struct Entry {
-    int at;
-    float p, z;
+// A row's entries in LDS, in whole fours: place (-1: empty), share, both logits; the place again where the
+// entry is the first one there (else -1), and the shares of all there.  More than kScan entries are
+// kept in lists too, a vector's in the list of its number modulo their count, a power of two.
+struct Entries {
+    int *at;
+    float *p, *v, *z;
+    int *to;
+    float *sum;
+    int *next, *first;
 };
+constexpr int kScan = 16;
+__host__ __device__ __forceinline__ int fours(int K) { return (K + 3) & ~3; }
+__host__ __device__ __forceinline__ int entry_bytes(int K, int lists)
+{
+    return K > kScan ? 28 * fours(K) + 4 * lists : 24 * fours(K);
+}
+
+constexpr int kOwn = 2;   // entries of a lane that stay in registers
 
 template <typename V, typename F>
 __device__ __forceinline__ V lanes_fold(V v, int width, F f)
 {
     for (int m = width >> 1; m > 0; m >>= 1) v = f(v, __shfl_xor(v, m, 64));
     return v;
+}
+
+// For each entry: the shares of all entries of its place, in their order, and whether it is the first
+// one there.  By one wave, whose LDS accesses are in order.
+template <int N>
+__device__ __forceinline__ void gather_places(const Entries &entry, int K, int lists, int lane, int width)
+{
+    const int kp = fours(K);
+    auto list_of = [&](int at) { return at / N & (lists - 1); };
+    if (K > kScan) {
+        for (int k = lane; k < lists / 4; k += width) reinterpret_cast<int4 *>(entry.first)[k] = int4{-1, -1, -1, -1};
+        team_sync(true);
+        for (int k = lane; k < K; k += width)
+            if (const int at = entry.at[k]; at >= 0) entry.next[k] = atomicExch(entry.first + list_of(at), k);
+    }
+    team_sync(true);
+    for (int k = lane; k < K; k += width) {
+        const int at = entry.at[k];
+        float p = at >= 0 ? entry.p[k] : 0.f;
+        bool alone = K <= kScan ? false : true, first = at >= 0;
+        if (K > kScan && at >= 0)
+            for (int o = entry.first[list_of(at)]; o >= 0; o = entry.next[o]) alone &= o == k || entry.at[o] != at;
+        if (!alone && at >= 0) {
+            p = 0.f;
+            for (int o = 0; o < kp; o += 4) {
+                const int4 four = *reinterpret_cast<const int4 *>(entry.at + o);
+                if (four.x != at && four.y != at && four.z != at && four.w != at) continue;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool same = (j == 0 ? four.x : j == 1 ? four.y : j == 2 ? four.z : four.w) == at;
+                    if (same) p += entry.p[o + j];
+                    first &= !(same && o + j < k);
+                }
+            }
+        }
+        entry.to[k] = first ? at : -1;
+        entry.sum[k] = p;
+    }
 }
 
 template <int N>
@@ -76,17 +129,27 @@ __device__ __forceinline__ float share(float z, float peak, float c) { return __
 // OP: GC_OP_FWD writes loss, peak and mass, GC_OP_BWD reads the last two and writes dlogits,
 // GC_OP_STEP writes loss and dlogits.  NV vectors of a row stay in registers, 0: the row is walked.
 template <typename T, int N, int NV, int OP, bool PAST>
-__global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, const T *logits, const void *__restrict__ index,
+__global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, int lists, const T *logits, const void *__restrict__ index,
                                                 const void *__restrict__ teacher, float *__restrict__ peak,
                                                 float *__restrict__ mass, const float *__restrict__ dloss,
                                                 float *__restrict__ loss, T *dlogits)
 {
     __shared__ float red[2][16];
-    extern __shared__ Entry all[];
+    __shared__ int any[32];      // whether a team's row has entries
+    extern __shared__ int4 all[];
     const int tt = threadIdx.x & (L - 1), team = threadIdx.x / L, teams = blockDim.x / L;
     const int64_t row = int64_t(blockIdx.x) * teams + team;
     if (row >= g.rows) return;   // a whole team; a team of several waves is alone in its workgroup
-    Entry *entry = all + team * g.K;
+    const int kp = fours(g.K);
+    Entries entry;
+    entry.at = reinterpret_cast<int *>(reinterpret_cast<char *>(all) + team * entry_bytes(g.K, lists));
+    entry.p = reinterpret_cast<float *>(entry.at + kp);
+    entry.v = entry.p + kp;
+    entry.z = entry.v + kp;
+    entry.to = reinterpret_cast<int *>(entry.z + kp);
+    entry.sum = reinterpret_cast<float *>(entry.to + kp);
+    entry.next = reinterpret_cast<int *>(entry.sum + kp);
+    entry.first = entry.next + kp;
     const T *z = logits + row * g.ld;
     const float t = g.temperature, c = kLog2e / t;
     const int nv = vectors(g.V, N);
@@ -102,16 +165,9 @@ __global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, const T *l
 #pragma unroll
         for (int u = 0; u < U; ++u) held[u] = load_vec<T, N>(z + Place<N>(i + int64_t(u) * L, g.V).at);
     };
-    fetch(tt);
-    float m = 0.f, s = 0.f, scale = 0.f;
-    if (OP == GC_OP_BWD) {
-        m = peak[row];
-        s = mass[row];
-    }
-    if (OP != GC_OP_FWD) scale = dloss[row];
-
-    // the teacher's shares, by every wave for itself; a lane's first entry stays in registers
+    // the teacher's shares, by the team's first wave; a lane's first entries stay in registers
     const int width = L < 64 ? L : 64, lane = tt & (width - 1);
+    const bool leads = tt < width;
     auto entry_at = [&](int k, int &at, float &v) {
         const int64_t i = g.i64 ? static_cast<const int64_t *>(index)[row * g.ld_index + k]
                                 : static_cast<const int32_t *>(index)[row * g.ld_index + k];
@@ -120,28 +176,57 @@ __global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, const T *l
                   : to_f32(static_cast<const bf16_t *>(teacher)[row * g.ld_teacher + k]);
         if (at < 0) v = -INFINITY;
     };
-    int at0 = -1;
-    float v0 = -INFINITY, top = -INFINITY, total = 0.f;
-    if (lane < g.K) entry_at(lane, at0, v0);
+    int own_at[kOwn];
+    float own_v[kOwn], own_z[kOwn], top = -INFINITY, total = 0.f, inv_total = 0.f;
+    auto logit = [&](int at) { return at >= 0 ? to_f32(z[at]) : 0.f; };
+    // f(k, place, teacher's logit, student's logit) for the lane's entries
     auto each_entry = [&](auto f) {
-        if (lane < g.K) f(lane, at0, v0);
-        for (int k = lane + width; k < g.K; k += width) {
+#pragma unroll
+        for (int e = 0; e < kOwn; ++e)
+            if (lane + e * width < g.K) f(lane + e * width, own_at[e], own_v[e], own_z[e]);
+        for (int k = lane + kOwn * width; k < g.K; k += width) {
             int at;
             float v;
             entry_at(k, at, v);
-            f(k, at, v);
+            f(k, at, v, logit(at));
         }
     };
-    each_entry([&](int, int, float v) { top = fmaxf(top, v != v ? INFINITY : v); });
-    top = lanes_fold(top, width, most);
-    const bool some = top > -INFINITY;
-    each_entry([&](int, int, float v) { total += v == -INFINITY ? 0.f : share(v, top, c); });
-    total = lanes_fold(total, width, plus);
-    const float inv_total = 1.f / total;
-    if (tt < width)
-        each_entry([&](int k, int at, float v) {
-            entry[k] = Entry{at, v == -INFINITY ? 0.f : share(v, top, c) * inv_total, at >= 0 ? to_f32(z[at]) : 0.f};
-        });
+    bool some = false;
+    if (leads) {
+#pragma unroll
+        for (int e = 0; e < kOwn; ++e)
+            if (lane + e * width < g.K) entry_at(lane + e * width, own_at[e], own_v[e]);
+    }
+    // behind the entries, which are waited for first
+    fetch(tt);
+    float m = 0.f, s = 0.f, scale = 0.f;
+    if (OP == GC_OP_BWD) {
+        m = peak[row];
+        s = mass[row];
+    }
+    if (OP != GC_OP_FWD) scale = dloss[row];
+    if (leads) {
+#pragma unroll
+        for (int e = 0; e < kOwn; ++e)
+            if (lane + e * width < g.K) own_z[e] = logit(own_at[e]);
+        each_entry([&](int, int, float v, float) { top = fmaxf(top, v != v ? INFINITY : v); });
+        top = lanes_fold(top, width, most);
+        some = top > -INFINITY;
+        each_entry([&](int, int, float v, float) { total += v == -INFINITY ? 0.f : share(v, top, c); });
+        total = lanes_fold(total, width, plus);
+        inv_total = 1.f / total;
+        if (tt == 0) any[team] = some;
+        if (OP != GC_OP_FWD) {
+            each_entry([&](int k, int at, float v, float x) {
+                entry.at[k] = at;
+                entry.p[k] = v == -INFINITY ? 0.f : share(v, top, c) * inv_total;
+                entry.v[k] = v;
+                entry.z[k] = x;
+            });
+            if (g.K + lane < kp) entry.at[g.K + lane] = -1;
+            gather_places<N>(entry, g.K, lists, lane, width);
+        }
+    }
 
     // The student's largest logit and the sum of the exponentials: each thread around its own largest,
     // so that one exchange joins both.
@@ -204,22 +289,25 @@ __global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, const T *l
         if (peak) peak[row] = m;
         if (mass) mass[row] = s;
     }
-    if (OP != GC_OP_BWD && tt < width) {
+    if (OP != GC_OP_BWD && leads) {
         // log q = (z - peak)/t - log(mass), log p = (teacher - top)/t - log(total)
         const float log_s = logf(s), log_total = logf(total);
         float sum = 0.f;
-        each_entry([&](int k, int, float v) {
-            const Entry e = entry[k];      // this thread's own
-            if (some && e.p != 0.f)
-                sum += e.z == -INFINITY ? INFINITY : e.p * (((v - top) - (e.z - m)) / t - log_total + log_s);
-        });
+        auto add = [&](float p, float v, float x) {
+            if (some && p != 0.f) sum += x == -INFINITY ? INFINITY : p * (((v - top) - (x - m)) / t - log_total + log_s);
+        };
+        if (OP == GC_OP_FWD)
+            each_entry([&](int, int, float v, float x) { add(v == -INFINITY ? 0.f : share(v, top, c) * inv_total, v, x); });
+        else
+            for (int k = lane; k < g.K; k += width) add(entry.p[k], entry.v[k], entry.z[k]);      // this thread's own
         sum = lanes_fold(sum, width, plus);
         if (tt == 0) loss[row] = t * t * sum;
     }
     if (OP == GC_OP_FWD) return;
 
-    // the entries' logits have been read, should the gradient take their place
-    if (OP == GC_OP_BWD && dlogits == logits) team_sync(L <= 64);
+    // the entries are in LDS, and their logits read, should the gradient take their place
+    if (OP == GC_OP_BWD || L <= 64) team_sync(L <= 64);
+    some = any[team];
     const float by = some ? scale * t : 0.f, inv = by / s;
     const float own = mine == -INFINITY ? 0.f : share(base, m, c) * inv;     // of this thread's exponentials
     T *out = dlogits + row * g.ld_grad;
@@ -236,6 +324,13 @@ __global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, const T *l
                 y[j] = KEEP ? shares[u][j] * own : share(held[u].get(j), m, c) * inv;
                 if (!some) y[j] = 0.f;
             }
+            if (g.K > kScan)
+                for (int k = entry.first[(i + int64_t(u) * L) & (lists - 1)]; k >= 0; k = entry.next[k]) {
+                    const int place = entry.to[k] - at.at;
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        if (j == place) y[j] -= by * entry.sum[k];
+                }
             Vec<T, N> o;
             o.put(y);
             put_own<PAST, T, N>(out + at.at, o, at.skip);
@@ -249,22 +344,12 @@ __global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, const T *l
             write(i);
         }
     }
-    if (!some) return;
+    if (!some || g.K > kScan) return;
     // the stores above have arrived before any of the entries' begins
     __builtin_amdgcn_s_waitcnt(0);
     team_sync(L <= 64);
-    for (int k = tt; k < g.K; k += L) {
-        const Entry e = entry[k];
-        if (e.at < 0) continue;
-        float p = 0.f;
-        bool first = true;
-        for (int o = 0; o < g.K; ++o) {
-            const bool same = entry[o].at == e.at;
-            if (same) p += entry[o].p;
-            first &= !(same && o < k);
-        }
-        if (first) out[e.at] = from_f32<T>(by * (share(e.z, m, c) / s - p));
-    }
+    for (int k = tt; k < g.K; k += L)
+        if (const int at = entry.to[k]; at >= 0) out[at] = from_f32<T>(by * (share(entry.z[k], m, c) / s - entry.sum[k]));
 }
 
 // Calls f(NV) for the numbers of vectors a thread may hold.
@@ -296,13 +381,15 @@ void plan_distill(const DistillGeom &g, int dtype, int op, DistillPlan &q)
     const int vec = dtype == GC_F32 ? 4 : 8;
     q.N = g.V < vec ? 1 : vec;
     const int64_t nv = vectors(g.V, q.N);
-    // two vectors a thread within a wave, then as many as keep two workgroups on a CU
-    const int many = dtype == GC_F32 ? 8 : 5;
+    // the fewest threads whose registers hold the row, then more while the chip has room for them
+    const int most = g.V <= 64 * 64 ? 64 / vec : 20;
     q.L = 8;
-    while (q.L < 64 && q.L * 2 < nv) q.L *= 2;
-    while (q.L < 1024 && int64_t(q.L) * many < nv) q.L *= 2;
+    while (q.L < 1024 && int64_t(q.L) * most < nv) q.L *= 2;
+    while (q.L < 1024 && q.L < nv && g.rows * q.L < kCUs * 1024) q.L *= 2;
     q.threads = std::max(256, q.L);
-    while (q.L <= 64 && size_t(q.threads / q.L) * g.K * sizeof(float) * 3 > 49152) {
+    q.lists = 4;
+    while (q.lists < 4096 && q.lists < nv && q.lists < 64 * g.K) q.lists *= 2;
+    while (q.L <= 64 && size_t(q.threads / q.L) * entry_bytes(g.K, q.lists) > 49152) {
         if (q.threads > 64) q.threads /= 2;
         else q.L *= 2;
     }
@@ -315,7 +402,7 @@ void plan_distill(const DistillGeom &g, int dtype, int op, DistillPlan &q)
     }
     const int teams = q.threads / q.L;
     q.grid = (g.rows + teams - 1) / teams;
-    q.lds_bytes = size_t(teams) * g.K * 12;
+    q.lds_bytes = op == GC_OP_FWD ? 0 : size_t(teams) * entry_bytes(g.K, q.lists);
     q.past = op != GC_OP_FWD && q.N > 1 && size_t(g.rows) * g.V * (dtype == GC_F32 ? 8 : 4) >= kStreamBytes;
 }
 
@@ -327,8 +414,8 @@ hipError_t launch_distill(const DistillGeom &g, const DistillPlan &q, int op, co
     if (!g.rows) return hipSuccess;
     auto go = [&](auto n, auto nv, auto o, auto past) {
         hipLaunchKernelGGL((distill<T, decltype(n)::value, decltype(nv)::value, decltype(o)::value, decltype(past)::value>),
-                           dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s, g, q.L, static_cast<const T *>(logits),
-                           index, teacher, peak, mass, dloss, loss, static_cast<T *>(dlogits));
+                           dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s, g, q.L, q.lists,
+                           static_cast<const T *>(logits), index, teacher, peak, mass, dloss, loss, static_cast<T *>(dlogits));
         return hipGetLastError();
     };
     using Fwd = std::integral_constant<int, GC_OP_FWD>;
