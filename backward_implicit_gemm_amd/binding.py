@@ -828,8 +828,30 @@ class _Descs:
         return ref
 
 
+class _Checked:
+    """A call's checks of its tensors (None where one is left out): done in full, by `full`, which gives
+    the descriptor, where the tensors differ from the last call's in type, shape, distances,
+    device or presence; else one C++ call compares all of these (checked one by one from Python,
+    the 8 tensors of a layer norm's forward cost 5 us more)."""
+
+    def __init__(self, full):
+        self.full, self.last = full, None
+
+    def __call__(self, helper, *tensors):
+        """The descriptor, and the tensors' addresses."""
+        there = [t for t in tensors if t is not None]
+        last = self.last
+        if last is not None and last[0] == [t is None for t in tensors] and last[1](*there):
+            desc = last[2]
+        else:
+            desc, keep = self.full(helper, *tensors)
+            guards = TensorGuards(*there, dynamic_dims_sizes=None, dynamic_dims_strides=None) if keep else None
+            self.last = ([t is None for t in tensors], guards.check, desc) if keep else None
+        return desc, [None if t is None else t.data_ptr() for t in tensors]
+
+
 def _dense_rows(t, name, dtype, shape, device):
-    """Address of t, rows of dense values, and the distance of two rows."""
+    """The distance of two rows of t, whose values have to be dense."""
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
@@ -842,7 +864,17 @@ def _dense_rows(t, name, dtype, shape, device):
         ld = n
     elif ld < n:
         raise ValueError(f"the rows of {name} must not overlap")
-    return _on(t, name, device), ld
+    _on(t, name, device)
+    return ld
+
+
+def _in_place(out, name, ld, *inputs):
+    """Refuses an output over an input whose rows lie otherwise; whether that can be left out where
+    the distances are the same."""
+    for t, other in inputs:
+        if t is not None and other != ld and t.data_ptr() == out.data_ptr() and t.data_ptr():
+            raise ValueError(f"{name} in place has to have the row distance of its input")
+    return all(t is None or other == ld for t, other in inputs)
 
 
 def _extent(value, name, least, most):
@@ -882,47 +914,47 @@ class LayerNorm:
         need = int(lib().gc_layer_norm_workspace_bytes(self._desc((dim,) * 4), self.dt))
         self._ws = _Workspace(need, self.device)
 
+        self._fwd, self._bwd = _Checked(LayerNorm._check_fwd), _Checked(LayerNorm._check_bwd)
+
     def _rows(self, t, name):
-        return _dense_rows(t, name, self.dtype, self.shape, self.device)
+        return self.shape[1] if t is None else _dense_rows(t, name, self.dtype, self.shape, self.device)
 
-    def _param(self, t, name):
-        return None if t is None else _arg(t, name, self.param_dtype, self.param_shape, self.device)
+    def _params(self, **tensors):
+        for name, t in tensors.items():
+            if t is not None:
+                _arg(t, name, self.param_dtype, self.param_shape, self.device)
 
-    def _stat(self, t, name):
-        return None if t is None else _arg(t, name, torch.float32, self.stat_shape, self.device)
+    def _stats(self, **tensors):
+        for name, t in tensors.items():
+            if t is not None:
+                _arg(t, name, torch.float32, self.stat_shape, self.device)
 
-    @staticmethod
-    def _in_place(out, name, *inputs):
-        for address, ld in inputs:
-            if address == out[0] and ld != out[1] and address:
-                raise ValueError(f"{name} in place has to have the row distance of its input")
+    def _check_fwd(self, x, residual, gamma, beta, y, total, mean, rstd):
+        lx, ly = self._rows(x, "x"), self._rows(y, "y")
+        lr, lt = self._rows(residual, "residual"), self._rows(total, "total")
+        same = total is None or _in_place(total, "total", lt, (x, lx), (residual, lr))
+        self._params(gamma=gamma, beta=beta)
+        self._stats(mean=mean, rstd=rstd)
+        return self._desc((lx, lr, lt, ly)), same
 
     def fwd(self, x, gamma, beta, y, mean=None, rstd=None, residual=None, total=None, stream=None):
-        xp, yp = self._rows(x, "x"), self._rows(y, "y")
-        none = None, self.shape[1]
-        rp = none if residual is None else self._rows(residual, "residual")
-        tp = none if total is None else self._rows(total, "total")
-        if total is not None:
-            self._in_place(tp, "total", xp, rp)
-        gp, bp = self._param(gamma, "gamma"), self._param(beta, "beta")
-        mp, sp = self._stat(mean, "mean"), self._stat(rstd, "rstd")
-        st = lib().gc_layer_norm_fwd(xp[0], rp[0], gp, bp, yp[0], tp[0], mp, sp,
-                                     self._desc((xp[1], rp[1], tp[1], yp[1])), self.dt, self.pt,
-                                     _raw_stream(stream, self.device))
+        desc, at = self._fwd(self, x, residual, gamma, beta, y, total, mean, rstd)
+        st = lib().gc_layer_norm_fwd(*at, desc, self.dt, self.pt, _raw_stream(stream, self.device))
         _check("gc_layer_norm_fwd", st)
         return y, mean, rstd, total
 
+    def _check_bwd(self, x, gamma, dy, dtotal, mean, rstd, dx, dgamma, dbeta):
+        lx, ly, lo, lt = self._rows(x, "x"), self._rows(dy, "dy"), self._rows(dx, "dx"), self._rows(dtotal, "dtotal")
+        same = _in_place(dx, "dx", lo, (x, lx), (dy, ly), (dtotal, lt))
+        self._params(gamma=gamma, dgamma=dgamma, dbeta=dbeta)
+        self._stats(mean=mean, rstd=rstd)
+        return self._desc((lx, lo, lt, ly)), same
+
     def bwd(self, x, gamma, dy, mean, rstd, dx, dgamma=None, dbeta=None, dtotal=None, stream=None):
-        xp, yp, op = self._rows(x, "x"), self._rows(dy, "dy"), self._rows(dx, "dx")
-        tp = (None, self.shape[1]) if dtotal is None else self._rows(dtotal, "dtotal")
-        self._in_place(op, "dx", xp, yp, tp)
-        gp = self._param(gamma, "gamma")
-        mp, sp = self._stat(mean, "mean"), self._stat(rstd, "rstd")
-        dg, db = self._param(dgamma, "dgamma"), self._param(dbeta, "dbeta")
+        desc, at = self._bwd(self, x, gamma, dy, dtotal, mean, rstd, dx, dgamma, dbeta)
         raw = _raw_stream(stream, self.device)
         ws, n, _owner = self._ws.on(raw)
-        st = lib().gc_layer_norm_bwd(xp[0], gp, yp[0], tp[0], mp, sp, op[0], dg, db, ws, n,
-                                     self._desc((xp[1], op[1], tp[1], yp[1])), self.dt, self.pt, raw)
+        st = lib().gc_layer_norm_bwd(*at, ws, n, desc, self.dt, self.pt, raw)
         _check("gc_layer_norm_bwd", st)
         return dx, dgamma, dbeta
 
@@ -953,9 +985,10 @@ class Recurrence:
         need = lib().gc_recurrence_workspace_bytes
         every = self._desc((self._dense,) * 5 + ((length, 1),))
         self._ws = {op: _Workspace(int(need(op, every, self.dt)), self.device) for op in (GC_OP_FWD, GC_OP_BWD)}
+        self._fwd, self._bwd = _Checked(Recurrence._check_fwd), _Checked(Recurrence._check_bwd)
 
     def _seq(self, t, name, output=False):
-        """Address of t and its distances of sequences and of steps."""
+        """The distances of t's sequences and steps."""
         if t.shape != self.shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(self.shape)}")
         if t.dtype != self.dtype:
@@ -965,7 +998,8 @@ class Recurrence:
             raise ValueError(f"the channels of {name} must be dense")
         if output and not self._apart(batch, step):
             raise ValueError(f"the steps of {name} must not overlap")
-        return _on(t, name, self.device), (batch, step)
+        _on(t, name, self.device)
+        return batch, step
 
     def _apart(self, batch, step):
         B, T, D = self.shape
@@ -974,49 +1008,50 @@ class Recurrence:
         near, far = sorted([(step, T)] * (T > 1) + [(batch, B)] * (B > 1) + [(D, 1)] * ((T == 1) + (B == 1)))
         return near[0] >= D and (far[1] == 1 or near[0] * (near[1] - 1) + D <= far[0])
 
-    def _end(self, t, name):
-        return None if t is None else _arg(t, name, torch.float32, self.end_shape, self.device)
-
-    def _states(self, t):
-        return None if t is None else _arg(t, "states", torch.float32, self.states_shape, self.device)
+    def _ends(self, states, **ends):
+        for name, t in ends.items():
+            if t is not None:
+                _arg(t, name, torch.float32, self.end_shape, self.device)
+        if states is not None:
+            _arg(states, "states", torch.float32, self.states_shape, self.device)
 
     def _steps(self, reset, lengths):
-        rp, rs, lp = None, (0, 0), None
-        if reset is not None:
-            if reset.shape != self._step_shape:
-                raise ValueError(f"reset has shape {tuple(reset.shape)}, expected {tuple(self._step_shape)}")
-            if reset.dtype not in (torch.bool, torch.uint8):
-                raise TypeError(f"reset has dtype {reset.dtype}, expected bool or uint8")
-            rp, rs = _on(reset, "reset", self.device), reset.stride()
+        """The distances of reset."""
         if lengths is not None:
-            lp = _arg(lengths, "lengths", torch.int32, self._length_shape, self.device)
-        return rp, rs, lp
+            _arg(lengths, "lengths", torch.int32, self._length_shape, self.device)
+        if reset is None:
+            return 0, 0
+        if reset.shape != self._step_shape:
+            raise ValueError(f"reset has shape {tuple(reset.shape)}, expected {tuple(self._step_shape)}")
+        if reset.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"reset has dtype {reset.dtype}, expected bool or uint8")
+        _on(reset, "reset", self.device)
+        return reset.stride()
+
+    def _check_fwd(self, gate, value, h0, reset, lengths, out, last, states):
+        seqs = self._seq(gate, "gate"), self._seq(value, "value"), self._seq(out, "out", True)
+        self._ends(states, h0=h0, last=last)
+        return self._desc((*seqs, self._dense, self._dense, self._steps(reset, lengths))), True
 
     def fwd(self, gate, value, out, h0=None, last=None, states=None, reset=None, lengths=None, stream=None):
-        gp, gs = self._seq(gate, "gate")
-        vp, vs = self._seq(value, "value")
-        op, os_ = self._seq(out, "out", True)
-        hp, ep, kp = self._end(h0, "h0"), self._end(last, "last"), self._states(states)
-        rp, rs, lp = self._steps(reset, lengths)
+        desc, at = self._fwd(self, gate, value, h0, reset, lengths, out, last, states)
         raw = _raw_stream(stream, self.device)
         ws, n, _owner = self._ws[GC_OP_FWD].on(raw)
-        st = lib().gc_recurrence_fwd(gp, vp, hp, rp, lp, op, ep, kp, ws, n,
-                                     self._desc((gs, vs, os_, self._dense, self._dense, rs)), self.dt, raw)
+        st = lib().gc_recurrence_fwd(*at, ws, n, desc, self.dt, raw)
         _check("gc_recurrence_fwd", st)
         return out, last
 
+    def _check_bwd(self, gate, value, states, reset, lengths, dout, dlast, dgate, dvalue, dh0):
+        seqs = (self._seq(gate, "gate"), self._seq(value, "value"), self._seq(dout, "dout"),
+                self._seq(dgate, "dgate", True), self._seq(dvalue, "dvalue", True))
+        self._ends(states, dlast=dlast, dh0=dh0)
+        return self._desc((*seqs, self._steps(reset, lengths))), True
+
     def bwd(self, gate, value, states, dout, dgate, dvalue, dlast=None, dh0=None, reset=None, lengths=None, stream=None):
-        gp, gs = self._seq(gate, "gate")
-        vp, vs = self._seq(value, "value")
-        op, os_ = self._seq(dout, "dout")
-        dgp, dgs = self._seq(dgate, "dgate", True)
-        dvp, dvs = self._seq(dvalue, "dvalue", True)
-        kp, ep, hp = self._states(states), self._end(dlast, "dlast"), self._end(dh0, "dh0")
-        rp, rs, lp = self._steps(reset, lengths)
+        desc, at = self._bwd(self, gate, value, states, reset, lengths, dout, dlast, dgate, dvalue, dh0)
         raw = _raw_stream(stream, self.device)
         ws, n, _owner = self._ws[GC_OP_BWD].on(raw)
-        st = lib().gc_recurrence_bwd(gp, vp, kp, rp, lp, op, ep, dgp, dvp, hp, ws, n,
-                                     self._desc((gs, vs, os_, dgs, dvs, rs)), self.dt, raw)
+        st = lib().gc_recurrence_bwd(*at, ws, n, desc, self.dt, raw)
         _check("gc_recurrence_bwd", st)
         return dgate, dvalue, dh0
 
@@ -1045,42 +1080,47 @@ class Distill:
         self.row_shape = torch.Size((rows,))
         self._desc = _Descs(lambda itype, *ld: gc_distill_desc(rows, vocab, top, itype, tt, t, *ld))
 
-    def _row(self, t, name):
-        return None if t is None else _arg(t, name, torch.float32, self.row_shape, self.device)
+        self._fwd, self._bwd, self._step = (_Checked(f) for f in (Distill._check_fwd, Distill._check_bwd, Distill._check_step))
 
-    def _inputs(self, logits, index, teacher, dlogits=None):
-        """Addresses of logits, index, teacher and dlogits, and the call's descriptor."""
+    def _inputs(self, logits, index, teacher, dlogits, **rows):
+        """The call's descriptor, and whether it stands for tensors alike."""
         if index.dtype not in (torch.int32, torch.int64):
             raise TypeError(f"index has dtype {index.dtype}, expected int32 or int64")
-        lp, ld = _dense_rows(logits, "logits", self.dtype, self.shape, self.device)
-        ip, li = _dense_rows(index, "index", index.dtype, self.entry_shape, self.device)
-        tp, lt = _dense_rows(teacher, "teacher", self.teacher_dtype, self.entry_shape, self.device)
-        gp, lg = None, self.shape[1]
+        ld = _dense_rows(logits, "logits", self.dtype, self.shape, self.device)
+        li = _dense_rows(index, "index", index.dtype, self.entry_shape, self.device)
+        lt = _dense_rows(teacher, "teacher", self.teacher_dtype, self.entry_shape, self.device)
+        lg, same = self.shape[1], True
         if dlogits is not None:
-            gp, lg = _dense_rows(dlogits, "dlogits", self.dtype, self.shape, self.device)
-            if gp == lp and lg != ld:
-                raise ValueError("dlogits in place has to have the row distance of logits")
-        return lp, ip, tp, gp, self._desc((_INDEX_TYPES[index.dtype], ld, lg, li, lt))
+            lg = _dense_rows(dlogits, "dlogits", self.dtype, self.shape, self.device)
+            same = _in_place(dlogits, "dlogits", lg, (logits, ld))
+        for name, t in rows.items():
+            if t is not None:
+                _arg(t, name, torch.float32, self.row_shape, self.device)
+        return self._desc((_INDEX_TYPES[index.dtype], ld, lg, li, lt)), same
+
+    def _check_fwd(self, logits, index, teacher, loss, peak, mass):
+        return self._inputs(logits, index, teacher, None, loss=loss, peak=peak, mass=mass)
 
     def fwd(self, logits, index, teacher, loss, peak=None, mass=None, stream=None):
-        lp, ip, tp, _, desc = self._inputs(logits, index, teacher)
-        if loss is None:
-            raise ValueError("loss is not optional")
-        st = lib().gc_distill_fwd(lp, ip, tp, self._row(loss, "loss"), self._row(peak, "peak"), self._row(mass, "mass"),
-                                  desc, self.dt, _raw_stream(stream, self.device))
+        desc, at = self._fwd(self, logits, index, teacher, loss, peak, mass)
+        st = lib().gc_distill_fwd(*at, desc, self.dt, _raw_stream(stream, self.device))
         _check("gc_distill_fwd", st)
         return loss, peak, mass
 
+    def _check_bwd(self, logits, index, teacher, peak, mass, dloss, dlogits):
+        return self._inputs(logits, index, teacher, dlogits, peak=peak, mass=mass, dloss=dloss)
+
     def bwd(self, logits, index, teacher, peak, mass, dloss, dlogits, stream=None):
-        lp, ip, tp, gp, desc = self._inputs(logits, index, teacher, dlogits)
-        st = lib().gc_distill_bwd(lp, ip, tp, self._row(peak, "peak"), self._row(mass, "mass"), self._row(dloss, "dloss"), gp,
-                                  desc, self.dt, _raw_stream(stream, self.device))
+        desc, at = self._bwd(self, logits, index, teacher, peak, mass, dloss, dlogits)
+        st = lib().gc_distill_bwd(*at, desc, self.dt, _raw_stream(stream, self.device))
         _check("gc_distill_bwd", st)
         return dlogits
 
+    def _check_step(self, logits, index, teacher, dloss, loss, dlogits):
+        return self._inputs(logits, index, teacher, dlogits, dloss=dloss, loss=loss)
+
     def step(self, logits, index, teacher, dloss, loss, dlogits, stream=None):
-        lp, ip, tp, gp, desc = self._inputs(logits, index, teacher, dlogits)
-        st = lib().gc_distill_step(lp, ip, tp, self._row(dloss, "dloss"), self._row(loss, "loss"), gp, desc, self.dt,
-                                   _raw_stream(stream, self.device))
+        desc, at = self._step(self, logits, index, teacher, dloss, loss, dlogits)
+        st = lib().gc_distill_step(*at, desc, self.dt, _raw_stream(stream, self.device))
         _check("gc_distill_step", st)
         return loss, dlogits
