@@ -255,8 +255,8 @@ int gc_recurrence_plan_name(int op, const gc_recurrence_desc *d, int dtype, char
     ScanPlan q;
     if (!plan_scan(g, dtype, op == GC_OP_BWD, q)) snprintf(buf, buf_bytes, "none");
     else
-        snprintf(buf, buf_bytes, "scan_%s<N=%d> chunks=%d steps=%d lanes=%lld", op == GC_OP_BWD ? "bwd" : "fwd", q.N,
-                 q.chunks, q.len, (long long)q.lanes);
+        snprintf(buf, buf_bytes, "scan_%s<N=%d> chunks=%d steps=%d lanes=%lld past=%d far=%d",
+                 op == GC_OP_BWD ? "bwd" : "fwd", q.N, q.chunks, q.len, (long long)q.lanes, q.past, q.far);
     return GC_OK;
 }
 

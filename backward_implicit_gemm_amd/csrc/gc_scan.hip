@@ -551,8 +551,9 @@ bool plan_scan(const ScanGeom &g, int dtype, bool bwd, ScanPlan &q)
     q = ScanPlan{};
     if (int64_t(g.B) * g.D >= int64_t(1) << 31) return false;
     const int blocks = g.T ? (g.T - 1) / kBlock + 1 : 1, size = dtype == GC_F32 ? 4 : 2;
-    q.far = !near(g.gate, g, g.D, size) || !near(g.value, g, g.D, size) || !near(g.out, g, g.D, size);
-    if (bwd) q.far |= !near(g.dgate, g, g.D, size) || !near(g.dvalue, g, g.D, size);
+    const int least = vectors(g.D, 2);     // threads of a step's channels, at least
+    q.far = !near(g.gate, g, least, size) || !near(g.value, g, least, size) || !near(g.out, g, least, size);
+    if (bwd) q.far |= !near(g.dgate, g, least, size) || !near(g.dvalue, g, least, size);
     auto waves_of = [&](int n) { return (int64_t(g.B) * vectors(g.D, n) + 63) / 64; };
     auto chunks_of = [&](int64_t waves) -> int64_t {
         if (!waves || waves >= 512 || blocks < (bwd ? 10 : 15)) return 1;

@@ -395,7 +395,8 @@ int gc_recurrence_bwd(const void *gate, const void *value, const float *states, 
  * An entry whose index is outside [0, V) is empty, and an entry of p == 0 adds
  * nothing; several entries may have one index.  A row without any entry of a
  * teacher's logit above -inf has loss 0 and gradient 0, whatever its logits
- * hold.  A logit of -inf has q == 0 (its loss is infinite where p is not 0).
+ * hold.  A logit of -inf has q == 0 (its loss is infinite where p is not 0), in a
+ * row of nothing else as well.
  * The forward also writes peak, the largest logit, and mass, the sum of
  * exp((logits - peak) / t) (either may be NULL); the backward reads them.  dloss,
  * loss, peak and mass are fp32 [rows].  logits and dlogits have the storage
@@ -420,8 +421,8 @@ int gc_distill_bwd(const void *logits, const void *index, const void *teacher, c
 int gc_distill_step(const void *logits, const void *index, const void *teacher, const float *dloss, float *loss,
                     void *dlogits, const gc_distill_desc *d, int dtype, void *stream);
 
-/* Which kernels these would run (pure host, as gc_conv_plan_name): op is GC_OP_FWD
- * or GC_OP_BWD, for the distillation also GC_OP_STEP, both at once. */
+/* Which kernels these would run (pure host, as gc_conv_plan_name): op is GC_OP_FWD or GC_OP_BWD
+ * (the layer norm's without a residual, or a gradient past it), for the distillation also GC_OP_STEP, both at once. */
 enum { GC_OP_STEP = 6 };
 int gc_layer_norm_plan_name(int op, const gc_layer_norm_desc *d, int dtype, char *buf, size_t buf_bytes);
 int gc_recurrence_plan_name(int op, const gc_recurrence_desc *d, int dtype, char *buf, size_t buf_bytes);
