@@ -387,7 +387,9 @@ void plan_distill(const DistillGeom &g, int dtype, int op, DistillPlan &q)
     const int vec = dtype == GC_F32 ? 4 : 8;
     q.N = g.V < vec ? 1 : vec;
     const int64_t nv = vectors(g.V, q.N);
-    // the fewest threads whose registers hold the row, then more while the chip has room for them
+    // The fewest threads whose registers hold the row, so that several rows are at work on a CU and hide each
+    // other's waits (steps of 4096 x 40,960 bf16: 256 threads a row 157 us, 512 161, 1024 199), then
+    // more while the chip has room for them (512 x 8000: 256 threads 14 us, 64 18).
     const int most = g.V <= 64 * 64 ? 64 / vec : 20;
     q.L = 8;
     while (q.L < 1024 && int64_t(q.L) * most < nv) q.L *= 2;

@@ -8,8 +8,14 @@
 // Memory bound: a row is read once into the registers of a team of threads, which adds up
 // its sums by lane exchanges (a team of one wave) or through LDS, and writes its outputs.  Teams
 // walk rows, so gamma and beta are read once a team, and the backward's sums over rows
-// stay in registers until a team's last row.  Rows past a workgroup's registers are
-// walked in several passes.
+// stay in registers until a team's last row; its next row's loads fly while a row is
+// worked on.  A second launch adds up the workgroups' sums.  Rows past a workgroup's
+// registers (16,384 values forward, 8192 backward) are walked in several passes.
+//
+// 32,768 rows of 1760 bf16 with a residual: 74 us forward (461 MB, 6.2 TB/s).  8191 rows of 4096 bf16,
+// with the stream's gradient: 57 us backward and 5 for the sums (268 MB; 82 in all without the loads ahead
+// and with the sums of 512 teams joined one by one).  1024 rows of 1760 fp32: 10.4 and 3.4 us, the
+// latency of a row's loads, its sums, and the join.
 #include <algorithm>
 #include <type_traits>
 
@@ -479,7 +485,9 @@ void plan_rows(const RowsGeom &g, int dtype, bool bwd, bool more, RowsPlan &q)
         q.grid = std::min<int64_t>(rows, 4 * kCUs);
         q.parts = std::min<int64_t>(rows, 64);
     } else {
-        // the smallest team that holds a row; while there are fewer teams than the chip takes, twice the threads
+        // The smallest team that holds a row; while there are fewer teams than the chip takes, twice the threads.
+        // The backward's workgroups are one a CU: with two, twice the rows of partial sums cost more than the
+        // overlap gains (8191 x 4096 bf16 69 us against 61).
         q.L = 1;
         while (int64_t(q.L) * most < nv) q.L *= 2;
         while (q.L < threads && q.L < nv && rows * q.L < 1024 * kCUs / 4) q.L *= 2;
