@@ -812,6 +812,15 @@ def gc_distill_plan_name(op, desc, dtype):
     return _plan_name("gc_distill_plan_name", op, desc, dtype)
 
 
+def _launch(device, fn, *args):
+    """Calls a C entry point with the tensors' device as the current one: a launch on a default stream
+    goes to the current device."""
+    if torch._C._cuda_getDevice() == device.index:
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
 class _Descs:
     """A helper's descriptors by the distances they were made for."""
 
@@ -939,7 +948,7 @@ class LayerNorm:
 
     def fwd(self, x, gamma, beta, y, mean=None, rstd=None, residual=None, total=None, stream=None):
         desc, at = self._fwd(self, x, residual, gamma, beta, y, total, mean, rstd)
-        st = lib().gc_layer_norm_fwd(*at, desc, self.dt, self.pt, _raw_stream(stream, self.device))
+        st = _launch(self.device, lib().gc_layer_norm_fwd, *at, desc, self.dt, self.pt, _raw_stream(stream, self.device))
         _check("gc_layer_norm_fwd", st)
         return y, mean, rstd, total
 
@@ -954,7 +963,7 @@ class LayerNorm:
         desc, at = self._bwd(self, x, gamma, dy, dtotal, mean, rstd, dx, dgamma, dbeta)
         raw = _raw_stream(stream, self.device)
         ws, n, _owner = self._ws.on(raw)
-        st = lib().gc_layer_norm_bwd(*at, ws, n, desc, self.dt, self.pt, raw)
+        st = _launch(self.device, lib().gc_layer_norm_bwd, *at, ws, n, desc, self.dt, self.pt, raw)
         _check("gc_layer_norm_bwd", st)
         return dx, dgamma, dbeta
 
@@ -1037,7 +1046,7 @@ class Recurrence:
         desc, at = self._fwd(self, gate, value, h0, reset, lengths, out, last, states)
         raw = _raw_stream(stream, self.device)
         ws, n, _owner = self._ws[GC_OP_FWD].on(raw)
-        st = lib().gc_recurrence_fwd(*at, ws, n, desc, self.dt, raw)
+        st = _launch(self.device, lib().gc_recurrence_fwd, *at, ws, n, desc, self.dt, raw)
         _check("gc_recurrence_fwd", st)
         return out, last
 
@@ -1051,7 +1060,7 @@ class Recurrence:
         desc, at = self._bwd(self, gate, value, states, reset, lengths, dout, dlast, dgate, dvalue, dh0)
         raw = _raw_stream(stream, self.device)
         ws, n, _owner = self._ws[GC_OP_BWD].on(raw)
-        st = lib().gc_recurrence_bwd(*at, ws, n, desc, self.dt, raw)
+        st = _launch(self.device, lib().gc_recurrence_bwd, *at, ws, n, desc, self.dt, raw)
         _check("gc_recurrence_bwd", st)
         return dgate, dvalue, dh0
 
@@ -1073,8 +1082,8 @@ class Distill:
         rows, vocab = _extent(rows, "rows", 0, _INT_MAX), _extent(vocab, "vocab", 1, _INT_MAX)
         top = _extent(top, "top", 1, 1024)
         t = ctypes.c_float(float(temperature)).value
-        if not 0 < t < math.inf:
-            raise ValueError(f"the temperature has to be positive and finite in fp32, not {temperature}")
+        if not 1e-18 <= t <= 1e18:
+            raise ValueError(f"the temperature has to be from 1e-18 to 1e18, not {temperature}")
         self.temperature, self.device = t, _device(device)
         self.shape, self.entry_shape = torch.Size((rows, vocab)), torch.Size((rows, top))
         self.row_shape = torch.Size((rows,))
@@ -1103,7 +1112,7 @@ class Distill:
 
     def fwd(self, logits, index, teacher, loss, peak=None, mass=None, stream=None):
         desc, at = self._fwd(self, logits, index, teacher, loss, peak, mass)
-        st = lib().gc_distill_fwd(*at, desc, self.dt, _raw_stream(stream, self.device))
+        st = _launch(self.device, lib().gc_distill_fwd, *at, desc, self.dt, _raw_stream(stream, self.device))
         _check("gc_distill_fwd", st)
         return loss, peak, mass
 
@@ -1112,7 +1121,7 @@ class Distill:
 
     def bwd(self, logits, index, teacher, peak, mass, dloss, dlogits, stream=None):
         desc, at = self._bwd(self, logits, index, teacher, peak, mass, dloss, dlogits)
-        st = lib().gc_distill_bwd(*at, desc, self.dt, _raw_stream(stream, self.device))
+        st = _launch(self.device, lib().gc_distill_bwd, *at, desc, self.dt, _raw_stream(stream, self.device))
         _check("gc_distill_bwd", st)
         return dlogits
 
@@ -1121,6 +1130,6 @@ class Distill:
 
     def step(self, logits, index, teacher, dloss, loss, dlogits, stream=None):
         desc, at = self._step(self, logits, index, teacher, dloss, loss, dlogits)
-        st = lib().gc_distill_step(*at, desc, self.dt, _raw_stream(stream, self.device))
+        st = _launch(self.device, lib().gc_distill_step, *at, desc, self.dt, _raw_stream(stream, self.device))
         _check("gc_distill_step", st)
         return loss, dlogits

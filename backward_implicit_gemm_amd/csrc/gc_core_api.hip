@@ -88,7 +88,8 @@ int check_distill(const gc_distill_desc *d, DistillGeom &g)
 {
     if (!d || d->rows < 0 || d->rows > INT_MAX || d->V < 1 || d->K < 1 || d->K > kMostTop) return GC_ERR_INVALID_ARG;
     if ((d->itype != GC_I32 && d->itype != GC_I64) || !valid_dtype(d->teacher_dtype)) return GC_ERR_INVALID_ARG;
-    if (!(d->temperature > 0.f) || isinf(d->temperature)) return GC_ERR_INVALID_ARG;
+    // its square and the reciprocal stay normal numbers
+    if (!(d->temperature >= 1e-18f && d->temperature <= 1e18f)) return GC_ERR_INVALID_ARG;
     if (d->ld < d->V || d->ld_grad < d->V || d->ld_index < d->K || d->ld_teacher < d->K) return GC_ERR_INVALID_ARG;
     for (const int64_t ld : {d->ld, d->ld_grad, d->ld_index, d->ld_teacher})
         if (!in_reach(d->rows, ld)) return GC_ERR_INVALID_ARG;

@@ -73,7 +73,8 @@ __device__ __forceinline__ void params_at(const RowsGeom &g, const void *p, int 
 }
 
 // Sums over the L threads of a team, the same value for all: lanes of a wave, or whole
-// waves of a workgroup that may hold several such teams (`red` 16*K values).
+// waves of a workgroup that may hold several such teams (`red` 16*K values, which the next call must
+// not use: it may begin before all have read them).
 template <int K>
 __device__ __forceinline__ void rows_sum(float (&v)[K], int L, float *red)
 {
@@ -82,7 +83,6 @@ __device__ __forceinline__ void rows_sum(float (&v)[K], int L, float *red)
     for (int k = 0; k < K; ++k) v[k] = lanes_sum(v[k], w);
     if (L <= 64) return;
     const int wave = threadIdx.x >> 6, nw = L >> 6, first = wave & ~(nw - 1);
-    __syncthreads();
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
         for (int k = 0; k < K; ++k) red[k * 16 + wave] = v[k];
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(512) rows_fwd(RowsGeom g, int L, const T *x, c
                                                  const void *__restrict__ gamma, const void *__restrict__ beta,
                                                  T *y, T *total, float *__restrict__ mean, float *__restrict__ rstd)
 {
-    __shared__ float red[16];
+    __shared__ float red[2][16];
     const int tt = threadIdx.x & (L - 1), teams = blockDim.x / L;
     float gm[NV][N], bt[NV][N];
 #pragma unroll
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(512) rows_fwd(RowsGeom g, int L, const T *x, c
                 sum[0] += j >= at.skip ? v[i][j] : 0.f;
             }
         }
-        rows_sum<1>(sum, L, red);
+        rows_sum<1>(sum, L, red[0]);
         const float m = sum[0] * inv;
         float sq[1] = {0.f};
 #pragma unroll
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(512) rows_fwd(RowsGeom g, int L, const T *x, c
                 sq[0] += j >= at.skip ? off * off : 0.f;
             }
         }
-        rows_sum<1>(sq, L, red);
+        rows_sum<1>(sq, L, red[1]);
         const float r = 1.f / sqrtf(sq[0] * inv + g.eps);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(512) rows_bwd(RowsGeom g, int L, const T *x, c
                                                 const T *dy, const T *dtotal, const float *__restrict__ mean,
                                                 const float *__restrict__ rstd, T *dx, float *__restrict__ part)
 {
-    __shared__ float red[32];
+    __shared__ float red[2][32];
     extern __shared__ float joined[];
     const int tt = threadIdx.x & (L - 1), teams = blockDim.x / L, team = threadIdx.x / L;
     // every team of a workgroup takes as many turns, for the barriers; one without a row reads the last again
@@ -311,7 +311,8 @@ __global__ void __launch_bounds__(512) rows_bwd(RowsGeom g, int L, const T *x, c
         params_at<T, N>(g, gamma, at.at, 1.f, gm[i]);
     }
     const float inv = 1.f / float(g.D);
-    for (int64_t turn = first; turn < g.rows; turn += stride) {
+    int half = 0;
+    for (int64_t turn = first; turn < g.rows; turn += stride, half ^= 1) {
         const bool own = turn + team < g.rows;
         const int64_t row = row_of(turn);
         const RowIn<T, N, NV> in = next;
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(512) rows_bwd(RowsGeom g, int L, const T *x, c
                 c[1] += gm[i][j] * dh;
             }
         }
-        rows_sum<2>(c, L, red);
+        rows_sum<2>(c, L, red[half]);
         const float c1 = c[0] * inv, c2 = c[1] * inv;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -436,6 +437,7 @@ __global__ void __launch_bounds__(1024) rows_bwd_loop(RowsGeom g, const T *x, co
             }
         }
         rows_sum<2>(c, 1024, red);
+        __syncthreads();
         const float c1 = c[0] * inv, c2 = c[1] * inv;
         for (int i = threadIdx.x; i < nv; i += blockDim.x) {
             const Place<N> at(i, g.D);

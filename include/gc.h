@@ -408,7 +408,7 @@ typedef struct {
     int V, K;
     int itype;              /* GC_I32 or GC_I64 */
     int teacher_dtype;      /* gc_dtype of teacher */
-    float temperature;      /* > 0, finite */
+    float temperature;      /* from 1e-18 to 1e18 */
     int64_t ld, ld_grad, ld_index, ld_teacher;
 } gc_distill_desc;
 

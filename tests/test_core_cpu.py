@@ -141,7 +141,7 @@ def distill_calls(d, dtype=0, **p):
 
 @pytest.mark.parametrize("change", [
     dict(rows=-1), dict(rows=1 << 31), dict(V=0), dict(K=0), dict(K=1025, ld_index=1025, ld_teacher=1025), dict(itype=gb.GC_U8),
-    dict(itype=-1), dict(teacher=2), dict(t=0.0), dict(t=-1.0), dict(t=NAN), dict(t=INF), dict(ld=29), dict(ld_grad=29),
+    dict(itype=-1), dict(teacher=2), dict(t=0.0), dict(t=-1.0), dict(t=NAN), dict(t=INF), dict(t=9e-19), dict(t=1.1e18), dict(ld=29), dict(ld_grad=29),
     dict(ld_index=3), dict(ld_teacher=3), dict(ld=1 << 59),
 ])
 def test_distill_descriptors(change):
@@ -220,11 +220,32 @@ def test_binding_distill_refusals():
     for args in ((-1, 9, 2), (3, 0, 2), (3, 9, 0), (3, 9, 1025), (1 << 31, 9, 2)):
         with pytest.raises(ValueError):
             gb.Distill(*args, torch.float32, device="cpu")
-    for t in (0.0, -1.0, NAN, INF, 1e-60, 1e60):
+    for t in (0.0, -1.0, NAN, INF, 1e-60, 1e60, 9e-19, 1.1e18):
         with pytest.raises(ValueError, match="temperature"):
             gb.Distill(3, 9, 2, torch.float32, t, device="cpu")
     with pytest.raises(TypeError, match="unsupported dtype"):
         gb.Distill(3, 9, 2, torch.float32, teacher_dtype=torch.float16, device="cpu")
+
+
+def test_launches_go_to_the_tensors_device(monkeypatch):
+    """With another device current, the call is made with the helper's, which is put back."""
+    current = [0]
+
+    class Switch:
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            self.was, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.was
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Switch)
+    for index in (0, 1):
+        assert gb._launch(torch.device("cuda", index), lambda a: (a, current[0]), 7) == (7, index)
+        assert current[0] == 0
 
 
 # ------------------------------------------------------------------- the plans --
