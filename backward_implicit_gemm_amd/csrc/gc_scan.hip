@@ -586,8 +586,10 @@ bool plan_scan(const ScanGeom &g, int dtype, bool bwd, ScanPlan &q)
     const int per = int((blocks + chunks - 1) / chunks);
     q.len = int(std::min<int64_t>(int64_t(per) * kBlock, 1 << 30));
     q.chunks = (blocks + per - 1) / per;
-    q.part_bytes = q.chunks > 1 ? (size_t(q.chunks) * g.B * g.D * 4 + 255) & ~size_t(255) : 0;
-    q.ws_bytes = 2 * q.part_bytes;
+    auto bytes_of = [&](int64_t n) { return n > 1 ? (size_t(n) * g.B * g.D * 4 + 255) & ~size_t(255) : 0; };
+    q.part_bytes = bytes_of(q.chunks);
+    // room for the most chunks that any distances lead to
+    q.ws_bytes = 2 * bytes_of(std::max(chunks_of(waves_of(1)), bwd && dtype == GC_BF16 ? chunks_of(waves_of(2)) : int64_t(1)));
     // Outputs of large calls go past the cache (512 x 64 x 512 fp32 backward 74 us without, 53 with), but not where
     // rows share words of memory, which would be written in halves (3 x 12,001 x 777 bf16 69 without, 79 with).
     auto words = [&](const gc_strides &s) { return s.step * size % 4 == 0 && (g.B == 1 || s.batch * size % 4 == 0); };

@@ -285,3 +285,16 @@ def test_plan_name_errors():
                     (gb.GC_OP_FWD, ctypes.byref(d), 4, buf, 8), (gb.GC_OP_FWD, ctypes.byref(d), 0, None, 8),
                     (gb.GC_OP_FWD, ctypes.byref(d), 0, buf, 0)):
             assert fn(*bad) == BAD
+
+
+def test_recurrence_workspace_does_not_depend_on_distances():
+    """A helper's workspace serves every layout its calls bring, sequences 4 GiB apart among them."""
+    L = gb.lib()
+    for dtype in (gb.GC_F32, gb.GC_BF16):
+        for op in (gb.GC_OP_FWD, gb.GC_OP_BWD):
+            for B, T, D in ((3, 300000, 10), (40, 1000, 33), (7, 12001, 777), (20, 300, 300), (1, 5000, 4096)):
+                sizes = set()
+                for batch, step in ((T * D, D), (D, B * D), (1 << 32, D), (D, 1 << 28), (1 << 40, 2 * D)):
+                    d = scan_desc(B, T, D, **{k: (batch, step) for k in DENSE})
+                    sizes.add(L.gc_recurrence_workspace_bytes(op, ctypes.byref(d), dtype))
+                assert len(sizes) == 1 and min(sizes) > 0, (B, T, D, sizes)
