@@ -13,7 +13,7 @@
 // registers (16,384 values forward, 8192 backward) are walked in several passes.
 //
 // 32,768 rows of 1760 bf16 with a residual: 74 us forward (461 MB, 6.2 TB/s).  8191 rows of 4096 bf16,
-// with the stream's gradient: 57 us backward and 5 for the sums (268 MB; 82 in all without the loads ahead
+// with the stream's gradient: 53 us backward and 5 for the sums (268 MB; 82 in all without the loads ahead
 // and with the sums of 512 teams joined one by one).  1024 rows of 1760 fp32: 10.4 and 3.4 us, the
 // latency of a row's loads, its sums, and the join.
 #include <algorithm>
@@ -279,7 +279,8 @@ struct RowIn {
     float mean, rstd;
 };
 
-template <typename T, int N, int NV, bool PAST>
+// AHEAD rows' loads fly while one is worked on.
+template <typename T, int N, int NV, int AHEAD, bool PAST>
 __global__ void __launch_bounds__(512) rows_bwd(RowsGeom g, int L, const T *x, const void *__restrict__ gamma,
                                                 const T *dy, const T *dtotal, const float *__restrict__ mean,
                                                 const float *__restrict__ rstd, T *dx, float *__restrict__ part)
@@ -303,7 +304,10 @@ __global__ void __launch_bounds__(512) rows_bwd(RowsGeom g, int L, const T *x, c
         return in;
     };
     const int64_t stride = int64_t(gridDim.x) * teams, first = int64_t(blockIdx.x) * teams;
-    RowIn<T, N, NV> next = fetch(row_of(first));
+    RowIn<T, N, NV> next[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+        if (first + k * stride < g.rows) next[k] = fetch(row_of(first + k * stride));
     float gm[NV][N], dg[NV][N] = {}, db[NV][N] = {};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -315,8 +319,10 @@ __global__ void __launch_bounds__(512) rows_bwd(RowsGeom g, int L, const T *x, c
     for (int64_t turn = first; turn < g.rows; turn += stride, half ^= 1) {
         const bool own = turn + team < g.rows;
         const int64_t row = row_of(turn);
-        const RowIn<T, N, NV> in = next;
-        if (turn + stride < g.rows) next = fetch(row_of(turn + stride));     // flies while this row is worked on
+        const RowIn<T, N, NV> in = next[0];
+#pragma unroll
+        for (int k = 1; k < AHEAD; ++k) next[k - 1] = next[k];
+        if (turn + AHEAD * stride < g.rows) next[AHEAD - 1] = fetch(row_of(turn + AHEAD * stride));
         float c[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -553,12 +559,19 @@ hipError_t launch_rows_bwd(const RowsGeom &g, const RowsPlan &q, const void *x, 
         } else {
             e = with_vectors<T, kBwdHeld>(q, [&](auto n, auto nv) {
                 constexpr int N = decltype(n)::value, NV = decltype(nv)::value;
-                return with_past<(N > 1)>(q.past, [&](auto past) {
-                    hipLaunchKernelGGL((rows_bwd<T, N, NV, decltype(past)::value>), dim3(unsigned(q.grid)),
-                                       dim3(q.threads), q.lds_bytes, s, g, q.L, xt, gamma, dt, tt, mean, rstd, out,
-                                       sums ? part : nullptr);
-                    return hipGetLastError();
-                });
+                auto go = [&](auto ahead) {
+                    return with_past<(N > 1)>(q.past, [&](auto past) {
+                        hipLaunchKernelGGL((rows_bwd<T, N, NV, decltype(ahead)::value, decltype(past)::value>),
+                                           dim3(unsigned(q.grid)), dim3(q.threads), q.lds_bytes, s, g, q.L, xt, gamma, dt, tt,
+                                           mean, rstd, out, sums ? part : nullptr);
+                        return hipGetLastError();
+                    });
+                };
+                // Two rows ahead where registers allow it and teams of several waves wait for each other: 8191 x 4096
+                // bf16 57.4 us, with one 59.6; teams within a wave lose by it (65,536 x 256 29.9 and 28.1).
+                if constexpr (NV * N * sizeof(T) == 32 && N > 1)
+                    if (q.L > 64) return go(std::integral_constant<int, 2>());
+                return go(std::integral_constant<int, 1>());
             });
         }
         if (e != hipSuccess) return e;
