@@ -50,14 +50,14 @@ struct ScanGeom {
 struct ScanPlan {
     int N;              // channels of a thread
     int nv;             // threads of a step's channels
-    int64_t lanes;      // B * nv
+    int64_t lanes;      // of all sequences
     int past;           // the outputs go past the cache
     int far;            // lanes of a wave may be 4 GiB apart and more
     int chunks, len;    // pieces the steps are cut into, and their length (a multiple of the block)
     size_t part_bytes, ws_bytes;
     FastDiv fd_nv, fd_blocks;
 };
-bool plan_scan(const ScanGeom &g, int dtype, bool bwd, ScanPlan &q);
+bool plan_scan(const ScanGeom &g, int dtype, bool bwd, bool ragged, ScanPlan &q);
 template <typename T>
 hipError_t launch_scan_fwd(const ScanGeom &g, const ScanPlan &q, const void *gate, const void *value, const float *h0,
                            const uint8_t *reset, const int32_t *lengths, void *out, float *last, float *states,

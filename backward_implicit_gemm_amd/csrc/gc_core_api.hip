@@ -197,7 +197,7 @@ size_t gc_recurrence_workspace_bytes(int op, const gc_recurrence_desc *d, int dt
     ScanGeom g;
     ScanPlan q;
     if ((op != GC_OP_FWD && op != GC_OP_BWD) || !valid_dtype(dtype)) return 0;
-    return check_scan(d, op == GC_OP_BWD, g) == GC_OK && plan_scan(g, dtype, op == GC_OP_BWD, q) ? q.ws_bytes : 0;
+    return check_scan(d, op == GC_OP_BWD, g) == GC_OK && plan_scan(g, dtype, op == GC_OP_BWD, false, q) ? q.ws_bytes : 0;
 }
 
 int gc_recurrence_fwd(const void *gate, const void *value, const float *h0, const uint8_t *reset, const int32_t *lengths,
@@ -213,7 +213,7 @@ int gc_recurrence_fwd(const void *gate, const void *value, const float *h0, cons
         for (const void *p : {gate, value, static_cast<const void *>(out)})
             if (!given(p, size_of(dtype))) return GC_ERR_INVALID_ARG;
     ScanPlan q;
-    if (!plan_scan(g, dtype, false, q)) return GC_ERR_UNSUPPORTED;
+    if (!plan_scan(g, dtype, false, lengths, q)) return GC_ERR_UNSUPPORTED;
     st = check_workspace(workspace, ws_bytes, q.ws_bytes);
     if (st != GC_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -237,7 +237,7 @@ int gc_recurrence_bwd(const void *gate, const void *value, const float *states, 
         if (!given(states, 4)) return GC_ERR_INVALID_ARG;
     }
     ScanPlan q;
-    if (!plan_scan(g, dtype, true, q)) return GC_ERR_UNSUPPORTED;
+    if (!plan_scan(g, dtype, true, lengths, q)) return GC_ERR_UNSUPPORTED;
     st = check_workspace(workspace, ws_bytes, q.ws_bytes);
     if (st != GC_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -254,7 +254,7 @@ int gc_recurrence_plan_name(int op, const gc_recurrence_desc *d, int dtype, char
     const int st = check_scan(d, op == GC_OP_BWD, g);
     if (st != GC_OK) return st;
     ScanPlan q;
-    if (!plan_scan(g, dtype, op == GC_OP_BWD, q)) snprintf(buf, buf_bytes, "none");
+    if (!plan_scan(g, dtype, op == GC_OP_BWD, false, q)) snprintf(buf, buf_bytes, "none");
     else
         snprintf(buf, buf_bytes, "scan_%s<N=%d> chunks=%d steps=%d lanes=%lld past=%d far=%d",
                  op == GC_OP_BWD ? "bwd" : "fwd", q.N, q.chunks, q.len, (long long)q.lanes, q.past, q.far);

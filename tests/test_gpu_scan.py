@@ -116,6 +116,14 @@ def test_resets_and_lengths(coupled, t):
     check(3, 3000, 21, t, coupled, reset=0.3, lengths=[2999, 64, 2048])
 
 
+@pytest.mark.parametrize("t", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("D", [63, 64, 65, 129, 130, 200])
+def test_lengths_around_a_wave(D, t):
+    """Channels that leave a wave partly empty or nearly so, sequences that end in different chunks."""
+    check(4, 700, D, t, lengths=[700, 333, 0, 16], reset=0.01)
+    check(4, 90, D, t, lengths=[90, 33, 64, 1], layout="tb")
+
+
 def test_lengths_outside_the_steps_are_taken_into_them():
     B, T, D = 4, 20, 6
     p = problem(B, T, D, F32)
