@@ -45,6 +45,12 @@ __host__ __device__ __forceinline__ int entry_bytes(int K, int lists)
 
 constexpr int kOwn = 2;   // entries of a lane that stay in registers
 
+// The backward, which meets a row's logits once, walks longer bf16 rows: its few registers leave room for
+// more waves (512 x 150,000 69 us, with the row held 74; 4096 x 40,960 with 256 entries 156 and 158;
+// from the cache 2048 x 40,961 60 and 67).  In fp32 it loses (4096 x 32,000 202 and 193).
+template <typename T>
+constexpr int kMostBwd = sizeof(T) == 2 ? 8 : 20;   // vectors that a thread of the backward holds
+
 template <typename V, typename F>
 __device__ __forceinline__ V lanes_fold(V v, int width, F f)
 {
@@ -409,12 +415,18 @@ void plan_distill(const DistillGeom &g, int dtype, int op, DistillPlan &q)
         q.NV = int(std::min<int64_t>(21, (nv + q.L - 1) / q.L));
         const int sizes[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20};
         const int *next = std::lower_bound(std::begin(sizes), std::end(sizes), q.NV);
-        q.NV = next == std::end(sizes) ? 0 : *next;
+        const int held = op != GC_OP_BWD ? 20 : dtype == GC_F32 ? kMostBwd<float> : kMostBwd<bf16_t>;
+        q.NV = next == std::end(sizes) || *next > held ? 0 : *next;
     }
     const int teams = q.threads / q.L;
     q.grid = (g.rows + teams - 1) / teams;
     q.lds_bytes = op == GC_OP_FWD ? 0 : size_t(teams) * entry_bytes(g.K, q.lists);
-    q.past = op != GC_OP_FWD && q.N > 1 && size_t(g.rows) * g.V * (dtype == GC_F32 ? 8 : 4) >= kStreamBytes;
+    // Large gradients go past the cache; the backward's do not where rows share 16 bytes of memory, which would be
+    // written in parts (4096 x 50,257 bf16 193 us past, 184 not, 4096 x 40,960 156 and 160; a step of 2048 x 40,961
+    // fp32 157 past and 166 not).
+    const int size = dtype == GC_F32 ? 4 : 2;
+    q.past = op != GC_OP_FWD && q.N > 1 && size_t(g.rows) * g.V * 2 * size >= kStreamBytes &&
+             (op == GC_OP_STEP || g.ld_grad * size % 16 == 0);
 }
 
 template <typename T>
@@ -442,7 +454,9 @@ hipError_t launch_distill(const DistillGeom &g, const DistillPlan &q, int op, co
         } else {
             return with_held(q.NV, [&](auto nv) {
                 return with_past<true>(q.past, [&](auto past) {
-                    return op == GC_OP_BWD ? go(n, nv, Bwd(), past) : go(n, nv, Step(), past);
+                    if (op != GC_OP_BWD) return go(n, nv, Step(), past);
+                    if constexpr (decltype(nv)::value <= kMostBwd<T>) return go(n, nv, Bwd(), past);
+                    return hipErrorInvalidValue;
                 });
             });
         }

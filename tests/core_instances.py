@@ -51,6 +51,8 @@ def scan(rng):
 
 def distill(rng):
     V, K = spread(rng, 1, 200000), spread(rng, 1, 300)
+    if rng.random() < 0.5:
+        V = -(-V // 8) * 8      # the backward's stores depend on it
     shape = count(rng, V), V, K
     dtype, op = rng.choice(DTYPES), rng.choice((gb.GC_OP_FWD, gb.GC_OP_BWD, gb.GC_OP_STEP))
     name = gb.gc_distill_plan_name(op, gb.gc_distill_desc(*shape, 0, 0, 1.0, V, V, K, K), dtype)
@@ -58,7 +60,7 @@ def distill(rng):
             _number(name, "past")), (op, dtype, *shape), shape[0] * V
 
 
-def instances(seed=0, draws=20000):
+def instances(seed=0, draws=60000):
     """{instance: shape}, the smallest shape found."""
     rng, found = random.Random(seed), {}
     for i in range(draws):
