@@ -1,18 +1,20 @@
 // gc_scan.hip -- the gated linear recurrence, forward and backward.
 //
-//   a = sigmoid(gate),  i = 1 - a,  h_t = h' + i * (value - h')  (coupled),  h_t = h' - i*h' + value  (not),
+//   a = sigmoid(gate),  i = 1 - a,  h_t = a*h' + i*value  (coupled),  h_t = a*h' + value  (not),
 //   h' = reset ? 0 : h_{t-1};
 //   g_t = dout_t + what comes back from step t+1,  dvalue = i*g (g),  dgate = a*i*(h' - value)*g (a*i*h'*g),
-//   back to step t-1: reset ? 0 : g - i*g
+//   back to step t-1: reset ? 0 : a*g
 //
-// With i as the small share, a state that keeps for thousands of steps is not worn off by the
-// rounding of a next to 1.  Everything is fp32; outputs are rounded once.
+// Only the smaller of a and i is a factor, s; the larger one is what it leaves: (1 - s)*x = x - s*x.  A state
+// that keeps for thousands of steps is not worn off by the rounding of a next to 1, and a gate that closes
+// leaves the value, or a share of 1e-9 of the state, right in its own size.  Everything is fp32; outputs
+// are rounded once.
 //
 // Memory bound: three tensors forward, five backward, and the fp32 states (an eighth of a bf16 tensor).
 // A thread walks the steps of one channel (backward of bf16: two where there are enough), eight
 // or sixteen steps at a time, the loads of the next ones in flight; scalar bases and 32-bit lane offsets
 // leave the vector unit to the gates.  A step costs a wave about 60 ns, mostly the exponential, the
-// reciprocal and ten more instructions, so a walk wants several waves on each of the 1024 SIMDs.  The
+// reciprocal and fifteen more instructions, so a walk wants several waves on each of the 1024 SIMDs.  The
 // backward takes blocks from the last to the first, each from the state that the forward kept
 // before it, so h needs no tensor of its own.
 //
@@ -22,6 +24,7 @@
 // (105 MB, 5.1 TB/s) and fp32 53 backward (352 MB, 6.6 TB/s); one of 32,768 x 1024 bf16 takes 61
 // (fold 23 at 5.8 TB/s, carry 5, walk 34), and 2.1 ms if it is walked as a whole.
 #include <algorithm>
+#include <float.h>
 #include <type_traits>
 
 #include "gc_core.h"
@@ -32,6 +35,8 @@ namespace {
 
 constexpr int kBlock = GC_RECURRENCE_BLOCK;
 constexpr int kHalf = kBlock / 2;
+constexpr float kLog2e = 1.44269504088896f;
+constexpr float kLeast = 1.4e-45f;     // the smallest number above 0
 
 // Where a thread works: sequence b, channels d .. d+N-1, of which the first `skip` belong to
 // the thread before it (the last vector of an odd row is moved back), steps [t0, t1) of chunk c.
@@ -155,20 +160,36 @@ struct Resets {
     }
 };
 
-// a = sigmoid(f) and i = 1 - a, each to fp32 accuracy: e = exp(-f), a = 1/(1+e), i = e*a.  Below -80
-// e would overflow; a is then below 2e-35 instead of smaller, NaN stays NaN.
-__device__ __forceinline__ void gates(float f, float &a, float &i)
+// A step's gate: whether it is open, SCALE (1 or 2) times its smaller share, which is then i and else a, and the
+// larger one.  With e = exp(-|f|) nothing overflows.  e is off by up to 1.5|f| + 3 half steps of fp32, as
+// exp2 of a rounded product, the smaller share by 5 more, the larger one by 3; shares below 1e-38 may be 0.
+template <int SCALE = 1>
+struct Gate {
+    float small, large;
+    bool open;
+    __device__ __forceinline__ explicit Gate(float f)
+    {
+        const float e = __builtin_amdgcn_exp2f(fmaf(fabsf(f), -kLog2e, SCALE - 1.f));
+        large = __builtin_amdgcn_rcpf(fmaf(e, 1.f / SCALE, 1.f));
+        small = e * large;
+        open = f >= 0.f;
+    }
+};
+
+// (1 - s)*x.  An infinite x meets the largest finite number of its sign, so that it stays and does not become
+// NaN.  (NaN becomes a number there, and is NaN in the difference.)
+__device__ __forceinline__ float rest(float s, float x)
 {
-    const float e = __expf(-(f < -80.f ? -80.f : f));
-    a = __builtin_amdgcn_rcpf(1.f + e);
-    i = e * a;
+    return fmaf(-s, __builtin_amdgcn_fmed3f(x, -FLT_MAX, FLT_MAX), x);
 }
 
-// One step of the state; i is 1 - a.
+// One step of the state.  In two products, not one with the difference of state and value, which overflows for
+// large ones and is NaN for infinite ones.
 template <bool COUPLED>
-__device__ __forceinline__ float advance(float before, float i, float v)
+__device__ __forceinline__ float advance(float before, const Gate<> &k, float v)
 {
-    return COUPLED ? fmaf(i, v - before, before) : fmaf(-i, before, before) + v;
+    if (!COUPLED) return (k.open ? rest(k.small, before) : k.small * before) + v;
+    return fmaf(k.small, k.open ? v : before, rest(k.small, k.open ? before : v));
 }
 
 // ----------------------------------------------------------------- forward --
@@ -247,9 +268,7 @@ __global__ void __launch_bounds__(64) scan_fwd(ScanGeom g, ScanPlan q, const T *
                 if (FULL || u < n) {
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
-                        float a, i;
-                        gates(f[u].get(j), a, i);
-                        h[j] = advance<COUPLED>(cut ? 0.f : h[j], i, v[u].get(j));
+                        h[j] = advance<COUPLED>(cut ? 0.f : h[j], Gate<>(f[u].get(j)), v[u].get(j));
                         y[j] = h[j];
                     }
                 }
@@ -266,7 +285,38 @@ __global__ void __launch_bounds__(64) scan_fwd(ScanGeom g, ScanPlan q, const T *
 }
 
 // A chunk as a step of its own: the product of its a (-1 where a reset cuts the state off), and its
-// state from zero.
+// state from zero.  Its steps take a quick form, in which a state behind an infinity, or behind a difference that
+// overflows, is not finite until a reset.  Chunks that end so are folded again in the safe form: two waves a
+// SIMD are bound by their instructions, and with the safe form for all 4 x 4000 x 512 bf16 takes 24.9 us, not 23.4.
+template <typename F>
+__device__ __forceinline__ void quick_or_safe(F fold)
+{
+    if (!__all(fold(std::false_type()))) fold(std::true_type());
+}
+
+template <int N>
+__device__ __forceinline__ bool all_finite(const float (&v)[N])
+{
+    bool all = true;
+#pragma unroll
+    for (int j = 0; j < N; ++j) all &= fabsf(v[j]) < INFINITY;
+    return all;
+}
+
+// a*x, in the quick form; w is the smaller share, negative where that is a.
+__device__ __forceinline__ float through(float w, float x, bool open) { return fmaf(-w, x, open ? x : 0.f); }
+
+// Stores a fold.  A product too small for fp32 stays above 0, so that an infinite state is infinite behind it.
+template <int N>
+__device__ __forceinline__ void put_fold(const float (&p)[N], const float (&h)[N], bool cut, float *keep, float *add, int skip)
+{
+    float k[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) k[j] = cut ? -1.f : fmaxf(p[j], kLeast);
+    put_own<float, N>(keep, k, skip);
+    put_own<float, N>(add, h, skip);
+}
+
 template <typename T, int N, bool COUPLED, bool SOME, typename Off>
 __global__ void __launch_bounds__(64) scan_fold_fwd(ScanGeom g, ScanPlan q, const T *__restrict__ gate,
                                                     const T *__restrict__ value, const uint8_t *__restrict__ reset,
@@ -275,30 +325,33 @@ __global__ void __launch_bounds__(64) scan_fold_fwd(ScanGeom g, ScanPlan q, cons
 {
     Lane<N> w;
     if (!w.find(g, q, lengths)) return;
-    float h[N] = {}, p[N];
+    const Line<const T, N, Off> fl(gate, g.gate, w), vl(value, g.value, w);
+    const Resets<SOME> rl(reset, g, w.b);
+    float h[N], p[N];
     bool cut = false;
+    quick_or_safe([&](auto safe) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) p[j] = 1.f;
-    walk<T, N, SOME, Off>(Line<const T, N, Off>(gate, g.gate, w), Line<const T, N, Off>(value, g.value, w),
-                          Resets<SOME>(reset, g, w.b), w.t0, min(w.t1, w.valid),
-                          [&](int, int n, auto full, const auto &f, const auto &v, uint32_t resets) {
-                              constexpr bool FULL = decltype(full)::value;
-                              cut |= resets != 0;
-                              each_step<kHalf, SOME>(resets, [&](int u, bool zero) {
-                                  if (!FULL && u >= n) return;
+        for (int j = 0; j < N; ++j) h[j] = 0.f, p[j] = 1.f;
+        walk<T, N, SOME, Off>(
+            fl, vl, rl, w.t0, min(w.t1, w.valid), [&](int, int n, auto full, const auto &f, const auto &v, uint32_t resets) {
+                constexpr bool FULL = decltype(full)::value, SAFE = decltype(safe)::value;
+                cut |= resets != 0;
+                each_step<kHalf, SOME>(resets, [&](int u, bool zero) {
+                    if (!FULL && u >= n) return;
 #pragma unroll
-                                  for (int j = 0; j < N; ++j) {
-                                      float a, i;
-                                      gates(f[u].get(j), a, i);
-                                      h[j] = advance<COUPLED>(zero ? 0.f : h[j], i, v[u].get(j));
-                                      p[j] = fmaf(-i, p[j], p[j]);
-                                  }
-                              });
-                          });
-#pragma unroll
-    for (int j = 0; j < N; ++j) p[j] = cut ? -1.f : p[j];
-    put_own<float, N>(keep + w.end(g, w.c), p, w.skip);
-    put_own<float, N>(add + w.end(g, w.c), h, w.skip);
+                    for (int j = 0; j < N; ++j) {
+                        const Gate<> k(f[u].get(j));
+                        const float small = k.open ? k.small : -k.small, before = zero ? 0.f : h[j], x = v[u].get(j);
+                        if (SAFE) h[j] = advance<COUPLED>(before, k, x);
+                        else if (COUPLED) h[j] = fmaf(small, x - before, k.open ? before : x);
+                        else h[j] = through(small, before, k.open) + x;
+                        p[j] = through(small, p[j], k.open);
+                    }
+                });
+            });
+        return all_finite(h);
+    });
+    put_fold<N>(p, h, cut, keep + w.end(g, w.c), add + w.end(g, w.c), w.skip);
 }
 
 // The state before each chunk (BACK: the gradient behind it), written over `keep`: 16 waves fold a
@@ -339,7 +392,7 @@ __global__ void __launch_bounds__(1024) scan_carry(int64_t ends, int chunks, con
                 p *= k[u];
             }
         }
-    part[0][wave][lane] = cut ? -1.f : p;
+    part[0][wave][lane] = cut ? -1.f : fmaxf(p, kLeast);
     part[1][wave][lane] = h;
     __syncthreads();
     if (!live) return;
@@ -357,9 +410,9 @@ __global__ void __launch_bounds__(1024) scan_carry(int64_t ends, int chunks, con
 }
 
 // ---------------------------------------------------------------- backward --
-// A block's states are worked out forward from the kept one, leaving two numbers a step: i, and what
-// dgate is of g.  The gates' and values' registers are then free for the next block's loads, which fly
-// while the block's gradient is walked back; dout's follow behind it.
+// A block's states are worked out forward from the kept one, leaving two numbers a step: twice the smaller
+// share, negative where that is a, and what dgate is of g.  The gates' and values' registers are then
+// free for the next block's loads, which fly while the block's gradient is walked back; dout's follow behind it.
 template <typename T, int N, bool COUPLED, bool SOME, bool PAST, typename Off>
 __global__ void __launch_bounds__(64) scan_bwd(ScanGeom g, ScanPlan q, const T *__restrict__ gate,
                                                const T *__restrict__ value, const float *__restrict__ states,
@@ -396,12 +449,15 @@ __global__ void __launch_bounds__(64) scan_bwd(ScanGeom g, ScanPlan q, const T *
             for (int j = 0; j < N; ++j) {
                 if (!FULL) share[u][j] = slope[u][j] = 0.f;
                 if (!FULL && u >= live) continue;
-                float a, i;
-                gates(f[u].get(j), a, i);
+                // Half the difference does not overflow.  Behind an infinite state h is NaN within a block: dgate is not
+                // finite there either way.
+                const Gate<2> k(f[u].get(j));
                 const float before = cut ? 0.f : h[j], x = v[u].get(j);
-                share[u][j] = i;
-                slope[u][j] = a * i * (COUPLED ? before - x : before);
-                h[j] = advance<COUPLED>(before, i, x);
+                const float half = COUPLED ? fmaf(0.5f, before, -0.5f * x) : 0.5f * before;
+                share[u][j] = k.open ? k.small : -k.small;
+                slope[u][j] = k.small * k.large * half;
+                h[j] = fmaf(-share[u][j], half, k.open ? before : COUPLED ? x : 0.f);
+                if (!COUPLED) h[j] += x;
             }
         });
     };
@@ -417,10 +473,12 @@ __global__ void __launch_bounds__(64) scan_bwd(ScanGeom g, ScanPlan q, const T *
             if (FULL || u < live) {
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    const float gr = back[j] + d[u].get(j);
+                    const float gr = back[j] + d[u].get(j), s = 0.5f * fabsf(share[u][j]);
+                    const bool open = !signbit(share[u][j]);
+                    const float less = s * gr, more = rest(s, gr);
                     yf[j] = slope[u][j] * gr;
-                    yv[j] = COUPLED ? share[u][j] * gr : gr;
-                    back[j] = cut ? 0.f : fmaf(-share[u][j], gr, gr);
+                    yv[j] = !COUPLED ? gr : open ? less : more;
+                    back[j] = cut ? 0.f : open ? more : less;
                 }
             }
             put_own<T, N, PAST>(dfl.lane(to_gate), yf, w.skip);
@@ -460,64 +518,64 @@ __global__ void __launch_bounds__(64) scan_fold_bwd(ScanGeom g, ScanPlan q, cons
 {
     Lane<N> w;
     if (!w.find(g, q, lengths)) return;
-    float back[N] = {}, p[N];
-    bool cut = false;
-#pragma unroll
-    for (int j = 0; j < N; ++j) p[j] = 1.f;
     const Line<const T, N, Off> fl(gate, g.gate, w), dl(dout, g.out, w);
     const Resets<SOME> rl(reset, g, w.b);
-    Vec<T, N> fa[kHalf], da[kHalf], fb[kHalf], db[kHalf];
-    const int t1 = min(w.t1, w.valid);
-    auto body = [&](int n, auto full, const Vec<T, N>(&f)[kHalf], const Vec<T, N>(&d)[kHalf], uint32_t resets) {
-        constexpr bool FULL = decltype(full)::value;
-        cut |= resets != 0;
-        each_step<kHalf, SOME>(SOME ? __brev(resets) >> (32 - kHalf) : 0, [&](int k, bool zero) {
-            const int u = kHalf - 1 - k;
-            if (!FULL && u >= n) return;
+    float back[N], p[N];
+    bool cut = false;
+    quick_or_safe([&](auto safe) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                float a, i;
-                gates(f[u].get(j), a, i);
-                const float gr = back[j] + d[u].get(j);
-                back[j] = zero ? 0.f : fmaf(-i, gr, gr);
-                p[j] = fmaf(-i, p[j], p[j]);
-            }
-        });
-    };
-    // halves from the last one back; t is the first step of the half behind the next
-    int t = w.t0 + (w.t1 - w.t0 + kHalf - 1) / kHalf * kHalf;
-    while (t > w.t0 && !__all(t <= t1 && t - w.t0 >= kBlock)) {
-        t -= kHalf;
-        const int n = min(kHalf, t1 - t);
-        fl.template load<kHalf, false>(fa, t, n);
-        dl.template load<kHalf, false>(da, t, n);
-        body(n, std::false_type(), fa, da, rl.template load<kHalf, false>(t, n));
-    }
-    if (t > w.t0) {
-        // whole halves only; an odd one first, so that pairs are left
-        auto fetch = [&](Vec<T, N>(&f)[kHalf], Vec<T, N>(&d)[kHalf], int at) {
-            fl.template load<kHalf, true>(f, at, 0);
-            dl.template load<kHalf, true>(d, at, 0);
-            return rl.template load<kHalf, true>(at, 0);
+        for (int j = 0; j < N; ++j) back[j] = 0.f, p[j] = 1.f;
+        Vec<T, N> fa[kHalf], da[kHalf], fb[kHalf], db[kHalf];
+        const int t1 = min(w.t1, w.valid);
+        auto body = [&](int n, auto full, const Vec<T, N>(&f)[kHalf], const Vec<T, N>(&d)[kHalf], uint32_t resets) {
+            constexpr bool FULL = decltype(full)::value, SAFE = decltype(safe)::value;
+            cut |= resets != 0;
+            each_step<kHalf, SOME>(SOME ? __brev(resets) >> (32 - kHalf) : 0, [&](int k, bool zero) {
+                const int u = kHalf - 1 - k;
+                if (!FULL && u >= n) return;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const Gate<> gate(f[u].get(j));
+                    const float small = gate.open ? gate.small : -gate.small, gr = back[j] + d[u].get(j);
+                    if (SAFE) back[j] = zero ? 0.f : gate.open ? rest(gate.small, gr) : gate.small * gr;
+                    else back[j] = zero ? 0.f : through(small, gr, gate.open);
+                    p[j] = through(small, p[j], gate.open);
+                }
+            });
         };
-        if ((t - w.t0) / kHalf % 2) {
+        // halves from the last one back; t is the first step of the half behind the next
+        int t = w.t0 + (w.t1 - w.t0 + kHalf - 1) / kHalf * kHalf;
+        while (t > w.t0 && !__all(t <= t1 && t - w.t0 >= kBlock)) {
             t -= kHalf;
-            const uint32_t r = fetch(fa, da, t);
-            body(kHalf, std::true_type(), fa, da, r);
+            const int n = min(kHalf, t1 - t);
+            fl.template load<kHalf, false>(fa, t, n);
+            dl.template load<kHalf, false>(da, t, n);
+            body(n, std::false_type(), fa, da, rl.template load<kHalf, false>(t, n));
         }
-        uint32_t ra = fetch(fa, da, t - kHalf);
-        while (t > w.t0) {
-            const uint32_t rb = fetch(fb, db, t - kBlock);
-            body(kHalf, std::true_type(), fa, da, ra);
-            t -= kBlock;
-            if (t > w.t0) ra = fetch(fa, da, t - kHalf);
-            body(kHalf, std::true_type(), fb, db, rb);
+        if (t > w.t0) {
+            // whole halves only; an odd one first, so that pairs are left
+            auto fetch = [&](Vec<T, N>(&f)[kHalf], Vec<T, N>(&d)[kHalf], int at) {
+                fl.template load<kHalf, true>(f, at, 0);
+                dl.template load<kHalf, true>(d, at, 0);
+                return rl.template load<kHalf, true>(at, 0);
+            };
+            if ((t - w.t0) / kHalf % 2) {
+                t -= kHalf;
+                const uint32_t r = fetch(fa, da, t);
+                body(kHalf, std::true_type(), fa, da, r);
+            }
+            uint32_t ra = fetch(fa, da, t - kHalf);
+            while (t > w.t0) {
+                const uint32_t rb = fetch(fb, db, t - kBlock);
+                body(kHalf, std::true_type(), fa, da, ra);
+                t -= kBlock;
+                if (t > w.t0) ra = fetch(fa, da, t - kHalf);
+                body(kHalf, std::true_type(), fb, db, rb);
+            }
         }
-    }
-#pragma unroll
-    for (int j = 0; j < N; ++j) p[j] = cut ? -1.f : p[j];
-    put_own<float, N>(keep + w.end(g, w.c), p, w.skip);
-    put_own<float, N>(add + w.end(g, w.c), back, w.skip);
+        return all_finite(back);
+    });
+    put_fold<N>(p, back, cut, keep + w.end(g, w.c), add + w.end(g, w.c), w.skip);
 }
 
 template <bool BACK>

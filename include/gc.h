@@ -343,6 +343,9 @@ int gc_layer_norm_bwd(const void *x, const void *gamma, const void *dy, const vo
  *   a = sigmoid(gate),  i = coupled ? 1 - a : 1
  *   h[b,t,:] = a[b,t,:] * (reset[b,t] ? 0 : h[b,t-1,:]) + i[b,t,:] * value[b,t,:],   out = h
  *
+ * a and i are each right in their own size, to (1.5|gate| + 8) * 2^-24 (0 where below 1e-38): a gate that is
+ * open keeps a state over any number of steps, one that closes leaves the value beside a state of any size.
+ *
  * h before the first step is h0 [B][D] (fp32; NULL for zeros), after the last
  * one it is written to last [B][D] (fp32, may be NULL, may be h0).  reset, one
  * byte a step (not 0: the step starts anew, as after an episode's end or at the
