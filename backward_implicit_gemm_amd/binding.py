@@ -840,23 +840,41 @@ class _Descs:
 class _Checked:
     """A call's checks of its tensors (None where one is left out): done in full, by `full`, which gives
     the descriptor, where the tensors differ from the last call's in type, shape, distances,
-    device or presence; else one C++ call compares all of these (checked one by one from Python,
-    the 8 tensors of a layer norm's forward cost 5 us more)."""
+    device, presence or which of them are one; else one C++ call compares the first four (checked one by one
+    from Python, the 8 tensors of a layer norm's forward cost 5 us more)."""
 
     def __init__(self, full):
         self.full, self.last = full, None
 
     def __call__(self, helper, *tensors):
         """The descriptor, and the tensors' addresses."""
-        there = [t for t in tensors if t is not None]
-        last = self.last
-        if last is not None and last[0] == [t is None for t in tensors] and last[1](*there):
-            desc = last[2]
-        else:
+        absent = [t is None for t in tensors]
+        if not self._as_last(absent, tensors):
             desc, keep = self.full(helper, *tensors)
-            guards = TensorGuards(*there, dynamic_dims_sizes=None, dynamic_dims_strides=None) if keep else None
-            self.last = ([t is None for t in tensors], guards.check, desc) if keep else None
+            self.last = (absent, desc, *self._guarded(tensors)) if keep else None
+        else:
+            desc = self.last[1]
         return desc, [None if t is None else t.data_ptr() for t in tensors]
+
+    def _as_last(self, absent, tensors):
+        if self.last is None or self.last[0] != absent:
+            return False
+        _, _, first, again, check = self.last
+        for i, k in again:
+            if tensors[i] is not tensors[k]:
+                return False
+        return check(*[tensors[i] for i in first])
+
+    @staticmethod
+    def _guarded(tensors):
+        """The places of the call's tensors, each tensor's first; (place, first place) of what comes again, for a
+        call in place; and the check of the former, which refuses one tensor twice."""
+        where, again = {}, []
+        for i, t in enumerate(tensors):
+            if t is not None and where.setdefault(id(t), i) != i:
+                again.append((i, where[id(t)]))
+        first = list(where.values())
+        return first, again, TensorGuards(*(tensors[i] for i in first), dynamic_dims_sizes=None, dynamic_dims_strides=None).check
 
 
 def _dense_rows(t, name, dtype, shape, device):
