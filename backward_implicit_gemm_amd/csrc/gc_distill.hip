@@ -304,7 +304,9 @@ __global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, int lists,
         const float log_s = logf(s), log_total = logf(total);
         float sum = 0.f;
         auto add = [&](float p, float v, float x) {
-            if (some && p != 0.f) sum += x == -INFINITY ? INFINITY : p * (((v - top) - (x - m)) / t - log_total + log_s);
+            // a masked logit's share is 0, but in a row whose sum is NaN
+            if (some && p != 0.f)
+                sum += x == -INFINITY && s == s ? INFINITY : p * (((v - top) - (x - m)) / t - log_total + log_s);
         };
         if (OP == GC_OP_FWD)
             each_entry([&](int, int, float v, float x) { add(v == -INFINITY ? 0.f : share(v, top, c) * inv_total, v, x); });
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, int lists,
         if (tt == 0) loss[row] = t * t * sum;
     }
     if (OP == GC_OP_FWD) return;
-    if (m == -INFINITY) {     // of a row of nothing but masked logits every share is 0
+    if (m == -INFINITY && s == s) {     // of a row of nothing but masked logits every share is 0
         m = 0.f;
         s = INFINITY;
     }
@@ -323,7 +325,8 @@ __global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, int lists,
     if (OP == GC_OP_BWD || L <= 64) team_sync(L <= 64);
     some = any[team];
     const float by = some ? scale * t : 0.f, inv = by / s;
-    const float own = mine == -INFINITY ? 0.f : share(base, m, c) * inv;     // of this thread's exponentials
+    // of this thread's exponentials; 0 where all are masked, but in a row whose sum is NaN
+    const float own = mine == -INFINITY ? 0.f * inv : share(base, m, c) * inv;
     T *out = dlogits + row * g.ld_grad;
     auto write = [&](int64_t i) {
         if (!KEEP) keep_packed(held);
