@@ -37,6 +37,8 @@ constexpr int kBlock = GC_RECURRENCE_BLOCK;
 constexpr int kHalf = kBlock / 2;
 constexpr float kLog2e = 1.44269504088896f;
 constexpr float kLeast = 1.4e-45f;     // the smallest number above 0
+constexpr int kCarryWaves = 16;
+constexpr int kMostChunks = kCarryWaves * 16;
 
 // Where a thread works: sequence b, channels d .. d+N-1, of which the first `skip` belong to
 // the thread before it (the last vector of an odd row is moved back), steps [t0, t1) of chunk c.
@@ -350,58 +352,51 @@ __global__ void __launch_bounds__(64) scan_fold_fwd(ScanGeom g, ScanPlan q, cons
 }
 
 // The state before each chunk (BACK: the gradient behind it), written over `keep`: 16 waves fold a
-// sixteenth of the chunks each, then walk them again from what the waves before them give.  Up to 16
-// chunks a wave are read once, together: 256 chunks take 4.9 us (9.2 when read one by one).
+// sixteenth of the chunks each, then walk them again from what the waves before them give.  A wave's chunks, 16
+// at most, are read together: 256 chunks take 4.9 us (9.2 when read one by one).
 __device__ __forceinline__ float carry_over(float keep, float add, float h) { return keep < 0.f ? add : fmaf(keep, h, add); }
 
 template <bool BACK>
-__global__ void __launch_bounds__(1024) scan_carry(int64_t ends, int chunks, const float *__restrict__ first,
+__global__ void __launch_bounds__(64 * kCarryWaves) scan_carry(int64_t ends, int chunks, const float *__restrict__ first,
                                                    float *keep, const float *__restrict__ add)
 {
-    __shared__ float part[2][16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ float part[2][kCarryWaves][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t e = int64_t(blockIdx.x) * 64 + lane;
-    const int per = (chunks + 15) / 16, c0 = min(wave * per, chunks), c1 = min(c0 + per, chunks);
+    const int per = (chunks + kCarryWaves - 1) / kCarryWaves, c0 = min(wave * per, chunks), c1 = min(c0 + per, chunks);
     const bool live = e < ends;
     auto place = [&](int c) { return int64_t(BACK ? chunks - 1 - c : c) * ends + e; };
     float p = 1.f, h = 0.f;
     bool cut = false;
-    constexpr int U = 16;     // chunks whose loads fly together
+    constexpr int U = kMostChunks / kCarryWaves;
     float k[U], a[U];
-    auto fetch = [&](int c) {
+    if (live) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (c + u < c1) {
-                k[u] = keep[place(c + u)];
-                a[u] = add[place(c + u)];
+            if (c0 + u < c1) {
+                k[u] = keep[place(c0 + u)];
+                a[u] = add[place(c0 + u)];
             }
-    };
-    if (live)
-        for (int c = c0; c < c1; c += U) {
-            fetch(c);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (c + u >= c1) break;
+        for (int u = 0; u < U; ++u)
+            if (c0 + u < c1) {
                 h = carry_over(k[u], a[u], h);
                 cut |= k[u] < 0.f;
                 p *= k[u];
             }
-        }
+    }
     part[0][wave][lane] = cut ? -1.f : fmaxf(p, kLeast);
     part[1][wave][lane] = h;
     __syncthreads();
     if (!live) return;
     h = first ? first[e] : 0.f;
     for (int w = 0; w < wave; ++w) h = carry_over(part[0][w][lane], part[1][w][lane], h);
-    for (int c = c0; c < c1; c += U) {
-        if (per > U) fetch(c);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (c + u >= c1) break;
-            keep[place(c + u)] = h;
+    for (int u = 0; u < U; ++u)
+        if (c0 + u < c1) {
+            keep[place(c0 + u)] = h;
             h = carry_over(k[u], a[u], h);
         }
-    }
 }
 
 // ---------------------------------------------------------------- backward --
@@ -579,8 +574,8 @@ template <bool BACK>
 hipError_t carry(const ScanGeom &g, const ScanPlan &q, const float *first, float *keep, const float *add, hipStream_t s)
 {
     const int64_t ends = int64_t(g.B) * g.D;
-    hipLaunchKernelGGL((scan_carry<BACK>), dim3(unsigned((ends + 63) / 64)), dim3(1024), 0, s, ends, q.chunks, first, keep,
-                       add);
+    hipLaunchKernelGGL((scan_carry<BACK>), dim3(unsigned((ends + 63) / 64)), dim3(64 * kCarryWaves), 0, s, ends, q.chunks,
+                       first, keep, add);
     return hipGetLastError();
 }
 
@@ -619,7 +614,7 @@ bool plan_scan(const ScanGeom &g, int dtype, bool bwd, bool ragged, ScanPlan &q)
     q.far = !near(g.gate, g, least, size) || !near(g.value, g, least, size) || !near(g.out, g, least, size);
     if (bwd) q.far |= !near(g.dgate, g, least, size) || !near(g.dvalue, g, least, size);
     // Chunks, while a walk leaves most of the chip idle and is long enough to pay for two more launches,
-    // so that 2048 waves have two blocks or more each; more than 256 chunks would make the carry longer
+    // so that 2048 waves have two blocks or more each; more than kMostChunks would make the carry longer
     // than it saves.  Walked and in chunks (us): 64 x 128 x 512 bf16 forward 11 and 23; 1 x 200 x 64 15
     // and 14, backward 24 and 14; 1 x 800 x 64 50 and 10; 64 x 512 x 512 (512 waves) fp32 40 and 57.
     // Two channels a thread halve the loads but also the waves: backward of 3 x 12,001 x 776 bf16 84
@@ -628,7 +623,7 @@ bool plan_scan(const ScanGeom &g, int dtype, bool bwd, bool ragged, ScanPlan &q)
     auto waves_of = [&](int n) { return (int64_t(g.B) * vectors(g.D, n) + 63) / 64; };
     auto chunks_of = [&](int64_t waves) -> int64_t {
         if (!waves || waves >= 512 || blocks < (bwd ? 10 : 15)) return 1;
-        return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(2048 / waves, 256), blocks / 2));
+        return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(2048 / waves, kMostChunks), blocks / 2));
     };
     q.N = 1;
     if (bwd && dtype == GC_BF16 && g.D >= 2 && !q.far) {
