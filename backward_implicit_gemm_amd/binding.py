@@ -803,7 +803,7 @@ def gc_layer_norm_plan_name(op, desc, dtype):
 
 
 def gc_recurrence_plan_name(op, desc, dtype):
-    """The kernels a recurrence would run (host only, enqueues nothing)."""
+    """The kernels a recurrence without lengths would run (host only, enqueues nothing)."""
     return _plan_name("gc_recurrence_plan_name", op, desc, dtype)
 
 

@@ -425,7 +425,8 @@ int gc_distill_step(const void *logits, const void *index, const void *teacher, 
                     void *dlogits, const gc_distill_desc *d, int dtype, void *stream);
 
 /* Which kernels these would run (pure host, as gc_conv_plan_name): op is GC_OP_FWD or GC_OP_BWD
- * (the layer norm's without a residual, or a gradient past it), for the distillation also GC_OP_STEP, both at once. */
+ * (the layer norm's without a residual, or a gradient past it; the recurrence's without lengths, with which each of
+ * the sequences begins with a wave), for the distillation also GC_OP_STEP, both at once. */
 enum { GC_OP_STEP = 6 };
 int gc_layer_norm_plan_name(int op, const gc_layer_norm_desc *d, int dtype, char *buf, size_t buf_bytes);
 int gc_recurrence_plan_name(int op, const gc_recurrence_desc *d, int dtype, char *buf, size_t buf_bytes);
