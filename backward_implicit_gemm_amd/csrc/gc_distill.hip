@@ -96,31 +96,6 @@ __device__ __forceinline__ void gather_places(const Entries &entry, int K, int l
     }
 }
 
-template <int N>
-struct Place {
-    int at, skip;
-    bool live;
-    __device__ __forceinline__ Place(int64_t i, int V)
-    {
-        const int64_t first = i * N;
-        live = first < V;
-        at = live ? min(int(first), V - N) : 0;
-        skip = live ? int(first) - at : N;
-    }
-};
-
-template <bool PAST, typename T, int N>
-__device__ __forceinline__ void put_own(T *p, const Vec<T, N> &v, int skip)
-{
-    if (N == 1 || skip == 0) {
-        put_vec<PAST, T, N>(p, v);
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (j >= skip) p[j] = from_f32<T>(v.get(j));
-    }
-}
-
 // Makes the compiler work out anew what depends on this number: the places of a row's vectors would
 // take more registers than the vectors do.
 __device__ __forceinline__ int64_t anew(int64_t i)
@@ -170,7 +145,7 @@ __global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, int lists,
     float shares[KEEP ? U : 1][N];
     auto fetch = [&](int64_t i) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) held[u] = load_vec<T, N>(z + Place<N>(i + int64_t(u) * L, g.V).at);
+        for (int u = 0; u < U; ++u) held[u] = load_vec<T, N>(z + Place<N, int64_t>(i + int64_t(u) * L, g.V).at);
     };
     // the teacher's shares, by the team's first wave; a lane's first entries stay in registers
     const int width = L < 64 ? L : 64, lane = tt & (width - 1);
@@ -247,7 +222,7 @@ __global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, int lists,
             float high = mine;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const Place<N> at(i + int64_t(u) * L, g.V);
+                const Place<N, int64_t> at(i + int64_t(u) * L, g.V);
 #pragma unroll
                 for (int j = 0; j < N; ++j) high = fmaxf(high, j >= at.skip ? held[u].get(j) : -INFINITY);
             }
@@ -257,7 +232,7 @@ __global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, int lists,
             if (!NV) s *= share(mine, base, c);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const Place<N> at(i + int64_t(u) * L, g.V);
+                const Place<N, int64_t> at(i + int64_t(u) * L, g.V);
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
                     const float e = j >= at.skip ? share(held[u].get(j), base, c) : 0.f;
@@ -333,7 +308,7 @@ __global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, int lists,
         i = anew(i);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const Place<N> at(i + int64_t(u) * L, g.V);
+            const Place<N, int64_t> at(i + int64_t(u) * L, g.V);
             if (!at.live) continue;
             float y[N];
 #pragma unroll

@@ -90,6 +90,35 @@ __device__ __forceinline__ void put_vec(T *p, const Vec<T, N> &v)
 // elements of a 16-byte vector
 template <typename T> constexpr int kVec = 16 / int(sizeof(T));
 
+// Place of vector number i of a row of D >= N values.  The last vector of a row whose length is
+// no multiple of N is moved back to end with the row; its first `skip` elements belong
+// to the vector before it and are neither counted nor stored.  I holds i*N of every thread.
+template <int N, typename I = int>
+struct Place {
+    int at, skip;
+    bool live;
+    __device__ __forceinline__ Place(I i, int D)
+    {
+        const I first = i * N;
+        live = first < D;
+        at = live ? min(int(first), D - N) : 0;
+        skip = live ? int(first) - at : N;
+    }
+};
+
+// Stores the elements that are this vector's own.
+template <bool PAST, typename T, int N>
+__device__ __forceinline__ void put_own(T *p, const Vec<T, N> &v, int skip)
+{
+    if (N == 1 || skip == 0) {
+        put_vec<PAST, T, N>(p, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j >= skip) p[j] = from_f32<T>(v.get(j));
+    }
+}
+
 // Sum over the aligned group of `width` lanes (a power of two, at most 64)
 // the lane lies in; every lane gets the same value.
 template <typename V>

@@ -25,35 +25,6 @@
 namespace gc {
 namespace {
 
-// Place of vector number i of a row of D >= N values.  The last vector of a row whose length is
-// no multiple of N is moved back to end with the row; its first `skip` elements belong
-// to the vector before it and are neither counted nor stored.
-template <int N>
-struct Place {
-    int at, skip;
-    bool live;
-    __device__ __forceinline__ Place(int i, int D)
-    {
-        const int first = i * N;
-        live = first < D;
-        at = live ? min(first, D - N) : 0;
-        skip = live ? first - at : N;
-    }
-};
-
-// Stores the elements that are this vector's own.
-template <bool PAST, typename T, int N>
-__device__ __forceinline__ void put_own(T *p, const Vec<T, N> &v, int skip)
-{
-    if (N == 1 || skip == 0) {
-        put_vec<PAST, T, N>(p, v);
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (j >= skip) p[j] = from_f32<T>(v.get(j));
-    }
-}
-
 // N neighbouring values of gamma or beta in fp32.
 template <typename T, int N>
 __device__ __forceinline__ void params_at(const RowsGeom &g, const void *p, int at, float none, float (&v)[N])
