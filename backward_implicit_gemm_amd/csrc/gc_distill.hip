@@ -11,8 +11,9 @@
 // gradient is written as if there were no entries, then the entries' places are written again
 // with all that belongs to them.  Many entries are rather looked up, vector by vector, while the
 // gradient is written, as each place written again costs a memory line: steps of 4096 rows of 40,960
-// bf16 with 256 entries take 202 us the one way and 181 the other, with 64 entries 166 and 157; with
-// 8 entries 147, where a look into the lists for every vector would cost what it does with 64.
+// bf16 with 256 entries take 375 us the one way and 192 the other, with 64 entries 166 and 159; with
+// 8 entries 145, where a look into the lists for every vector takes 156.  Times, here and below, are of
+// passes whose inputs come from HBM.
 #include <algorithm>
 #include <iterator>
 #include <math.h>
@@ -46,8 +47,8 @@ __host__ __device__ __forceinline__ int entry_bytes(int K, int lists)
 constexpr int kOwn = 2;   // entries of a lane that stay in registers
 
 // The backward, which meets a row's logits once, walks longer bf16 rows: its few registers leave room for
-// more waves (512 x 150,000 69 us, with the row held 74; 4096 x 40,960 with 256 entries 156 and 158;
-// from the cache 2048 x 40,961 60 and 67).  In fp32 it loses (4096 x 32,000 202 and 193).
+// more waves (512 x 150,000 69 us, with the row held 73; 4096 x 40,960 with 256 entries 154 and 160;
+// 2048 x 40,961 79 and 82).  In fp32 it loses (4096 x 32,000 205 and 192).
 template <typename T>
 constexpr int kMostBwd = sizeof(T) == 2 ? 8 : 20;   // vectors that a thread of the backward holds
 
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(1024) distill(DistillGeom g, int L, int lists,
     int own_at[kOwn];
     float own_v[kOwn], own_z[kOwn], top = -INFINITY, total = 0.f, inv_total = 0.f;
     // The loss reads the entries' logits, the backward where it writes their places again (2048 x 40,961 bf16 with
-    // 64 entries 65 us without the reads, 69 with; 4096 x 40,960 with 256 161 and 157).
+    // 64 entries 79 us without the reads, 81 with; 4096 x 40,960 with 256 154 and 153).
     const bool reads = OP != GC_OP_BWD || g.K <= kScan;
     auto logit = [&](int at) { return reads && at >= 0 ? to_f32(z[at]) : 0.f; };
     // f(k, place, teacher's logit, student's logit) for the lane's entries
@@ -375,8 +376,10 @@ void plan_distill(const DistillGeom &g, int dtype, int op, DistillPlan &q)
     q.N = g.V < vec ? 1 : vec;
     const int64_t nv = vectors(g.V, q.N);
     // The fewest threads whose registers hold the row, so that several rows are at work on a CU and hide each
-    // other's waits (steps of 4096 x 40,960 bf16: 256 threads a row 157 us, 512 161, 1024 199), then
-    // more while the chip has room for them (512 x 8000: 256 threads 14 us, 64 18).
+    // other's waits (bf16 steps of 4096 x 32,000: 256 threads a row 115 us, 512 125; of 2048 x 50,257: 512 threads
+    // 115, 1024 134; rows that take all 20 vectors of a thread would rather have twice the threads, 4096 x
+    // 40,960 256 threads 158, 512 144, 1024 194), then more while the chip has room for them (512 x 8000
+    // bf16: 512 threads 12 us, 64 23).
     const int most = g.V <= 64 * 64 ? 64 / vec : 20;
     q.L = 8;
     while (q.L < 1024 && int64_t(q.L) * most < nv) q.L *= 2;
@@ -400,7 +403,7 @@ void plan_distill(const DistillGeom &g, int dtype, int op, DistillPlan &q)
     q.grid = (g.rows + teams - 1) / teams;
     q.lds_bytes = op == GC_OP_FWD ? 0 : size_t(teams) * entry_bytes(g.K, q.lists);
     // Large gradients go past the cache; the backward's do not where rows share 16 bytes of memory, which would be
-    // written in parts (4096 x 50,257 bf16 193 us past, 184 not, 4096 x 40,960 156 and 160; a step of 2048 x 40,961
+    // written in parts (4096 x 50,257 bf16 191 us past, 181 not, 4096 x 40,960 154 and 158; a step of 2048 x 40,961
     // fp32 157 past and 166 not).
     const int size = dtype == GC_F32 ? 4 : 2;
     q.past = op != GC_OP_FWD && q.N > 1 && size_t(g.rows) * g.V * 2 * size >= kStreamBytes &&

@@ -20,9 +20,10 @@
 //
 // Few sequences are cut into chunks: one launch folds each chunk into (product of a, state from
 // zero), one carries the states over the chunks, and the walk then starts every chunk from its
-// state; that reads two tensors twice.  512 sequences of 64 x 512 bf16 take 20.5 us forward
-// (105 MB, 5.1 TB/s) and fp32 53 backward (352 MB, 6.6 TB/s); one of 32,768 x 1024 bf16 takes 61
-// (fold 23 at 5.8 TB/s, carry 5, walk 34), and 2.1 ms if it is walked as a whole.
+// state; that reads two tensors twice.  512 sequences of 64 x 512 with resets take 25 us forward in bf16
+// (107 MB, 4.3 TB/s) and 72 backward in fp32 (342 MB, 4.7 TB/s); one of 32,768 x 1024 bf16 takes 74
+// (fold 29 at 4.6 TB/s, carry 5, walk 39), and 2.5 ms if it is walked as a whole.  Times, here and below, are
+// of passes whose inputs come from HBM, unless they name the cache.
 #include <algorithm>
 #include <float.h>
 #include <type_traits>
@@ -196,7 +197,7 @@ __device__ __forceinline__ float advance(float before, const Gate<> &k, float v)
 
 // ----------------------------------------------------------------- forward --
 // Runs step(u, bit u of resets) for COUNT steps.  A second form of the steps, for waves that meet no reset
-// meanwhile, costs the registers of both: backward of 512 x 64 x 512 bf16 with resets 45 us so, 35 with one.
+// meanwhile, costs the registers of both: backward of 512 x 64 x 512 bf16 with resets 54 us so, 41 with one.
 template <int COUNT, bool SOME, typename F>
 __device__ __forceinline__ void each_step(uint32_t resets, F step)
 {
@@ -283,8 +284,9 @@ __global__ void __launch_bounds__(64) scan_fwd(ScanGeom g, ScanPlan q, const T *
 
 // A chunk as a step of its own: the product of its a (-1 where a reset cuts the state off), and its
 // state from zero.  Its steps take a quick form, in which a state behind an infinity, or behind a difference that
-// overflows, is not finite until a reset.  Chunks that end so are folded again in the safe form: two waves a
-// SIMD are bound by their instructions, and with the safe form for all 4 x 4000 x 512 bf16 takes 24.9 us, not 23.4.
+// overflows, is not finite until a reset.  Chunks that end so are folded again in the safe form.  Inputs
+// that a projection has just left in the cache do not hide the safe form's instructions: forward of 4 x 4000 x 512
+// bf16 24.9 us with it for all chunks, 23.4 so (26 both from HBM).
 template <typename F>
 __device__ __forceinline__ void quick_or_safe(F fold)
 {
@@ -615,10 +617,10 @@ bool plan_scan(const ScanGeom &g, int dtype, bool bwd, bool ragged, ScanPlan &q)
     if (bwd) q.far |= !near(g.dgate, g, least, size) || !near(g.dvalue, g, least, size);
     // Chunks, while a walk leaves most of the chip idle and is long enough to pay for two more launches,
     // so that 2048 waves have two blocks or more each; more than kMostChunks would make the carry longer
-    // than it saves.  Walked and in chunks (us): 64 x 128 x 512 bf16 forward 11 and 23; 1 x 200 x 64 15
-    // and 14, backward 24 and 14; 1 x 800 x 64 50 and 10; 64 x 512 x 512 (512 waves) fp32 40 and 57.
-    // Two channels a thread halve the loads but also the waves: backward of 3 x 12,001 x 776 bf16 84
-    // against 99 with one, of 128 x 256 x 512 (512 waves of two) 56 against 37; the forward
+    // than it saves.  Walked and in chunks (us): 64 x 128 x 512 bf16 forward 15 and 18; 1 x 200 x 64 15
+    // and 12, backward 27 and 15; 1 x 800 x 64 54 and 10; 64 x 512 x 512 (512 waves) fp32 55 and 68.
+    // Two channels a thread halve the loads but also the waves: backward of 3 x 12,001 x 776 bf16 97
+    // against 116 with one, of 128 x 256 x 512 (512 waves of two) 67 against 52; the forward
     // is never faster with two.
     auto waves_of = [&](int n) { return (int64_t(g.B) * vectors(g.D, n) + 63) / 64; };
     auto chunks_of = [&](int64_t waves) -> int64_t {
@@ -632,8 +634,8 @@ bool plan_scan(const ScanGeom &g, int dtype, bool bwd, bool ragged, ScanPlan &q)
     }
     q.nv = vectors(g.D, q.N);
     // Sequences of their own lengths start with a wave: one that holds two goes step by step, without loads
-    // ahead, where either has ended (3 x 12,001 x 777 bf16 of different lengths: the walk 29 us so and 76
-    // packed, backward 64 and 73).
+    // ahead, where either has ended (3 x 12,001 x 777 bf16 of different lengths: 64 us so and 114
+    // packed, backward 100 and 112).
     const int wide = ragged && q.nv > 64 && int64_t(g.B) * (q.nv + 63) < int64_t(1) << 31 ? (q.nv + 63) / 64 * 64 : q.nv;
     q.lanes = int64_t(g.B) * wide;
     const int64_t waves = (q.lanes + 63) / 64;
@@ -645,8 +647,9 @@ bool plan_scan(const ScanGeom &g, int dtype, bool bwd, bool ragged, ScanPlan &q)
     q.part_bytes = bytes_of(q.chunks);
     // room for the most chunks that any distances lead to
     q.ws_bytes = 2 * bytes_of(std::max(chunks_of(waves_of(1)), bwd && dtype == GC_BF16 ? chunks_of(waves_of(2)) : int64_t(1)));
-    // Outputs of large calls go past the cache (512 x 64 x 512 fp32 backward 74 us without, 53 with), but not where
-    // rows share words of memory, which would be written in halves (3 x 12,001 x 777 bf16 69 without, 79 with).
+    // Outputs of large calls go past the cache (512 x 64 x 512 fp32 backward 78 us without, 74 with), but not where
+    // rows share words of memory, which would be written in halves (3 x 12,001 x 777 bf16 backward 104 without,
+    // 106 with; of different lengths 100 and 106, forward 64 and 70).
     auto words = [&](const gc_strides &s) { return s.step * size % 4 == 0 && (g.B == 1 || s.batch * size % 4 == 0); };
     q.past = size_t(g.B) * g.T * g.D * size * (bwd ? 5 : 3) >= kStreamBytes &&
              (bwd ? words(g.dgate) && words(g.dvalue) : words(g.out));

@@ -12,10 +12,9 @@
 // worked on.  A second launch adds up the workgroups' sums.  Rows past a workgroup's
 // registers (16,384 values forward, 8192 backward) are walked in several passes.
 //
-// 32,768 rows of 1760 bf16 with a residual: 74 us forward (461 MB, 6.2 TB/s).  8191 rows of 4096 bf16,
-// with the stream's gradient: 53 us backward and 5 for the sums (268 MB; 82 in all without the loads ahead
-// and with the sums of 512 teams joined one by one).  1024 rows of 1760 fp32: 10.4 and 3.4 us, the
-// latency of a row's loads, its sums, and the join.
+// With inputs from HBM, here and below: 32,768 rows of 1760 bf16 with a residual 88 us forward (462 MB,
+// 5.2 TB/s); 8191 rows of 4096 bf16, with the stream's gradient, 60 us backward (269 MB, 4.5 TB/s) and 5 for the
+// sums; 1024 rows of 1760 fp32 12.6 and 4.0 us, the latency of a row's loads, its sums, and the join.
 #include <algorithm>
 #include <type_traits>
 
@@ -466,7 +465,7 @@ void plan_rows(const RowsGeom &g, int dtype, bool bwd, bool more, RowsPlan &q)
     } else {
         // The smallest team that holds a row; while there are fewer teams than the chip takes, twice the threads.
         // The backward's workgroups are one a CU: with two, twice the rows of partial sums cost more than the
-        // overlap gains (8191 x 4096 bf16 69 us against 61).
+        // overlap gains (8191 x 4096 bf16 72 us against 63).
         q.L = 1;
         while (int64_t(q.L) * most < nv) q.L *= 2;
         while (q.L < threads && q.L < nv && rows * q.L < 1024 * kCUs / 4) q.L *= 2;
@@ -539,7 +538,7 @@ hipError_t launch_rows_bwd(const RowsGeom &g, const RowsPlan &q, const void *x, 
                     });
                 };
                 // Two rows ahead where registers allow it and teams of several waves wait for each other: 8191 x 4096
-                // bf16 57.4 us, with one 59.6; teams within a wave lose by it (65,536 x 256 29.9 and 28.1).
+                // bf16 62.9 us, with one 70.3; teams within a wave lose by it (65,536 x 256 34.0 and 33.1).
                 if constexpr (NV * N * sizeof(T) == 32 && N > 1)
                     if (q.L > 64) return go(std::integral_constant<int, 2>());
                 return go(std::integral_constant<int, 1>());
