@@ -849,17 +849,19 @@ class _Checked:
     def __call__(self, helper, *tensors):
         """The descriptor, and the tensors' addresses."""
         absent = [t is None for t in tensors]
-        if not self._as_last(absent, tensors):
+        last = self.last       # read once: another thread's call may replace it meanwhile
+        if last is not None and self._as_last(last, absent, tensors):
+            desc = last[1]
+        else:
             desc, keep = self.full(helper, *tensors)
             self.last = (absent, desc, *self._guarded(tensors)) if keep else None
-        else:
-            desc = self.last[1]
         return desc, [None if t is None else t.data_ptr() for t in tensors]
 
-    def _as_last(self, absent, tensors):
-        if self.last is None or self.last[0] != absent:
+    @staticmethod
+    def _as_last(last, absent, tensors):
+        was_absent, _, first, again, check = last
+        if absent != was_absent:
             return False
-        _, _, first, again, check = self.last
         for i, k in again:
             if tensors[i] is not tensors[k]:
                 return False

@@ -96,3 +96,21 @@ def test_a_failed_check_is_not_remembered():
         with pytest.raises(ValueError):
             check(None, bad, bad)
     assert check(None, good, good)[0] == "desc"
+
+
+@pytest.mark.parametrize("other", [lambda t: t, lambda t: t[:2]], ids=["kept", "refused"])
+def test_another_threads_call_in_between(other):
+    """A call whose comparison is under way when another one replaces what is remembered, or drops it."""
+    full = Counted()
+    check = gb._Checked(full)
+    a, b = tensors(2)
+    desc, _ = check(None, a, b)
+    remembered = check.last
+
+    def compare(*ts):
+        full.keep = other(a) is a
+        check(None, other(b), None)
+        return True
+
+    check.last = (*remembered[:-1], compare)
+    assert check(None, a, b) == (desc, [a.data_ptr(), b.data_ptr()])
